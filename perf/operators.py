@@ -123,7 +123,7 @@ def prepare(case, seed):
         s["r"] = rows_in(g, m, d, dtype).mul_(2)
         s["y"] = rows_in(g, m, d, dtype)
         s["w_post"], s["w_pre"] = (normal(g, (d,), dtype, 0.2, 1.0) for _ in range(2))
-        shape = {"none": None, "channel": (d,), "token": (m,), "full": (m, d)}[case["gate"]]
+        shape = {"none": None, "channel": (d,), "token": (m, 1), "full": (m, d)}[case["gate"]]
         s["gate"] = None if shape is None else normal(g, shape, dtype, 0.3, 0.5)
         s["r_out"], s["n"] = torch.empty_like(s["r"]), torch.empty_like(s["r"])
         if case["dir"] == "step":
@@ -189,8 +189,6 @@ def norm_plain(s):
     c = s["case"]
     r, y, w_post, w_pre = (s[k].float() for k in ("r", "y", "w_post", "w_pre"))
     gate = 1.0 if s["gate"] is None else s["gate"].float()
-    if c["gate"] == "token":
-        gate = gate[:, None]
     rs1 = torch.rsqrt((y * y).mean(1, keepdim=True) + EPS)
     p = y * rs1 * w_post
     t = c["res_scale"] * r + gate * p
@@ -206,7 +204,7 @@ def norm_plain(s):
     grads = {"r": c["res_scale"] * e, "y": rs1 * (b - y * rs1 * rs1 * (y * b).mean(1, keepdim=True)),
              "w_post": (dp * y * rs1).sum(0), "w_pre": (dn * t * rs2).sum(0)}
     if c["gate"] != "none":
-        grads["gate"] = {"channel": lambda v: v.sum(0), "token": lambda v: v.sum(1), "full": lambda v: v}[c["gate"]](e * p)
+        grads["gate"] = {"channel": lambda v: v.sum(0), "token": lambda v: v.sum(1, keepdim=True), "full": lambda v: v}[c["gate"]](e * p)
     return out | {"d_" + k: v.to(s[k].dtype) for k, v in grads.items()}
 
 
@@ -304,7 +302,7 @@ def exact(case, seed):
 
         branch = rms(v["y"]) * v["w_post"]
         if "gate" in v:
-            branch = branch * (v["gate"].unsqueeze(-1) if case["gate"] == "token" else v["gate"])
+            branch = branch * v["gate"]
         r_out = v["r"] * case["res_scale"] + branch
         n = rms(r_out) * v["w_pre"]
         out = {"r_out": r_out.detach(), "n": n.detach()}
