@@ -335,6 +335,151 @@ int moe_forward_static(const moe_cfg* cfg, const moe_weights* w, const void* are
                        const void* x_bf16, int32_t m, void* out_bf16, float* weights_out, int32_t* idx_out,
                        int32_t* status, void* stream);
 
+/* ------------------------------------------------------------------------
+ * Operators around the layer: the norms before and after a block, a dense gated
+ * feed-forward block with its backward pass, and products with 4-bit weights.
+ * They need no context. The caller owns every buffer, the workspaces included;
+ * a workspace holds nothing between calls, may be shared by calls that follow
+ * each other on one stream, and must not be shared by calls that may overlap.
+ * Nothing is allocated and nothing waits for the device, so every call can be
+ * captured in a HIP graph. Sums do not depend on scheduling: the same inputs
+ * give the same bits. A strided tensor is described by its row stride in
+ * values (`ld...`); the values of a row are consecutive.
+ * ------------------------------------------------------------------------ */
+
+/* value types */
+#define MOE_BF16 0
+#define MOE_F16 1
+#define MOE_F32 2
+
+/* activations of the gated product */
+#define MOE_ACT_SILU 0   /* v / (1 + exp(-v)) */
+#define MOE_ACT_GELU 1   /* v / 2 (1 + tanh(sqrt(2 / pi) (v + 0.044715 v^3))) */
+
+/* A dense gated feed-forward block:
+ *   g = x Wg^T, u = x Wu^T;  h = act(gc) uc with gc = min(g, limit) and
+ *   uc = min(max(u, -limit), limit) (no clamps when limit <= 0);  y = h Wd^T.
+ * Products are summed in f32; h is rounded to the value type, as it is the
+ * operand of the second product, and nothing else before y is. */
+typedef struct moe_ffn {
+    int32_t dim;        /* D: a multiple of 8, 8..16384 */
+    int32_t inter;      /* I: a multiple of 8, 8..16384 */
+    int32_t dtype;      /* MOE_BF16 or MOE_F16: x, y, the weights and every gradient */
+    int32_t act;        /* MOE_ACT_* */
+    float limit;        /* clamp; <= 0: none */
+    const void* w_gate; /* device, [I, D] row-major, 16-byte aligned, as the next two */
+    const void* w_up;   /* device, [I, D] */
+    const void* w_down; /* device, [D, I] */
+} moe_ffn;
+
+/* Bytes that calls with m rows need: `forward` and `backward`, the workspaces of
+ * the two calls, and `saved`, what a forward call leaves for its backward call
+ * (g and u in f32). Each a multiple of 256, possibly 0. MOE_EINVAL for a bad
+ * description, m < 0, m > 2^24 or NULL. */
+int moe_ffn_workspace(const moe_ffn* f, int32_t m, size_t* forward, size_t* saved, size_t* backward);
+
+/* y = block(x) for m rows. x [m, D] with row stride ldx, y [m, D] with row stride
+ * ldy (both >= D and multiples of 8; device, 16-byte aligned; y does not overlap
+ * x or the weights). saved: NULL, or the `saved` bytes that moe_ffn_backward
+ * takes (256-byte aligned, as work is). m = 0 does nothing. MOE_EINVAL for a bad
+ * description, size, stride, NULL or misaligned pointer; MOE_ESCRATCH when
+ * work_bytes (or, with saved, saved_bytes) is less than moe_ffn_workspace says;
+ * MOE_EHIP on a runtime error. */
+int moe_ffn_forward(const moe_ffn* f, const void* x, int64_t ldx, int32_t m, void* y, int64_t ldy, void* saved,
+                    size_t saved_bytes, void* work, size_t work_bytes, void* stream);
+
+/* Gradients of the block, from dy [m, D] (row stride lddy):
+ *   dh = dy Wd;  dg = dh uc act'(gc) where g <= limit, else 0;  du = dh act(gc)
+ *   where |u| <= limit, else 0;  dx = dg Wg + du Wu;  dWg = dg^T x;
+ *   dWu = du^T x;  dWd = dy^T h.
+ * x, m, the weights and saved are those of the forward call. dx [m, D] (row
+ * stride lddx), dw_gate and dw_up [I, D] and dw_down [D, I] (row-major, 16-byte
+ * aligned) are written, not added to; each may be NULL and is then not computed.
+ * dg, du and h are rounded to the value type, as operands of the products.
+ * m = 0 writes zeros to the weights' gradients. No output may overlap an input.
+ * Errors as moe_ffn_forward. */
+int moe_ffn_backward(const moe_ffn* f, const void* x, int64_t ldx, const void* dy, int64_t lddy, int32_t m,
+                     const void* saved, size_t saved_bytes, void* dx, int64_t lddx, void* dw_gate, void* dw_up,
+                     void* dw_down, void* work, size_t work_bytes, void* stream);
+
+/* The norm after a block, its gate, the scaled residual, and the norm before the
+ * next block, in one pass over the rows:
+ *   p = y / rms(y) * w_post  (p = y without w_post),  rms(v) = sqrt(mean(v^2) + eps)
+ *   r' = res_scale r + gate p,     n = r' / rms(r') * w_pre
+ * Everything is computed in f32 and rounded once, where it is stored; n comes
+ * from the unrounded r'. */
+#define MOE_GATE_NONE 0     /* 1 */
+#define MOE_GATE_CHANNEL 1  /* gate [dim] */
+#define MOE_GATE_TOKEN 2    /* gate [m] */
+#define MOE_GATE_FULL 3     /* gate [m, dim], row-major */
+typedef struct moe_norm {
+    int32_t dim;         /* 1..16384 */
+    int32_t dtype;       /* MOE_BF16, MOE_F16 or MOE_F32: rows, gate, weights and gradients */
+    float eps;           /* > 0 */
+    float res_scale;     /* finite */
+    const void* w_post;  /* device, [dim], or NULL: no norm after the block */
+    const void* w_pre;   /* device, [dim], or NULL: no norm before the next one (n must then be NULL) */
+} moe_norm;
+
+/* Workspace bytes of moe_norm_backward for m rows. MOE_EINVAL for a bad
+ * description, m < 0 or NULL. */
+int moe_norm_workspace(const moe_norm* f, int32_t m, size_t* backward);
+
+/* r_out [m, dim] = r' and n [m, dim], from r and y [m, dim] and gate (gate_kind
+ * MOE_GATE_*; NULL exactly for MOE_GATE_NONE). Each row stride is >= dim. y may
+ * be NULL (r' = res_scale r; the first block has none before it; w_post must be
+ * NULL then, and gate_kind MOE_GATE_NONE); r_out may be NULL when only n is
+ * wanted. stats: NULL, or f32 [m, 2] for the backward pass: 1 / rms(y) and
+ * 1 / rms(r') (0 where there is no such norm). r_out may be r itself and n may
+ * be y itself (same stride); no other overlap. Pointers are aligned to their
+ * value type (rows whose pointers and strides are multiples of 16 bytes move
+ * fastest). m = 0 does nothing. MOE_EINVAL, MOE_EHIP. */
+int moe_norm_forward(const moe_norm* f, const void* r, int64_t ldr, const void* y, int64_t ldy, const void* gate,
+                     int32_t gate_kind, int32_t m, void* r_out, int64_t ldro, void* n, int64_t ldn, float* stats,
+                     void* stream);
+
+/* Gradients from dr_out (of r') and dn (of n; NULL when w_pre is, and either may
+ * be NULL for zero, not both): with a = w_pre dn, rs1 and rs2 the stats,
+ *   e = dr_out + rs2 (a - r' rs2^2 mean(r' a));   dr = res_scale e
+ *   dp = gate e;  b = w_post dp;  dy = rs1 (b - y rs1^2 mean(y b))  (dp without w_post)
+ *   dgate = e p, summed over what the gate is broadcast over
+ *   dw_post = sum over rows of dp y rs1;   dw_pre = sum over rows of dn r' rs2
+ * r, y, gate and stats as in the forward call (r' is computed again from them).
+ * Any output may be NULL and is then not computed. Sums over rows are made in
+ * f32 in a fixed order. dr may be dr_out itself and dy may be dn itself (same
+ * stride); no other overlap. m = 0 writes zeros to the gradients that are sums
+ * over rows. work: 256-byte aligned; MOE_ESCRATCH when it is too small. */
+int moe_norm_backward(const moe_norm* f, const void* r, int64_t ldr, const void* y, int64_t ldy, const void* gate,
+                      int32_t gate_kind, int32_t m, const float* stats, const void* dr_out, int64_t lddro,
+                      const void* dn, int64_t lddn, void* dr, int64_t lddr, void* dy, int64_t lddy, void* dgate,
+                      void* dw_post, void* dw_pre, void* work, size_t work_bytes, void* stream);
+
+/* A matrix [rows, cols] of 4-bit weights with a scale, and perhaps a zero point,
+ * per `group` consecutive columns of a row: w = scale (code - zero), code and
+ * zero in 0..15. It is read as it lies; nothing is laid out anew. */
+typedef struct moe_w4 {
+    int32_t rows;        /* N: 1..2^22 */
+    int32_t cols;        /* K: a multiple of group, up to 65536 */
+    int32_t group;       /* 32, 64 or 128 */
+    int32_t dtype;       /* MOE_BF16 or MOE_F16: scales, x and the results */
+    const void* codes;   /* device, [rows, cols / 2] bytes, the even column in the low four bits; 16-byte aligned */
+    const void* scales;  /* device, [rows, cols / group] */
+    const void* zeros;   /* device, [rows, cols / group] bytes of 0..15, or NULL: 8 everywhere */
+} moe_w4;
+
+/* y [m, N] = x W^T, summed in f32 with the exact w and rounded once. x [m, K] with
+ * row stride ldx (a multiple of 8; 16-byte aligned), y with row stride ldy >= N
+ * (2-byte aligned). Made for few rows: each 64 rows of x read the weights once.
+ * A row of x that holds an infinity gives NaN. m = 0 does nothing. MOE_EINVAL,
+ * MOE_EHIP. */
+int moe_w4_matmul(const moe_w4* w, const void* x, int64_t ldx, int32_t m, void* y, int64_t ldy, void* stream);
+
+/* h [m, N] = act(gc) uc of g = x Wg^T and u = x Wu^T, clamped as in moe_ffn, in one
+ * launch: the first half of the gated block with 4-bit weights (moe_w4_matmul is
+ * the second). Wg and Wu have the same rows, cols, group and dtype. */
+int moe_w4_gated(const moe_w4* w_gate, const moe_w4* w_up, int32_t act, float limit, const void* x, int64_t ldx,
+                 int32_t m, void* h, int64_t ldh, void* stream);
+
 /* Static text for a status code. */
 const char* moe_strerror(int code);
 

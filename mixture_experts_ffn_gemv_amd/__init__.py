@@ -39,12 +39,27 @@ MOE_PATH_MMQ = 2
 
 MOE_STATIC_SCRATCH_BYTES = 8 << 20
 
+MOE_BF16 = 0
+MOE_F16 = 1
+MOE_F32 = 2
+
+MOE_ACT_SILU = 0
+MOE_ACT_GELU = 1
+
+MOE_GATE_NONE = 0
+MOE_GATE_CHANNEL = 1
+MOE_GATE_TOKEN = 2
+MOE_GATE_FULL = 3
+
 EXPORTED = (
     "moe_create", "moe_destroy", "moe_expert_layout", "moe_pack_expert", "moe_set_slots", "moe_slot_bind",
     "moe_slot_evict",
     "moe_slot_of", "moe_set_host_arena", "moe_route", "moe_forward", "moe_forward_ex", "moe_check",
     "moe_get_stats", "moe_reset_stats", "moe_strerror", "moe_quantize_q8_1", "moe_set_profiling",
     "moe_kernel_times", "moe_set_dispatch", "moe_plan_call", "moe_forward_static",
+    "moe_ffn_workspace", "moe_ffn_forward", "moe_ffn_backward",
+    "moe_norm_workspace", "moe_norm_forward", "moe_norm_backward",
+    "moe_w4_matmul", "moe_w4_gated",
 )
 
 KERNEL_CLASSES = ("router", "quant_h", "topk", "bucket", "gateup", "shared_gateup", "down", "shared_down",
@@ -101,6 +116,42 @@ class moe_plan(ctypes.Structure):
     ]
 
 
+class moe_ffn(ctypes.Structure):
+    _fields_ = [
+        ("dim", ctypes.c_int32),
+        ("inter", ctypes.c_int32),
+        ("dtype", ctypes.c_int32),
+        ("act", ctypes.c_int32),
+        ("limit", ctypes.c_float),
+        ("w_gate", ctypes.c_void_p),
+        ("w_up", ctypes.c_void_p),
+        ("w_down", ctypes.c_void_p),
+    ]
+
+
+class moe_norm(ctypes.Structure):
+    _fields_ = [
+        ("dim", ctypes.c_int32),
+        ("dtype", ctypes.c_int32),
+        ("eps", ctypes.c_float),
+        ("res_scale", ctypes.c_float),
+        ("w_post", ctypes.c_void_p),
+        ("w_pre", ctypes.c_void_p),
+    ]
+
+
+class moe_w4(ctypes.Structure):
+    _fields_ = [
+        ("rows", ctypes.c_int32),
+        ("cols", ctypes.c_int32),
+        ("group", ctypes.c_int32),
+        ("dtype", ctypes.c_int32),
+        ("codes", ctypes.c_void_p),
+        ("scales", ctypes.c_void_p),
+        ("zeros", ctypes.c_void_p),
+    ]
+
+
 class MoeError(RuntimeError):
     def __init__(self, code, where):
         self.code = code
@@ -117,7 +168,7 @@ def lib():
         if not os.path.exists(LIB_PATH):
             raise RuntimeError(f"{LIB_PATH} is missing: build it with __graft_entry__.build()")
         L = ctypes.CDLL(LIB_PATH)
-        vp, i32, sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_size_t
+        vp, i32, i64, sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
         P = ctypes.POINTER
         sigs = {
             "moe_create": [P(moe_cfg), P(vp)],
@@ -141,6 +192,15 @@ def lib():
             "moe_kernel_times": [vp, P(ctypes.c_double), P(ctypes.c_int64), i32],
             "moe_plan_call": [vp, i32, i32, P(moe_plan)],
             "moe_forward_static": [P(moe_cfg), P(moe_weights), vp, vp, vp, i32, vp, vp, vp, vp, vp],
+            "moe_ffn_workspace": [P(moe_ffn), i32, P(sz), P(sz), P(sz)],
+            "moe_ffn_forward": [P(moe_ffn), vp, i64, i32, vp, i64, vp, sz, vp, sz, vp],
+            "moe_ffn_backward": [P(moe_ffn), vp, i64, vp, i64, i32, vp, sz, vp, i64, vp, vp, vp, vp, sz, vp],
+            "moe_norm_workspace": [P(moe_norm), i32, P(sz)],
+            "moe_norm_forward": [P(moe_norm), vp, i64, vp, i64, vp, i32, i32, vp, i64, vp, i64, vp, vp],
+            "moe_norm_backward": [P(moe_norm), vp, i64, vp, i64, vp, i32, i32, vp, vp, i64, vp, i64, vp, i64, vp, i64,
+                                  vp, vp, vp, vp, sz, vp],
+            "moe_w4_matmul": [P(moe_w4), vp, i64, i32, vp, i64, vp],
+            "moe_w4_gated": [P(moe_w4), P(moe_w4), i32, ctypes.c_float, vp, i64, i32, vp, i64, vp],
         }
         for name, args in sigs.items():
             fn = getattr(L, name)
@@ -308,3 +368,174 @@ def moe_get_stats(ctx):
 
 def moe_reset_stats(ctx):
     return _check(lib().moe_reset_stats(ctx), "moe_reset_stats")
+
+
+# ----------------------------------------------------------------------------- operators around the layer
+#
+# Tensors are checked here for what C cannot see (device, type, shape, rows whose
+# values are consecutive); everything else is checked by the entry point.
+
+_DTYPES = {torch.bfloat16: MOE_BF16, torch.float16: MOE_F16, torch.float32: MOE_F32}
+_ACTS = {"silu": MOE_ACT_SILU, "gelu": MOE_ACT_GELU}
+
+
+def _dtype(t, where):
+    if t not in _DTYPES:
+        raise MoeError(MOE_EINVAL, where)
+    return _DTYPES[t]
+
+
+def _act(act, where):
+    act = _ACTS.get(act, act)
+    if act not in (MOE_ACT_SILU, MOE_ACT_GELU):
+        raise MoeError(MOE_EINVAL, where)
+    return act
+
+
+def _rows(t, m, dim, dtype, where):
+    """A device matrix [m, dim] with consecutive values in each row -> (pointer, row stride); None -> (None, 0)."""
+    if t is None:
+        return None, 0
+    if not t.is_cuda or t.dtype is not dtype or t.shape != (m, dim):
+        raise MoeError(MOE_EINVAL, where)
+    ld, one = t.stride()
+    if one != 1 and dim != 1:
+        raise MoeError(MOE_EINVAL, where)
+    return t.data_ptr(), ld if m > 1 else max(ld, dim)
+
+
+def _whole(t, shape, dtype, where):
+    """A contiguous device tensor of that shape and type -> its pointer; None -> None."""
+    if t is None:
+        return None
+    if not t.is_cuda or t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
+        raise MoeError(MOE_EINVAL, where)
+    return t.data_ptr()
+
+
+def _bytes(t, where):
+    """A workspace -> (pointer, bytes); None -> (None, 0)."""
+    if t is None:
+        return None, 0
+    if not t.is_cuda or not t.is_contiguous():
+        raise MoeError(MOE_EINVAL, where)
+    return t.data_ptr(), t.numel() * t.element_size()
+
+
+def make_ffn(w_gate, w_up, w_down, act="silu", limit=0.0):
+    """Describe a dense gated feed-forward block: w_gate, w_up [inter, dim], w_down [dim, inter]
+    (kept alive by the result); act "silu" or "gelu"; limit <= 0: no clamps."""
+    if w_gate.dim() != 2:
+        raise MoeError(MOE_EINVAL, "make_ffn")
+    inter, dim = w_gate.shape
+    dt = w_gate.dtype
+    f = moe_ffn(dim, inter, _dtype(dt, "make_ffn"), _act(act, "make_ffn"), limit,
+                _whole(w_gate, (inter, dim), dt, "make_ffn"), _whole(w_up, (inter, dim), dt, "make_ffn"),
+                _whole(w_down, (dim, inter), dt, "make_ffn"))
+    f.torch_dtype, f.tensors = dt, (w_gate, w_up, w_down)
+    return f
+
+
+def moe_ffn_workspace(f, m):
+    """-> (forward, saved, backward) bytes for m rows."""
+    out = [ctypes.c_size_t() for _ in range(3)]
+    _check(lib().moe_ffn_workspace(ctypes.byref(f), m, *[ctypes.byref(o) for o in out]), "moe_ffn_workspace")
+    return tuple(o.value for o in out)
+
+
+def moe_ffn_forward(f, x, y, work, saved=None, stream=None):
+    """y = block(x), x and y [m, dim]; saved: what moe_ffn_backward takes."""
+    me, m, dt = "moe_ffn_forward", x.shape[0], f.torch_dtype
+    return _check(lib().moe_ffn_forward(ctypes.byref(f), *_rows(x, m, f.dim, dt, me), m, *_rows(y, m, f.dim, dt, me),
+                                        *_bytes(saved, me), *_bytes(work, me), _stream(stream)), me)
+
+
+def moe_ffn_backward(f, x, dy, saved, work, dx=None, dw_gate=None, dw_up=None, dw_down=None, stream=None):
+    """Gradients of the block into the tensors that are given."""
+    me, m, dt = "moe_ffn_backward", x.shape[0], f.torch_dtype
+    wide = (f.inter, f.dim)
+    return _check(lib().moe_ffn_backward(
+        ctypes.byref(f), *_rows(x, m, f.dim, dt, me), *_rows(dy, m, f.dim, dt, me), m, *_bytes(saved, me),
+        *_rows(dx, m, f.dim, dt, me), _whole(dw_gate, wide, dt, me), _whole(dw_up, wide, dt, me),
+        _whole(dw_down, (f.dim, f.inter), dt, me), *_bytes(work, me), _stream(stream)), me)
+
+
+def make_norm(dim, dtype, w_post=None, w_pre=None, eps=1e-6, res_scale=1.0):
+    """Describe the norms around a block: w_post and w_pre [dim] or None (kept alive by the result)."""
+    f = moe_norm(dim, _dtype(dtype, "make_norm"), eps, res_scale, _whole(w_post, (dim,), dtype, "make_norm"),
+                 _whole(w_pre, (dim,), dtype, "make_norm"))
+    f.torch_dtype, f.tensors = dtype, (w_post, w_pre)
+    return f
+
+
+def moe_norm_workspace(f, m):
+    """-> workspace bytes of moe_norm_backward for m rows."""
+    out = ctypes.c_size_t()
+    _check(lib().moe_norm_workspace(ctypes.byref(f), m, ctypes.byref(out)), "moe_norm_workspace")
+    return out.value
+
+
+def _gate(gate, m, dim, dtype, where):
+    """-> (pointer, MOE_GATE_*) of a gate [dim] (per channel), [m, 1] (per token) or [m, dim]."""
+    if gate is None:
+        return None, MOE_GATE_NONE
+    shape = tuple(gate.shape)
+    kind = {(m, 1): MOE_GATE_TOKEN, (m, dim): MOE_GATE_FULL, (dim,): MOE_GATE_CHANNEL}.get(shape)
+    if kind is None:
+        raise MoeError(MOE_EINVAL, where)
+    return _whole(gate, shape, dtype, where), kind
+
+
+def moe_norm_forward(f, r, y, r_out, n, gate=None, stats=None, stream=None):
+    """r_out = res_scale r + gate norm(y), n = norm(r_out). gate [dim] (per channel), [m, 1] (per token)
+    or [m, dim]. y, r_out and n may be None as moe.h says."""
+    me, m, dt, d = "moe_norm_forward", r.shape[0], f.torch_dtype, f.dim
+    return _check(lib().moe_norm_forward(
+        ctypes.byref(f), *_rows(r, m, d, dt, me), *_rows(y, m, d, dt, me), *_gate(gate, m, d, dt, me), m,
+        *_rows(r_out, m, d, dt, me), *_rows(n, m, d, dt, me), _whole(stats, (m, 2), torch.float32, me),
+        _stream(stream)), me)
+
+
+def moe_norm_backward(f, r, y, stats, dr_out, dn, work, gate=None, dr=None, dy=None, dgate=None, dw_post=None,
+                      dw_pre=None, stream=None):
+    """Gradients of moe_norm_forward into the tensors that are given."""
+    me, m, dt, d = "moe_norm_backward", r.shape[0], f.torch_dtype, f.dim
+    if dgate is not None and (gate is None or dgate.shape != gate.shape):
+        raise MoeError(MOE_EINVAL, me)
+    return _check(lib().moe_norm_backward(
+        ctypes.byref(f), *_rows(r, m, d, dt, me), *_rows(y, m, d, dt, me), *_gate(gate, m, d, dt, me), m,
+        _whole(stats, (m, 2), torch.float32, me), *_rows(dr_out, m, d, dt, me), *_rows(dn, m, d, dt, me),
+        *_rows(dr, m, d, dt, me), *_rows(dy, m, d, dt, me), _gate(dgate, m, d, dt, me)[0],
+        _whole(dw_post, (d,), dt, me), _whole(dw_pre, (d,), dt, me), *_bytes(work, me), _stream(stream)), me)
+
+
+def make_w4(codes, scales, zeros=None, group=None):
+    """Describe a matrix of 4-bit weights: codes uint8 [rows, cols / 2], scales [rows, cols / group] (bf16 or
+    f16), zeros uint8 [rows, cols / group] or None (kept alive by the result)."""
+    me = "make_w4"
+    if codes.dim() != 2 or scales.dim() != 2 or not scales.shape[1]:
+        raise MoeError(MOE_EINVAL, me)
+    rows, cols = codes.shape[0], 2 * codes.shape[1]
+    group = cols // scales.shape[1] if group is None else group
+    if group <= 0 or cols % group:
+        raise MoeError(MOE_EINVAL, me)
+    shape = (rows, cols // group)
+    w = moe_w4(rows, cols, group, _dtype(scales.dtype, me), _whole(codes, (rows, cols // 2), torch.uint8, me),
+               _whole(scales, shape, scales.dtype, me), _whole(zeros, shape, torch.uint8, me))
+    w.torch_dtype, w.tensors = scales.dtype, (codes, scales, zeros)
+    return w
+
+
+def moe_w4_matmul(w, x, y, stream=None):
+    """y [m, rows] = x [m, cols] W^T."""
+    me, m, dt = "moe_w4_matmul", x.shape[0], w.torch_dtype
+    return _check(lib().moe_w4_matmul(ctypes.byref(w), *_rows(x, m, w.cols, dt, me), m, *_rows(y, m, w.rows, dt, me),
+                                      _stream(stream)), me)
+
+
+def moe_w4_gated(w_gate, w_up, x, h, act="silu", limit=0.0, stream=None):
+    """h [m, rows] = act(x Wg^T) * (x Wu^T), clamped as in make_ffn."""
+    me, m, dt = "moe_w4_gated", x.shape[0], w_gate.torch_dtype
+    return _check(lib().moe_w4_gated(ctypes.byref(w_gate), ctypes.byref(w_up), _act(act, me), limit,
+                                     *_rows(x, m, w_gate.cols, dt, me), m, *_rows(h, m, w_gate.rows, dt, me),
+                                     _stream(stream)), me)

@@ -1,4 +1,5 @@
-"""Compile the HIP sources under csrc/ into libmoe.so for gfx950 (in-tree).
+"""Compile the HIP sources under csrc/ (the layer) and csrc_block/ (the operators
+around it) into libmoe.so for gfx950 (in-tree).
 
 Each .hip file is compiled to an object in parallel, then linked into a shared
 library next to this file. Packed-FP32 instructions are disabled for the device
@@ -13,6 +14,7 @@ import sys
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
+CSRC_BLOCK = os.path.join(HERE, "csrc_block")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(ROOT, "_build")
 LIB_PATH = os.path.join(HERE, "libmoe.so")
@@ -49,7 +51,7 @@ def _compile(src):
 def build(verbose=False):
     """Build libmoe.so; returns its path. Always recompiles."""
     os.makedirs(BUILD_DIR, exist_ok=True)
-    srcs = sorted(glob.glob(os.path.join(CSRC, "*.hip")))
+    srcs = sorted(glob.glob(os.path.join(CSRC, "*.hip")) + glob.glob(os.path.join(CSRC_BLOCK, "*.hip")))
     with concurrent.futures.ThreadPoolExecutor(max_workers=min(8, len(srcs))) as pool:
         results = list(pool.map(_compile, srcs))
     objs = []
