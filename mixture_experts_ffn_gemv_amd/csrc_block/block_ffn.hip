@@ -52,139 +52,246 @@ struct Operand {
 // hold them: four consecutive i of one q per lane
 MOE_DEV size_t saved_at(int q16, int i16, int I) { return ((size_t)q16 * ((I + 15) / 16) + i16) * 512; }
 
-MOE_DEV int swz_k(int row) { return (row & 7) ^ ((row >> 3) & 1); }            // chunk permutation of a rows x 64 k tile
-MOE_DEV int swz_r(int k) { return ((k & 3) | (((k >> 3) & 1) << 2)) << 1; }    // of a 64 k x rows tile
+// Tiles in LDS. rows x 64 k (128 bytes a row): chunk c of 16 bytes of row r lies at c ^ swz_k(r),
+// so that the 16 rows of an operand read fall on distinct banks.
+MOE_DEV int swz_k(int row) { return (row & 7) ^ ((row >> 3) & 1); }
+// 64 k x rows, rows = 128 or 256: runs of 1024 bytes, PIECE apart, each holding rows k that are
+// never read together; a transposing read takes four rows k of two lane groups at a time, and
+// these lie in eight runs, whose distance puts them on distinct banks. Every read of a
+// lane is then one address and a constant.
+constexpr int PIECE = 1024 + 32;
+constexpr int tile_bytes(int rows, bool by_rows) { return by_rows ? rows / 8 * PIECE : rows * BK * 2; }
+// row k of run c: its part from the wavefront's share of c and the place in the run, and from the unit
+MOE_DEV int run_row_wave(int rows, int waves, int wv, int slot) {
+    const int in = rows == 256 ? 4 * slot : 4 * (slot & 1) + 16 * (slot >> 1);
+    return (wv & 3) + (waves == 8 ? 8 * (wv >> 2) : 0) + in;
+}
+constexpr int run_row_unit(int rows, int waves, int u) {
+    const int far = rows == 256 ? 16 : 32;
+    return waves == 8 ? far * u : 8 * (u & 1) + far * (u >> 1);
+}
 
 MOE_DEV s16x4 read_tr(const uint8_t* p) {
     return __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)p);
 }
 
+// Asks the compiler for this order of half a step's instructions: READS LDS reads, and
+// the first LOADS of the loads into LDS, spread between MFMAS matrix products
+template <int READS, int MFMAS, int LOADS, int R = 0>
+MOE_DEV void interleave() {
+    if constexpr (R < READS) {
+        __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);   // an LDS read
+        if constexpr (R < LOADS) __builtin_amdgcn_sched_group_barrier(0x20, 1, 0);   // a load
+        constexpr int n = (R + 1) * MFMAS / READS - R * MFMAS / READS;
+        if constexpr (n > 0) __builtin_amdgcn_sched_group_barrier(0x8, n, 0);
+        interleave<READS, MFMAS, LOADS, R + 1>();
+    }
+}
+
+// Where a tile lies and what it multiplies
+struct Tile {
+    Operand P, Q;
+    uint16_t* out;   // [q, p] with row stride ldo (DOWN, DX, DW)
+    int64_t ldo;
+    int K, segs, q0, p0;   // segs matrices one after another, K of k each
+};
+// Tile `tile` of a product with nq x np tiles of BQ x BP (DW: along I and along D): eight q tiles
+// deep, so that the tiles an XCD works on at a time share their operands in its L2
+template <Kind KIND, int BQ, int BP>
+MOE_DEV Tile locate(const FfnArgs& a, int tile, int nq, int np) {
+    Tile t;
+    t.K = a.D, t.segs = 1, t.out = nullptr, t.ldo = 0;
+    if (KIND == GATEUP) t.P = {a.wg, a.wu, a.D, a.I}, t.Q = {a.x, a.x, a.ldx, a.m};
+    if (KIND == DOWN) t.P = {a.wd, a.wd, a.I, a.D}, t.Q = {a.h, a.h, a.I, a.m}, t.K = a.I, t.out = a.y, t.ldo = a.ldy;
+    if (KIND == DH) t.P = {a.wd, a.wd, a.I, a.I}, t.Q = {a.dy, a.dy, a.lddy, a.m};
+    if (KIND == DX) t.P = {a.wg, a.wu, a.D, a.D}, t.Q = {a.dg, a.du, a.I, a.m}, t.K = a.I, t.segs = 2, t.out = a.dx, t.ldo = a.lddx;
+    if (KIND == DW) {
+        // products whose output is not wanted have no tiles
+        t.K = a.m;
+        const int each = nq * np, n0 = a.dwg != nullptr ? each : 0, n1 = a.dwu != nullptr ? each : 0;
+        if (tile < n0 + n1) {
+            const bool up = tile >= n0;
+            if (up) tile -= n0;
+            t.P = {a.x, a.x, a.ldx, a.D}, t.Q = {up ? a.du : a.dg, nullptr, a.I, a.I};
+            t.out = up ? a.dwu : a.dwg, t.ldo = a.D;
+        } else {
+            tile -= n0 + n1;
+            t.P = {a.h, a.h, a.I, a.I}, t.Q = {a.dy, a.dy, a.lddy, a.D};
+            t.out = a.dwd, t.ldo = a.I;
+            nq = (a.D + BQ - 1) / BQ, np = (a.I + BP - 1) / BP;
+        }
+    }
+    const int deep = 8 * np, gr = tile / deep, gq = min(8, nq - gr * 8), in = tile - gr * deep;
+    t.q0 = (gr * 8 + in % gq) * BQ;
+    t.p0 = in / gq * (KIND == GATEUP ? BP / 2 : BP);   // GATEUP: 32 rows of Wg, the same 32 of Wu, and so on
+    return t;
+}
+
+// What a wavefront does with the sums of 16 q (q = qw + l16) and its TP p: a lane holds p =
+// 16 i + 4 g + 0..3 in v[i], counted from pw
+template <typename T, Kind KIND, int NI>
+MOE_DEV void finish(const FfnArgs& a, const Tile& t, int qw, int pw, const f32x4 (&v)[NI]) {
+    const int lane = threadIdx.x & 63, l16 = lane & 15, g = lane >> 4, q = qw + l16;
+    if constexpr (KIND == GATEUP) {
+        if (qw >= a.m) return;
+#pragma unroll
+        for (int b = 0; b < NI / 4; ++b)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const f32x4 gv = v[4 * b + i], uv = v[4 * b + 2 + i];
+                const int at = t.p0 + (pw + 64 * b) / 2 + 16 * i, p = at + 4 * g;
+                if (at >= a.I) continue;
+                if (a.saved != nullptr) {
+                    float* s = a.saved + saved_at(qw / 16, at / 16, a.I) + lane * 4;
+                    *reinterpret_cast<f32x4*>(s) = gv;
+                    *reinterpret_cast<f32x4*>(s + 256) = uv;
+                }
+                float h[4];
+#pragma unroll
+                for (int r = 0; r < 4; ++r) h[r] = act_value(clamp_gate(gv[r], a.limit), a.act) * clamp_up(uv[r], a.limit);
+                if (q < a.m && p < a.I)
+                    *reinterpret_cast<uint2*>(a.h + (size_t)q * a.I + p) = make_uint2(T::pack2(h[0], h[1]), T::pack2(h[2], h[3]));
+            }
+    } else if constexpr (KIND == DH) {
+        if (qw >= a.m) return;
+#pragma unroll
+        for (int i = 0; i < NI; ++i) {
+            const int at = t.p0 + pw + 16 * i, p = at + 4 * g;
+            if (at >= a.I) continue;
+            const float* s = a.saved + saved_at(qw / 16, at / 16, a.I) + lane * 4;
+            const f32x4 gv = *reinterpret_cast<const f32x4*>(s), uv = *reinterpret_cast<const f32x4*>(s + 256);
+            float dg[4], du[4], h[4];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const float uc = clamp_up(uv[r], a.limit), dh = v[i][r];
+                float f, df;
+                act_both(clamp_gate(gv[r], a.limit), a.act, f, df);
+                const bool clamped = a.limit > 0.f;
+                dg[r] = clamped && gv[r] > a.limit ? 0.f : dh * uc * df;
+                du[r] = clamped && fabsf(uv[r]) > a.limit ? 0.f : dh * f;
+                h[r] = f * uc;
+            }
+            if (q < a.m && p < a.I) {
+                const size_t o = (size_t)q * a.I + p;
+                *reinterpret_cast<uint2*>(a.dg + o) = make_uint2(T::pack2(dg[0], dg[1]), T::pack2(dg[2], dg[3]));
+                *reinterpret_cast<uint2*>(a.du + o) = make_uint2(T::pack2(du[0], du[1]), T::pack2(du[2], du[3]));
+                *reinterpret_cast<uint2*>(a.h + o) = make_uint2(T::pack2(h[0], h[1]), T::pack2(h[2], h[3]));
+            }
+        }
+    } else {
+        if (q >= t.Q.rows) return;
+#pragma unroll
+        for (int i = 0; i < NI; ++i) {
+            const int p = t.p0 + pw + 16 * i + 4 * g;
+            if (p < t.P.rows)
+                *reinterpret_cast<uint2*>(t.out + (size_t)q * t.ldo + p) = make_uint2(T::pack2(v[i][0], v[i][1]), T::pack2(v[i][2], v[i][3]));
+        }
+    }
+}
+
+// The work of one launch: the first `whole` tiles by a workgroup each, the `rest` (what does
+// not fill the CUs once more) by `splits` workgroups each, every one with its part of k
+struct Plan {
+    int nq, np;          // tiles along q and p
+    int whole, rest, splits;
+    float* partial;      // [split][rest][j][i][thread] of the split tiles' sums, four f32 each
+};
+
 // BQ x BP tile of the output, WQ x WP wavefronts
 template <typename T, Kind KIND, int BQ, int BP, int WQ, int WP>
-__global__ __launch_bounds__(64 * WQ * WP) void ffn_gemm_kernel(FfnArgs a, int nq, int np, int tiles) {
+__global__ __launch_bounds__(64 * WQ * WP) void ffn_gemm_kernel(FfnArgs a, Plan plan) {
     extern __shared__ __align__(16) uint8_t smem[];
     constexpr int TH = 64 * WQ * WP, TQ = BQ / WQ, TP = BP / WP, NI = TP / 16, NJ = TQ / 16;
-    constexpr int P_BYTES = BP * BK * 2, STEP = (BP + BQ) * BK * 2;
-    constexpr int UP = BP * 8 / TH, UQ = BQ * 8 / TH;   // 16-byte units per thread
+    constexpr int UP = BP * 8 / TH, UQ = BQ * 8 / TH, NW = TH / 64;   // 16-byte units per thread
     constexpr bool PR = p_by_rows(KIND), QR = q_by_rows(KIND);
+    constexpr int P_BYTES = tile_bytes(BP, PR), STEP = P_BYTES + tile_bytes(BQ, QR);
+    static_assert(NW == 8 || NW == 4, "");
     const int tid = threadIdx.x, lane = tid & 63, wv = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int l16 = lane & 15, g = lane >> 4, wq = wv / WP, wp = wv % WP;
 
-    // which tile: consecutive tiles on one XCD, eight q tiles deep, so that the tiles an XCD
-    // works on at a time share their operands in its L2
-    int tile = xcd_logical_block(blockIdx.x, tiles);
-    int which = 0;   // DW: the product
-    if (tile >= tiles) return;
-    Operand P, Q;
-    int K = a.D, segs = 1, tq_n = nq, tp_n = np;
-    if (KIND == GATEUP) P = {a.wg, a.wu, a.D, a.I}, Q = {a.x, a.x, a.ldx, a.m};
-    if (KIND == DOWN) P = {a.wd, a.wd, a.I, a.D}, Q = {a.h, a.h, a.I, a.m}, K = a.I;
-    if (KIND == DH) P = {a.wd, a.wd, a.I, a.I}, Q = {a.dy, a.dy, a.lddy, a.m};
-    if (KIND == DX) P = {a.wg, a.wu, a.D, a.D}, Q = {a.dg, a.du, a.I, a.m}, K = a.I, segs = 2;
-    uint16_t* out = nullptr;
-    int64_t ldo = 0;
-    if (KIND == DOWN) out = a.y, ldo = a.ldy;
-    if (KIND == DX) out = a.dx, ldo = a.lddx;
-    if (KIND == DW) {
-        // products whose output is not wanted have no tiles
-        K = a.m;
-        const int each = nq * np;   // nq: tiles along I, np: tiles along D
-        const int n0 = a.dwg != nullptr ? each : 0, n1 = a.dwu != nullptr ? each : 0;
-        if (tile < n0) which = 0;
-        else if (tile < n0 + n1) which = 1, tile -= n0;
-        else which = 2, tile -= n0 + n1;
-        if (which < 2) {
-            P = {a.x, a.x, a.ldx, a.D};
-            Q = {which == 0 ? a.dg : a.du, nullptr, a.I, a.I};
-            out = which == 0 ? a.dwg : a.dwu, ldo = a.D;
-        } else {
-            P = {a.h, a.h, a.I, a.I};
-            Q = {a.dy, a.dy, a.lddy, a.D};
-            out = a.dwd, ldo = a.I;
-            tq_n = (a.D + BQ - 1) / BQ, tp_n = (a.I + BP - 1) / BP;
-        }
+    // consecutive tiles (of a split part: those of one part of k) on one XCD
+    const int whole_blocks = (plan.whole + 7) / 8 * 8;
+    int tile, split = -1;
+    if ((int)blockIdx.x < whole_blocks) {
+        tile = xcd_logical_block(blockIdx.x, plan.whole);
+        if (tile >= plan.whole) return;
+    } else {
+        const int items = plan.rest * plan.splits, item = xcd_logical_block(blockIdx.x - whole_blocks, items);
+        if (item >= items) return;
+        split = item / plan.rest;
+        tile = plan.whole + item - split * plan.rest;
     }
-    const int deep = 8 * tp_n, gr = tile / deep, gq = min(8, tq_n - gr * 8), in = tile - gr * deep;
-    const int q0 = (gr * 8 + in % gq) * BQ, ptile = in / gq;
-    constexpr int PSPAN = KIND == GATEUP ? BP / 2 : BP;   // GATEUP: 32 rows of Wg, the same 32 of Wu, and so on
-    const int p0 = ptile * PSPAN;
+    const Tile t = locate<KIND, BQ, BP>(a, tile, plan.nq, plan.np);
+    const Operand &P = t.P, &Q = t.Q;
+    const int K = t.K, segs = t.segs, q0 = t.q0, p0 = t.p0;
+    constexpr int PSPAN = KIND == GATEUP ? BP / 2 : BP;
 
-    // this thread's units of the tiles: byte offsets from the tile's corner, and chunk
-    // numbers along k (for the K tail)
-    uint32_t offp[UP], offq[UQ];
-    int ck_p = 0, ck_q = 0;   // K-contiguous tiles: the unit's chunk (the same in every unit of a thread)
-    auto offsets = [&](auto& off, const Operand& o, bool by_rows, int R, int& ck, bool paired, int U) {
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int p = u * TH + tid;
-            if (by_rows) {
-                const int k = p / (R / 8), c = (p % (R / 8)) ^ swz_r(k);
-                off[u] = (uint32_t)(k * o.ld + c * 8) * 2;
-            } else {
-                const int row = p >> 3, c = (p & 7) ^ swz_k(row);
-                const int r = paired ? (row >> 6) * 32 + (row & 31) : row;
-                ck = c;
-                off[u] = (uint32_t)(r * o.ld + c * 8) * 2;
-            }
-        }
-    };
-    offsets(offp, P, PR, BP, ck_p, KIND == GATEUP, UP);
-    offsets(offq, Q, QR, BQ, ck_q, false, UQ);
+    // This thread's first unit of each tile: its byte offset from the tile's corner; unit u is
+    // unit_rows(u) rows further. A K-contiguous tile's units of a thread share their chunk of k.
+    const int slot_p = PR ? lane / (BP / 8) : 0, slot_q = QR ? lane / (BQ / 8) : 0;
+    const int row_k = wv * 8 + (lane >> 3), chunk = (lane & 7) ^ swz_k(row_k);
+    const int first = KIND == GATEUP ? (row_k & 31) : row_k;
+    const uint32_t off_p = PR ? (uint32_t)(run_row_wave(BP, NW, wv, slot_p) * P.ld + lane % (BP / 8) * 8) * 2
+                              : (uint32_t)(first * P.ld + chunk * 8) * 2;
+    const uint32_t off_q = QR ? (uint32_t)(run_row_wave(BQ, NW, wv, slot_q) * Q.ld + lane % (BQ / 8) * 8) * 2
+                              : (uint32_t)(row_k * Q.ld + chunk * 8) * 2;
 
-    const int seg_steps = (K + BK - 1) / BK, nk = seg_steps * segs;
+    const int seg_steps = (K + BK - 1) / BK, steps = seg_steps * segs;
+    const int kt0 = split < 0 ? 0 : (int)((int64_t)split * steps / plan.splits);
+    const int nk = (split < 0 ? steps : (int)((int64_t)(split + 1) * steps / plan.splits)) - kt0;
     auto stage = [&](int kt, uint8_t* buf) {
+        const bool past = kt >= nk;
+        kt += kt0;
         const int seg = segs == 2 && kt >= seg_steps ? 1 : 0;
         const int k0 = (kt - seg * seg_steps) * BK, kleft = min(BK, K - k0);
-        const bool tail = kleft < BK;
-        auto side = [&](auto& off, const Operand& o, bool by_rows, int at, int span, int ck, bool paired, int U, uint8_t* dst) {
+        const uint32_t beyond = chunk * 8 >= kleft ? PAST : 0u;   // a K tail's missing chunks
+        auto side = [&](uint32_t off, const Operand& o, bool by_rows, int R, int at, int span, bool paired, int U, uint8_t* dst) {
             const uint16_t* base = seg ? o.b : o.a;
             const int left = min(o.rows - at, span);
             if (by_rows) {
-                const auto R = buffer_rsrc(base + (size_t)k0 * o.ld + at, (uint32_t)((kleft - 1) * o.ld + left) * 2);
+                const auto buffer = buffer_rsrc(base + (size_t)k0 * o.ld + at, past ? 0u : (uint32_t)((kleft - 1) * o.ld + left) * 2);
 #pragma unroll
-                for (int u = 0; u < U; ++u) buffer_load_lds16(R, dst + (u * TH + wv * 64) * 16, off[u]);
+                for (int u = 0; u < U; ++u)
+                    buffer_load_lds16(buffer, dst + (u * NW + wv) * PIECE, off + (uint32_t)(run_row_unit(R, NW, u) * o.ld * 2));
             } else {
-                const uint32_t bytes = (uint32_t)((left - 1) * o.ld + kleft) * 2;
+                const uint32_t bytes = past ? 0u : (uint32_t)((left - 1) * o.ld + kleft) * 2;
                 const size_t corner = (size_t)at * o.ld + k0;
-                const auto R = buffer_rsrc(base + corner, bytes);
-                const auto S = paired ? buffer_rsrc(o.b + corner, bytes) : R;
+                // GATEUP: rows 32..63 of every 64 are the second matrix's: with eight wavefronts those
+                // of wavefronts 4..7, with four those of every second unit
+                const bool second = paired && NW == 8 && (wv & 4);
+                const auto buffer = buffer_rsrc((second ? o.b : base) + corner, bytes);
+                const auto other = paired && NW == 4 ? buffer_rsrc(o.b + corner, bytes) : buffer;
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
-                    // a K tail's missing chunks are within the buffer for all rows but the last
-                    const uint32_t v = tail && ck * 8 >= kleft ? PAST : off[u];
-                    const bool second = paired && ((((u * TH + wv * 64) >> 3) >> 5) & 1);
-                    if (second) buffer_load_lds16(S, dst + (u * TH + wv * 64) * 16, v);
-                    else buffer_load_lds16(R, dst + (u * TH + wv * 64) * 16, v);
+                    const int rows = paired ? (u * NW * 8 >> 6) * 32 : u * NW * 8;
+                    const uint32_t v = (off + (uint32_t)(rows * o.ld * 2)) | beyond;
+                    uint8_t* to = dst + (u * NW + wv) * 1024;
+                    if (paired && NW == 4 && (u & 1)) buffer_load_lds16(other, to, v);
+                    else buffer_load_lds16(buffer, to, v);
                 }
             }
         };
-        side(offp, P, PR, p0, PSPAN, ck_p, KIND == GATEUP, UP, buf);
-        side(offq, Q, QR, q0, BQ, ck_q, false, UQ, buf + P_BYTES);
+        side(off_p, P, PR, BP, p0, PSPAN, KIND == GATEUP, UP, buf);
+        side(off_q, Q, QR, BQ, q0, BQ, false, UQ, buf + P_BYTES);
     };
 
-    // LDS byte offsets of this lane's operand reads, for k 0..31 of a step
-    int rdp[NI], rdq[NJ];
-    auto reads = [&](auto& rd, bool by_rows, int R, int base, int n) {
-#pragma unroll
-        for (int i = 0; i < n; ++i) {
-            const int r0 = base + 16 * i;
-            if (by_rows) {
-                const int k = 8 * g + (l16 >> 2);
-                rd[i] = k * R * 2 + (((r0 / 8 + ((l16 >> 1) & 1)) ^ swz_r(k)) << 4) + (l16 & 1) * 8;
-            } else {
-                rd[i] = (r0 + l16) * (BK * 2) + ((g ^ swz_k(l16)) << 4);
-            }
-        }
-    };
-    reads(rdp, PR, BP, wp * TP, NI);
-    reads(rdq, QR, BQ, wq * TQ, NJ);
-    auto fragment = [&](const uint8_t* tile_lds, int rd, bool by_rows, int R, int kk) -> s16x8 {
+    // LDS byte offset of this lane's operand reads for half kk of a step; operand i lies 16 rows
+    // further, which is a constant in either layout
+    auto read_base = [&](bool by_rows, int R, int base, int kk) {
         if (by_rows) {
-            const uint8_t* p = tile_lds + rd + kk * 32 * R * 2;
-            const s16x4 lo = read_tr(p), hi = read_tr(p + 4 * R * 2);
+            const int run = (l16 >> 2) + 4 * (g & 1) + (R == 256 ? 8 * (g >> 1) : 0);
+            return (run + kk * (R / 16)) * PIECE + (R == 256 ? 0 : (g >> 1) * 512) + base * 2 + (l16 & 3) * 8;
+        }
+        return (base + l16) * (BK * 2) + (((g + 4 * kk) ^ swz_k(l16)) << 4);
+    };
+    const int rdp0 = read_base(PR, BP, wp * TP, 0), rdp1 = read_base(PR, BP, wp * TP, 1);
+    const int rdq0 = read_base(QR, BQ, wq * TQ, 0), rdq1 = read_base(QR, BQ, wq * TQ, 1);
+    auto fragment = [&](const uint8_t* p, bool by_rows, int R, int i) -> s16x8 {
+        if (by_rows) {
+            const s16x4 lo = read_tr(p + i * 32), hi = read_tr(p + i * 32 + R * 2);   // k + 0..3, k + 4..7
             return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
         }
-        return *reinterpret_cast<const s16x8*>(tile_lds + (rd ^ (kk << 6)));   // chunk g + 4 kk, permuted
+        return *reinterpret_cast<const s16x8*>(p + i * 16 * BK * 2);
     };
 
     f32x4 acc[NI][NJ];
@@ -193,110 +300,171 @@ __global__ __launch_bounds__(64 * WQ * WP) void ffn_gemm_kernel(FfnArgs a, int n
 #pragma unroll
         for (int j = 0; j < NJ; ++j) acc[i][j] = (f32x4){0.f, 0.f, 0.f, 0.f};
 
-    if (nk > 0) stage(0, smem);
-    for (int kt = 0; kt < nk; ++kt) {
+    // Half a K step (32 k) at a time: while one half is multiplied, the operands of the
+    // next are read from LDS into registers. A step's buffer is free once its second half
+    // is in registers, in the middle of its products: the barrier there lets the loads of
+    // the step after next go into it, a whole step before they are needed.
+    s16x8 fp[2][NI], fq[2][NJ];
+    auto read_half = [&](const uint8_t* buf, int kk, int to) {
+        const uint8_t *bp = buf + (kk ? rdp1 : rdp0), *bq = buf + P_BYTES + (kk ? rdq1 : rdq0);
+#pragma unroll
+        for (int i = 0; i < NI; ++i) fp[to][i] = fragment(bp, PR, BP, i);
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) fq[to][j] = fragment(bq, QR, BQ, j);
+    };
+    auto multiply = [&](int from) {
+#pragma unroll
+        for (int j = 0; j < NJ; ++j)
+#pragma unroll
+            for (int i = 0; i < NI; ++i) acc[i][j] = T::mfma(fp[from][i], fq[from][j], acc[i][j]);
+    };
+    constexpr int READS = NI * (PR ? 2 : 1) + NJ * (QR ? 2 : 1), MFMAS = NI * NJ;
+    // Two steps, one of each buffer. The buffers are the lambda's own restricted pointers so
+    // that the compiler sees that the loads into one do not touch what is read from the other:
+    // it would wait for every load before the next LDS read.
+    auto two_steps = [&](uint8_t* __restrict b0, uint8_t* __restrict b1, int kt) {
+        read_half(b0, 1, 1);
+        multiply(0);
+        interleave<READS, MFMAS, 0>();
+        wait_vm_loads<0>();   // step kt + 1 has landed
+        barrier_lds();        // for every wavefront, and every one has read the last of step kt
+        stage(kt + 2, b0);
+        read_half(b1, 0, 0);
+        multiply(1);
+        interleave<READS, MFMAS, UP + UQ>();
+        read_half(b1, 1, 1);
+        multiply(0);
+        interleave<READS, MFMAS, 0>();
         wait_vm_loads<0>();
-        barrier_lds();   // step kt is in LDS for every wavefront; the other buffer is free
-        const uint8_t* buf = smem + (kt & 1) * STEP;
-        if (kt + 1 < nk) stage(kt + 1, smem + ((kt + 1) & 1) * STEP);
-#pragma unroll
-        for (int kk = 0; kk < BK / 32; ++kk) {
-            s16x8 fp[NI], fq[NJ];
-#pragma unroll
-            for (int i = 0; i < NI; ++i) fp[i] = fragment(buf, rdp[i], PR, BP, kk);
-#pragma unroll
-            for (int j = 0; j < NJ; ++j) fq[j] = fragment(buf + P_BYTES, rdq[j], QR, BQ, kk);
-#pragma unroll
-            for (int j = 0; j < NJ; ++j)
-#pragma unroll
-                for (int i = 0; i < NI; ++i) acc[i][j] = T::mfma(fp[i], fq[j], acc[i][j]);
+        barrier_lds();
+        stage(kt + 3, b1);    // (past the last step: zeros)
+        read_half(b0, 0, 0);
+        multiply(1);
+        interleave<READS, MFMAS, UP + UQ>();
+    };
+    if (nk > 0) {
+        stage(0, smem);
+        stage(1, smem + STEP);
+        wait_vm_loads<UP + UQ>();
+        barrier_lds();
+        read_half(smem, 0, 0);
+        int kt = 0;
+        for (; kt + 2 < nk; kt += 2) two_steps(smem, smem + STEP, kt);
+        read_half(smem, 1, 1);
+        multiply(0);
+        multiply(1);
+        wait_vm_loads<0>();   // (no load into LDS outlives the workgroup)
+        if (kt + 1 < nk) {
+            barrier_lds();
+            read_half(smem + STEP, 0, 0);
+            read_half(smem + STEP, 1, 1);
+            multiply(0);
+            multiply(1);
         }
     }
 
-    // a lane holds p = 16 i + 4 g + 0..3 of q = 16 j + l16 (of its wavefront's part)
+    if (split >= 0) {
+        f32x4* o = reinterpret_cast<f32x4*>(plan.partial) + (size_t)(split * plan.rest + tile - plan.whole) * NI * NJ * TH + tid;
+#pragma unroll
+        for (int j = 0; j < NJ; ++j)
+#pragma unroll
+            for (int i = 0; i < NI; ++i) o[(j * NI + i) * TH] = acc[i][j];
+        return;
+    }
 #pragma unroll
     for (int j = 0; j < NJ; ++j) {
-        const int q = q0 + wq * TQ + 16 * j + l16, q16 = (q0 + wq * TQ) / 16 + j;
-        if constexpr (KIND == GATEUP) {
-            if (16 * q16 >= a.m) continue;
+        f32x4 v[NI];
 #pragma unroll
-            for (int b = 0; b < NI / 4; ++b)
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const f32x4 gv = acc[4 * b + i][j], uv = acc[4 * b + 2 + i][j];
-                    const int at = p0 + (wp * TP + 64 * b) / 2 + 16 * i, p = at + 4 * g;
-                    if (at >= a.I) continue;
-                    if (a.saved != nullptr) {
-                        float* s = a.saved + saved_at(q16, at / 16, a.I) + lane * 4;
-                        *reinterpret_cast<f32x4*>(s) = gv;
-                        *reinterpret_cast<f32x4*>(s + 256) = uv;
-                    }
-                    float h[4];
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) h[r] = act_value(clamp_gate(gv[r], a.limit), a.act) * clamp_up(uv[r], a.limit);
-                    if (q < a.m && p < a.I)
-                        *reinterpret_cast<uint2*>(a.h + (size_t)q * a.I + p) = make_uint2(T::pack2(h[0], h[1]), T::pack2(h[2], h[3]));
-                }
-        } else if constexpr (KIND == DH) {
-            if (16 * q16 >= a.m) continue;
-#pragma unroll
-            for (int i = 0; i < NI; ++i) {
-                const int at = p0 + wp * TP + 16 * i, p = at + 4 * g;
-                if (at >= a.I) continue;
-                const float* s = a.saved + saved_at(q16, at / 16, a.I) + lane * 4;
-                const f32x4 gv = *reinterpret_cast<const f32x4*>(s), uv = *reinterpret_cast<const f32x4*>(s + 256);
-                float dg[4], du[4], h[4];
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const float uc = clamp_up(uv[r], a.limit);
-                    float v, dv;
-                    act_both(clamp_gate(gv[r], a.limit), a.act, v, dv);
-                    const float dh = acc[i][j][r];
-                    const bool clamped = a.limit > 0.f;
-                    dg[r] = clamped && gv[r] > a.limit ? 0.f : dh * uc * dv;
-                    du[r] = clamped && fabsf(uv[r]) > a.limit ? 0.f : dh * v;
-                    h[r] = v * uc;
-                }
-                if (q < a.m && p < a.I) {
-                    const size_t o = (size_t)q * a.I + p;
-                    *reinterpret_cast<uint2*>(a.dg + o) = make_uint2(T::pack2(dg[0], dg[1]), T::pack2(dg[2], dg[3]));
-                    *reinterpret_cast<uint2*>(a.du + o) = make_uint2(T::pack2(du[0], du[1]), T::pack2(du[2], du[3]));
-                    *reinterpret_cast<uint2*>(a.h + o) = make_uint2(T::pack2(h[0], h[1]), T::pack2(h[2], h[3]));
-                }
-            }
-        } else {
-            if (q >= Q.rows) continue;
-#pragma unroll
-            for (int i = 0; i < NI; ++i) {
-                const int p = p0 + wp * TP + 16 * i + 4 * g;
-                const f32x4 v = acc[i][j];
-                if (p < P.rows)
-                    *reinterpret_cast<uint2*>(out + (size_t)q * ldo + p) = make_uint2(T::pack2(v[0], v[1]), T::pack2(v[2], v[3]));
-            }
-        }
+        for (int i = 0; i < NI; ++i) v[i] = acc[i][j];
+        finish<T, KIND, NI>(a, t, q0 + wq * TQ + 16 * j, wp * TP, v);
     }
+}
+
+// The split tiles' sums, added in order of k, and what is done with them: a workgroup per
+// tile and j (16 q of each wavefront)
+template <typename T, Kind KIND, int BQ, int BP, int WQ, int WP>
+__global__ __launch_bounds__(64 * WQ * WP) void ffn_join_kernel(FfnArgs a, Plan plan) {
+    constexpr int TH = 64 * WQ * WP, TQ = BQ / WQ, TP = BP / WP, NI = TP / 16, NJ = TQ / 16;
+    const int tid = threadIdx.x, wv = tid >> 6, wq = wv / WP, wp = wv % WP;
+    const int r = blockIdx.x / NJ, j = blockIdx.x % NJ;
+    const f32x4* from = reinterpret_cast<const f32x4*>(plan.partial) + ((size_t)r * NJ + j) * NI * TH + tid;
+    f32x4 v[NI];
+#pragma unroll
+    for (int i = 0; i < NI; ++i) v[i] = from[i * TH];
+#pragma unroll 2
+    for (int s = 1; s < plan.splits; ++s) {
+        const f32x4* f = from + (size_t)s * plan.rest * NI * NJ * TH;
+#pragma unroll
+        for (int i = 0; i < NI; ++i) v[i] += f[i * TH];
+    }
+    const Tile t = locate<KIND, BQ, BP>(a, plan.whole + r, plan.nq, plan.np);
+    finish<T, KIND, NI>(a, t, t.q0 + wq * TQ + 16 * j, wp * TP, v);
 }
 
 int cdiv(int a, int b) { return (a + b - 1) / b; }
 
-template <typename T, Kind KIND, int BQ, int BP, int WQ, int WP>
-hipError_t launch_tiles(const FfnArgs& a, hipStream_t st) {
-    int nq = cdiv(a.m, BQ), np = cdiv(KIND == GATEUP ? 2 * a.I : KIND == DH ? a.I : a.D, BP), tiles = nq * np;
-    if (KIND == DW) {
-        nq = cdiv(a.I, BQ), np = cdiv(a.D, BP);
-        tiles = nq * np * ((a.dwg != nullptr) + (a.dwu != nullptr));
-        if (a.dwd != nullptr) tiles += cdiv(a.D, BQ) * cdiv(a.I, BP);
+// Tiles of B x B, B = 256 (eight wavefronts, one workgroup per CU) or 128 (four, two per CU)
+constexpr int N_CU = 256;
+struct Product {
+    Plan plan;
+    int tile;         // 256 or 128
+    size_t bytes;     // of plan.partial
+};
+
+// How a product is cut up. Costs in units of one K step of a 256 x 256 tile on a CU (1.65 us): a
+// 128 x 128 tile's step takes 0.33 of it (a quarter of the products, at three quarters of the rate);
+// the split tiles' sums pass through memory twice (0.06 a 256 x 256 tile and split, and 4 for the
+// second launch).
+Product plan_product(Kind kind, int m, int D, int I, int wide, bool down) {
+    Product best{};
+    double best_cost = 1e30;
+    for (int B : {256, 128}) {
+        Product p{};
+        p.tile = B;
+        const int steps = kind == DX ? 2 * cdiv(I, BK) : cdiv(kind == DOWN ? I : kind == DW ? m : D, BK);
+        int tiles;
+        if (kind == DW) {
+            p.plan.nq = cdiv(I, B), p.plan.np = cdiv(D, B);
+            tiles = p.plan.nq * p.plan.np * (wide + (down ? 1 : 0));
+        } else {
+            p.plan.nq = cdiv(m, B), p.plan.np = cdiv(kind == GATEUP ? 2 * I : kind == DH ? I : D, B);
+            tiles = p.plan.nq * p.plan.np;
+        }
+        const int slots = B == 256 ? N_CU : 2 * N_CU;
+        const double step = B == 256 ? 1 : 0.66, share = B == 256 ? 0.06 : 0.015;   // (two workgroups share a CU)
+        const int rounds = tiles / slots, rest = tiles % slots;
+        double cost = rounds * (double)steps * step;
+        p.plan.whole = tiles, p.plan.splits = 1;
+        if (rest > 0) {
+            double tail = steps * step;
+            for (int s = 2; s <= 16 && s * 2 <= steps && rest * s <= slots; ++s) {
+                const double t = cdiv(steps, s) * step + 4 + share * rest * s;
+                if (t < tail) tail = t, p.plan.whole = tiles - rest, p.plan.rest = rest, p.plan.splits = s;
+            }
+            cost += tail;
+        }
+        p.bytes = p.plan.rest > 0 ? (size_t)p.plan.rest * p.plan.splits * B * B * sizeof(float) : 0;
+        if (cost < best_cost) best_cost = cost, best = p;
     }
-    if (tiles == 0) return hipSuccess;
-    return launch_kernel(ffn_gemm_kernel<T, KIND, BQ, BP, WQ, WP>, dim3((tiles + 7) / 8 * 8), dim3(64 * WQ * WP),
-                         2 * (BQ + BP) * BK * 2, st, a, nq, np, tiles);
+    return best;
+}
+
+template <typename T, Kind KIND, int B, int WQ, int WP>
+hipError_t launch_tiles(const FfnArgs& a, const Plan& plan, hipStream_t st) {
+    const int grid = (plan.whole + 7) / 8 * 8 + (plan.rest * plan.splits + 7) / 8 * 8;
+    if (grid == 0) return hipSuccess;
+    constexpr int NJ = B / WQ / 16;
+    const hipError_t e = launch_kernel(ffn_gemm_kernel<T, KIND, B, B, WQ, WP>, dim3(grid), dim3(64 * WQ * WP),
+                                       2 * (tile_bytes(B, p_by_rows(KIND)) + tile_bytes(B, q_by_rows(KIND))), st, a, plan);
+    if (e != hipSuccess || plan.rest == 0) return e;
+    return launch_kernel(ffn_join_kernel<T, KIND, B, B, WQ, WP>, dim3(plan.rest * NJ), dim3(64 * WQ * WP), 0, st, a, plan);
 }
 
 template <typename T, Kind KIND>
-hipError_t launch_product(const FfnArgs& a, hipStream_t st) {
-    const int out_q = KIND == DW ? a.I : a.m, out_p = KIND == GATEUP ? 2 * a.I : KIND == DH ? a.I : a.D;
-    if (cdiv(out_q, 256) * cdiv(out_p, 256) * (KIND == DW ? 3 : 1) >= 128) return launch_tiles<T, KIND, 256, 256, 2, 4>(a, st);
-    return launch_tiles<T, KIND, 128, 128, 2, 2>(a, st);
+hipError_t launch_product(const FfnArgs& a, float* partial, hipStream_t st) {
+    Product p = plan_product(KIND, a.m, a.D, a.I, (a.dwg != nullptr) + (a.dwu != nullptr), a.dwd != nullptr);
+    p.plan.partial = partial;
+    return p.tile == 256 ? launch_tiles<T, KIND, 256, 2, 4>(a, p.plan, st) : launch_tiles<T, KIND, 128, 2, 2>(a, p.plan, st);
 }
 
 constexpr int MAX_M = 1 << 24;
@@ -318,8 +486,18 @@ bool rows_ok(const void* p, int64_t ld, int dim) {
 }
 
 size_t rows_bytes(const moe_ffn* f, int m) { return round_up((size_t)m * f->inter * 2, 256); }
-size_t forward_bytes(const moe_ffn* f, int m) { return rows_bytes(f, m); }
-size_t backward_bytes(const moe_ffn* f, int m) { return 3 * rows_bytes(f, m); }
+// room for the split tiles' sums of the products of one direction, whichever outputs are wanted
+size_t forward_partial(const moe_ffn* f, int m) {
+    return std::max(plan_product(GATEUP, m, f->dim, f->inter, 0, false).bytes, plan_product(DOWN, m, f->dim, f->inter, 0, false).bytes);
+}
+size_t backward_partial(const moe_ffn* f, int m) {
+    size_t b = std::max(plan_product(DH, m, f->dim, f->inter, 0, false).bytes, plan_product(DX, m, f->dim, f->inter, 0, false).bytes);
+    for (int wide = 0; wide <= 2; ++wide)
+        for (bool down : {false, true}) b = std::max(b, plan_product(DW, m, f->dim, f->inter, wide, down).bytes);
+    return b;
+}
+size_t forward_bytes(const moe_ffn* f, int m) { return rows_bytes(f, m) + forward_partial(f, m); }
+size_t backward_bytes(const moe_ffn* f, int m) { return 3 * rows_bytes(f, m) + backward_partial(f, m); }
 size_t saved_bytes_of(const moe_ffn* f, int m) { return (size_t)cdiv(m, 16) * cdiv(f->inter, 16) * 2048; }
 
 FfnArgs describe(const moe_ffn* f, int m) {
@@ -332,16 +510,16 @@ FfnArgs describe(const moe_ffn* f, int m) {
 }
 
 template <typename T>
-hipError_t forward(const FfnArgs& a, hipStream_t st) {
-    const hipError_t e = launch_product<T, GATEUP>(a, st);
-    return e != hipSuccess ? e : launch_product<T, DOWN>(a, st);
+hipError_t forward(const FfnArgs& a, float* partial, hipStream_t st) {
+    const hipError_t e = launch_product<T, GATEUP>(a, partial, st);
+    return e != hipSuccess ? e : launch_product<T, DOWN>(a, partial, st);
 }
 
 template <typename T>
-hipError_t backward(const FfnArgs& a, hipStream_t st) {
-    hipError_t e = a.m > 0 ? launch_product<T, DH>(a, st) : hipSuccess;
-    if (e == hipSuccess && a.m > 0 && a.dx != nullptr) e = launch_product<T, DX>(a, st);
-    if (e == hipSuccess) e = launch_product<T, DW>(a, st);
+hipError_t backward(const FfnArgs& a, float* partial, hipStream_t st) {
+    hipError_t e = a.m > 0 ? launch_product<T, DH>(a, partial, st) : hipSuccess;
+    if (e == hipSuccess && a.m > 0 && a.dx != nullptr) e = launch_product<T, DX>(a, partial, st);
+    if (e == hipSuccess) e = launch_product<T, DW>(a, partial, st);
     return e;
 }
 
@@ -376,8 +554,9 @@ int moe_ffn_forward(const moe_ffn* f, const void* x, int64_t ldx, int32_t m, voi
     a.y = reinterpret_cast<uint16_t*>(y), a.ldy = ldy;
     a.h = reinterpret_cast<uint16_t*>(work);
     a.saved = reinterpret_cast<float*>(saved);
+    float* const partial = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(work) + rows_bytes(f, m));
     const hipStream_t st = (hipStream_t)stream;
-    return status_of(f->dtype == MOE_BF16 ? forward<Bf16>(a, st) : forward<F16>(a, st));
+    return status_of(f->dtype == MOE_BF16 ? forward<Bf16>(a, partial, st) : forward<F16>(a, partial, st));
 }
 
 int moe_ffn_backward(const moe_ffn* f, const void* x, int64_t ldx, const void* dy, int64_t lddy, int32_t m,
@@ -406,8 +585,9 @@ int moe_ffn_backward(const moe_ffn* f, const void* x, int64_t ldx, const void* d
     a.dwg = reinterpret_cast<uint16_t*>(dw_gate);
     a.dwu = reinterpret_cast<uint16_t*>(dw_up);
     a.dwd = reinterpret_cast<uint16_t*>(dw_down);
+    float* const partial = m > 0 ? reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(work) + 3 * rows_bytes(f, m)) : nullptr;
     const hipStream_t st = (hipStream_t)stream;
-    return status_of(f->dtype == MOE_BF16 ? backward<Bf16>(a, st) : backward<F16>(a, st));
+    return status_of(f->dtype == MOE_BF16 ? backward<Bf16>(a, partial, st) : backward<F16>(a, partial, st));
 }
 
 }  // extern "C"
