@@ -401,6 +401,104 @@ __global__ __launch_bounds__(64 * WQ * WP) void ffn_join_kernel(FfnArgs a, Plan 
     finish<T, KIND, NI>(a, t, t.q0 + wq * TQ + 16 * j, wp * TP, v);
 }
 
+// Few rows (m <= 16 NT): GATEUP or DOWN with the weights read straight into registers, since
+// nothing would be read twice. A workgroup owns RT tiles of 16 weight rows (GATEUP: RT = 1,
+// eight rows of Wg and the same of Wu; RT = 2, sixteen of each); its W wavefronts split k, and
+// their sums are joined through LDS in wavefront order. A wavefront has AHEAD chunks of 32 k
+// of its weights and of x (from the L2s) in flight: each slot is requested anew as soon as it
+// has been multiplied.
+template <typename T, Kind KIND, int NT, int RT, int W, int AHEAD>
+__global__ __launch_bounds__(64 * W) void ffn_skinny_kernel(FfnArgs a) {
+    constexpr int RB = KIND == GATEUP ? 8 * RT : 16 * RT;   // output columns
+    extern __shared__ float red[];   // [W][RT][NT][256]
+    const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6, l16 = lane & 15, g = lane >> 4;
+    const int K = KIND == GATEUP ? a.D : a.I, N = KIND == GATEUP ? a.I : a.D, n0 = blockIdx.x * RB;
+    // chunk c of this wavefront: the wavefronts take pairs of chunks (whole lines) in turn
+    const int chunks = (K + 31) / 32, pairs = (chunks + 1) / 2, c0 = 0, c1 = 2 * ((pairs + W - 1 - wv) / W);
+    auto k_of = [&](int c) { return 32 * ((c >> 1) * 2 * W + 2 * wv + (c & 1)) + 8 * g; };
+    const uint16_t* w[RT];
+#pragma unroll
+    for (int r = 0; r < RT; ++r) {
+        const bool up = KIND == GATEUP && (RT == 1 ? l16 >= 8 : r == 1);
+        const int row = n0 + (KIND == GATEUP ? (RT == 1 ? l16 & 7 : l16) : 16 * r + l16);
+        w[r] = (KIND == DOWN ? a.wd : up ? a.wu : a.wg) + (size_t)min(row, N - 1) * K;
+    }
+    const int64_t ldx = KIND == GATEUP ? a.ldx : a.I;
+    const auto X = buffer_rsrc(KIND == GATEUP ? a.x : a.h, (uint32_t)((a.m - 1) * ldx + K) * 2);
+    uint32_t xoff[NT];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) xoff[t] = 16 * t + l16 < a.m ? (uint32_t)((16 * t + l16) * ldx) * 2 : PAST;
+
+    uint4 wq[AHEAD][RT], xq[AHEAD][NT];
+    auto request = [&](int i, int c) {
+        // past this wavefront's k, or past K: x reads as zeros
+        const int k = k_of(c);
+        const uint32_t off = c < c1 && k < K ? (uint32_t)k * 2 : PAST;
+#pragma unroll
+        for (int t = 0; t < NT; ++t) xq[i][t] = buffer_load16(X, off == PAST ? PAST : xoff[t] == PAST ? PAST : xoff[t] + off);
+#pragma unroll
+        for (int r = 0; r < RT; ++r) wq[i][r] = *reinterpret_cast<const uint4*>(w[r] + min(k_of(min(c, c1 - 1)), K - 8));
+    };
+    f32x4 acc[RT][NT];
+#pragma unroll
+    for (int r = 0; r < RT; ++r)
+#pragma unroll
+        for (int t = 0; t < NT; ++t) acc[r][t] = (f32x4){0.f, 0.f, 0.f, 0.f};
+    if (c0 < c1) {
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) request(i, c0 + i);
+    }
+    auto multiply = [&](int i, int c) {
+        // a weight that stands in for one past K must not bring a NaN
+        const uint32_t on = c < c1 && k_of(c) < K ? ~0u : 0u;
+#pragma unroll
+        for (int r = 0; r < RT; ++r) {
+            const u32x4 wm = {wq[i][r].x & on, wq[i][r].y & on, wq[i][r].z & on, wq[i][r].w & on};
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+                acc[r][t] = T::mfma(__builtin_bit_cast(s16x8, wm), __builtin_bit_cast(s16x8, xq[i][t]), acc[r][t]);
+        }
+    };
+    int c = c0;
+    for (; c + AHEAD < c1; c += AHEAD)
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) {
+            multiply(i, c + i);
+            request(i, c + AHEAD + i);
+        }
+    if (c0 < c1) {
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) multiply(i, c + i);
+    }
+    // a lane holds weight rows 4 g + 0..3 of token l16
+#pragma unroll
+    for (int r = 0; r < RT; ++r)
+#pragma unroll
+        for (int t = 0; t < NT; ++t) *reinterpret_cast<f32x4*>(&red[((wv * RT + r) * NT + t) * 256 + lane * 4]) = acc[r][t];
+    __syncthreads();
+    auto total = [&](int tok, int r, int row) {
+        float v = 0.f;
+#pragma unroll
+        for (int i = 0; i < W; ++i) v += red[((i * RT + r) * NT + (tok >> 4)) * 256 + ((row >> 2) * 16 + (tok & 15)) * 4 + (row & 3)];
+        return v;
+    };
+    for (int e = tid; e < a.m * RB; e += 64 * W) {
+        const int tok = e / RB, c = e % RB, n = n0 + c;
+        if (n >= N) continue;
+        if (KIND == GATEUP) {
+            const float gv = total(tok, 0, c), uv = RT == 1 ? total(tok, 0, c + 8) : total(tok, RT - 1, c);
+            if (a.saved != nullptr) {
+                float* s = a.saved + saved_at(tok >> 4, n >> 4, a.I) + (((n & 15) >> 2) * 16 + (tok & 15)) * 4 + (n & 3);
+                s[0] = gv;
+                s[256] = uv;
+            }
+            a.h[(size_t)tok * a.I + n] = T::store(act_value(clamp_gate(gv, a.limit), a.act) * clamp_up(uv, a.limit));
+        } else {
+            a.y[(size_t)tok * a.ldy + n] = T::store(total(tok, c >> 4, c & 15));
+        }
+    }
+}
+
 int cdiv(int a, int b) { return (a + b - 1) / b; }
 
 // Tiles of B x B, B = 256 (eight wavefronts, one workgroup per CU) or 128 (four, two per CU)
@@ -509,10 +607,37 @@ FfnArgs describe(const moe_ffn* f, int m) {
     return a;
 }
 
+template <typename T, Kind KIND, int NT, int RT, int W, int AHEAD>
+hipError_t launch_skinny(const FfnArgs& a, hipStream_t st) {
+    const int grid = KIND == GATEUP ? cdiv(a.I, 8 * RT) : cdiv(a.D, 16 * RT);
+    return launch_kernel(ffn_skinny_kernel<T, KIND, NT, RT, W, AHEAD>, dim3(grid), dim3(64 * W), sizeof(float) * W * RT * NT * 256, st, a);
+}
+
+// GATEUP or DOWN of the forward pass. Up to 16 rows: the skinny kernel (one row at 5120 x 2304:
+// 14.7 + 7.6 us, tiles 23 + 15). From 17 to 64 rows every workgroup of it reads all of x from
+// the L2s, which bounds it: it is taken where launches count more (up to 2M weights a matrix: 1024 x 1024
+// with 47 rows 13 against 23 us) and where two row tiles per workgroup still give every
+// second CU one (DOWN of 47 rows at 8192 x 2048: 15 against 17.7 us).
+template <typename T, Kind KIND>
+hipError_t launch_forward(const FfnArgs& a, float* partial, hipStream_t st) {
+    if (a.m <= 16) return launch_skinny<T, KIND, 1, 1, 8, 10>(a, st);
+    if (a.m <= 64 && (size_t)a.D * a.I <= (size_t)1 << 21) {
+        if (a.m <= 32) return launch_skinny<T, KIND, 2, 1, 8, 6>(a, st);
+        return a.m <= 48 ? launch_skinny<T, KIND, 3, 1, 8, 5>(a, st) : launch_skinny<T, KIND, 4, 1, 8, 4>(a, st);
+    }
+    if constexpr (KIND == DOWN) {
+        if (a.m <= 64 && a.D >= 4096) {
+            if (a.m <= 32) return launch_skinny<T, KIND, 2, 2, 8, 5>(a, st);
+            return a.m <= 48 ? launch_skinny<T, KIND, 3, 2, 8, 4>(a, st) : launch_skinny<T, KIND, 4, 2, 8, 4>(a, st);
+        }
+    }
+    return launch_product<T, KIND>(a, partial, st);
+}
+
 template <typename T>
 hipError_t forward(const FfnArgs& a, float* partial, hipStream_t st) {
-    const hipError_t e = launch_product<T, GATEUP>(a, partial, st);
-    return e != hipSuccess ? e : launch_product<T, DOWN>(a, partial, st);
+    const hipError_t e = launch_forward<T, GATEUP>(a, partial, st);
+    return e != hipSuccess ? e : launch_forward<T, DOWN>(a, partial, st);
 }
 
 template <typename T>
