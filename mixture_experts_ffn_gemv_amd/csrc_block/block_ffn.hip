@@ -401,63 +401,78 @@ __global__ __launch_bounds__(64 * WQ * WP) void ffn_join_kernel(FfnArgs a, Plan 
     finish<T, KIND, NI>(a, t, t.q0 + wq * TQ + 16 * j, wp * TP, v);
 }
 
-// Few rows (m <= 16 NT): GATEUP or DOWN with the weights read straight into registers, since
-// nothing would be read twice. A workgroup owns RT tiles of 16 weight rows (GATEUP: RT = 1,
-// eight rows of Wg and the same of Wu; RT = 2, sixteen of each); its W wavefronts split k, and
-// their sums are joined through LDS in wavefront order. A wavefront has AHEAD chunks of 32 k
-// of its weights and of x (from the L2s) in flight: each slot is requested anew as soon as it
-// has been multiplied.
-template <typename T, Kind KIND, int NT, int RT, int W, int AHEAD>
-__global__ __launch_bounds__(64 * W) void ffn_skinny_kernel(FfnArgs a) {
-    constexpr int RB = KIND == GATEUP ? 8 * RT : 16 * RT;   // output columns
-    extern __shared__ float red[];   // [W][RT][NT][256]
-    const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6, l16 = lane & 15, g = lane >> 4;
-    const int K = KIND == GATEUP ? a.D : a.I, N = KIND == GATEUP ? a.I : a.D, n0 = blockIdx.x * RB;
-    // chunk c of this wavefront: the wavefronts take pairs of chunks (whole lines) in turn
-    const int chunks = (K + 31) / 32, pairs = (chunks + 1) / 2, c0 = 0, c1 = 2 * ((pairs + W - 1 - wv) / W);
-    auto k_of = [&](int c) { return 32 * ((c >> 1) * 2 * W + 2 * wv + (c & 1)) + 8 * g; };
-    const uint16_t* w[RT];
+constexpr int SKINNY_WAVES = 8, SKINNY_LOADERS = 2, SKINNY_RING = 4;   // RING: slabs of x
+// The sums of a workgroup's eight wavefronts, acc[t] of tokens 16 t + l16 and weight rows 4 g +
+// 0..3, joined through LDS (which takes the place of x), and what is done with them
+template <typename T, Kind KIND, int NT, int THREADS>
+MOE_DEV void skinny_finish(const FfnArgs& a, float* red, int n0, const f32x4 (&acc)[NT]) {
+    constexpr int RB = KIND == GATEUP ? 8 : 16;
+    const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6, N = KIND == GATEUP ? a.I : a.D;
+    __syncthreads();
+    if (wv < SKINNY_WAVES) {
 #pragma unroll
-    for (int r = 0; r < RT; ++r) {
-        const bool up = KIND == GATEUP && (RT == 1 ? l16 >= 8 : r == 1);
-        const int row = n0 + (KIND == GATEUP ? (RT == 1 ? l16 & 7 : l16) : 16 * r + l16);
-        w[r] = (KIND == DOWN ? a.wd : up ? a.wu : a.wg) + (size_t)min(row, N - 1) * K;
+        for (int t = 0; t < NT; ++t) *reinterpret_cast<f32x4*>(&red[(wv * NT + t) * 256 + lane * 4]) = acc[t];
     }
-    const int64_t ldx = KIND == GATEUP ? a.ldx : a.I;
-    const auto X = buffer_rsrc(KIND == GATEUP ? a.x : a.h, (uint32_t)((a.m - 1) * ldx + K) * 2);
-    uint32_t xoff[NT];
+    __syncthreads();
+    auto total = [&](int tok, int r) {
+        float v = 0.f;
 #pragma unroll
-    for (int t = 0; t < NT; ++t) xoff[t] = 16 * t + l16 < a.m ? (uint32_t)((16 * t + l16) * ldx) * 2 : PAST;
-
-    uint4 wq[AHEAD][RT], xq[AHEAD][NT];
-    auto request = [&](int i, int c) {
-        // past this wavefront's k, or past K: x reads as zeros
-        const int k = k_of(c);
-        const uint32_t off = c < c1 && k < K ? (uint32_t)k * 2 : PAST;
-#pragma unroll
-        for (int t = 0; t < NT; ++t) xq[i][t] = buffer_load16(X, off == PAST ? PAST : xoff[t] == PAST ? PAST : xoff[t] + off);
-#pragma unroll
-        for (int r = 0; r < RT; ++r) wq[i][r] = *reinterpret_cast<const uint4*>(w[r] + min(k_of(min(c, c1 - 1)), K - 8));
+        for (int i = 0; i < SKINNY_WAVES; ++i) v += red[(i * NT + (tok >> 4)) * 256 + ((r >> 2) * 16 + (tok & 15)) * 4 + (r & 3)];
+        return v;
     };
-    f32x4 acc[RT][NT];
-#pragma unroll
-    for (int r = 0; r < RT; ++r)
-#pragma unroll
-        for (int t = 0; t < NT; ++t) acc[r][t] = (f32x4){0.f, 0.f, 0.f, 0.f};
-    if (c0 < c1) {
-#pragma unroll
-        for (int i = 0; i < AHEAD; ++i) request(i, c0 + i);
-    }
-    auto multiply = [&](int i, int c) {
-        // a weight that stands in for one past K must not bring a NaN
-        const uint32_t on = c < c1 && k_of(c) < K ? ~0u : 0u;
-#pragma unroll
-        for (int r = 0; r < RT; ++r) {
-            const u32x4 wm = {wq[i][r].x & on, wq[i][r].y & on, wq[i][r].z & on, wq[i][r].w & on};
-#pragma unroll
-            for (int t = 0; t < NT; ++t)
-                acc[r][t] = T::mfma(__builtin_bit_cast(s16x8, wm), __builtin_bit_cast(s16x8, xq[i][t]), acc[r][t]);
+    for (int e = tid; e < a.m * RB; e += THREADS) {
+        const int tok = e / RB, c = e % RB, n = n0 + c;
+        if (n >= N) continue;
+        if (KIND == GATEUP) {
+            const float gv = total(tok, c), uv = total(tok, c + 8);
+            if (a.saved != nullptr) {
+                float* s = a.saved + saved_at(tok >> 4, n >> 4, a.I) + (((n & 15) >> 2) * 16 + (tok & 15)) * 4 + (n & 3);
+                s[0] = gv;
+                s[256] = uv;
+            }
+            a.h[(size_t)tok * a.I + n] = T::store(act_value(clamp_gate(gv, a.limit), a.act) * clamp_up(uv, a.limit));
+        } else {
+            a.y[(size_t)tok * a.ldy + n] = T::store(total(tok, c));
         }
+    }
+}
+
+// The same for up to 16 rows whose x fits into LDS whole: one wait for it, and the wavefronts
+// then go their own ways through k, AHEAD chunks of 32 of their weights in flight
+constexpr size_t FEW_LDS = 64 << 10;
+MOE_DEV __host__ int few_row(int K) { return (K + 511) / 512 * 1024; }   // bytes of a token's row there
+template <typename T, Kind KIND>
+__global__ __launch_bounds__(64 * SKINNY_WAVES) void ffn_few_kernel(FfnArgs a) {
+    constexpr int RB = KIND == GATEUP ? 8 : 16, AHEAD = 5;
+    extern __shared__ __align__(16) uint8_t smem[];   // x; then sums [wavefront][256]
+    const int tid = threadIdx.x, lane = tid & 63, wv = __builtin_amdgcn_readfirstlane(tid >> 6), l16 = lane & 15, g = lane >> 4;
+    const int K = KIND == GATEUP ? a.D : a.I, N = KIND == GATEUP ? a.I : a.D, n0 = blockIdx.x * RB;
+    const int64_t ldx = KIND == GATEUP ? a.ldx : a.I;
+    const int row_bytes = few_row(K), runs = row_bytes / 1024;
+    const auto X = buffer_rsrc(KIND == GATEUP ? a.x : a.h, (uint32_t)((a.m - 1) * ldx + K) * 2);
+    for (int r = wv; r < a.m * runs; r += SKINNY_WAVES) {
+        // 16-byte chunk c of a token's row lies at c ^ (token & 15)
+        const int tok = r / runs, k = (r - tok * runs) * 512 + (lane ^ (tok & 15)) * 8;
+        buffer_load_lds16(X, smem + r * 1024, k < K ? (uint32_t)(tok * ldx + k) * 2 : PAST);
+    }
+    const int chunks = (K + 31) / 32, c0 = wv * chunks / SKINNY_WAVES, c1 = (wv + 1) * chunks / SKINNY_WAVES;
+    const int row = min(n0 + (l16 & (RB - 1)), N - 1);
+    const uint16_t* w = (KIND == DOWN ? a.wd : l16 < 8 ? a.wg : a.wu) + (size_t)row * K;
+    uint4 wq[AHEAD];
+    auto request = [&](int i, int c) { wq[i] = *reinterpret_cast<const uint4*>(w + min(32 * min(c, chunks - 1) + 8 * g, K - 8)); };
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) request(i, c0 + i);
+    wait_vm_loads<AHEAD>();   // this wavefront's part of x has landed
+    barrier_lds();
+    const int xt = min(l16, a.m - 1);   // (a token that does not exist reads another's; its sums are not used)
+    const uint8_t* x = smem + xt * row_bytes;
+    f32x4 acc[1] = {{0.f, 0.f, 0.f, 0.f}};
+    auto multiply = [&](int i, int c) {
+        // a weight that stands in for one past K, or past this wavefront's part, is not one
+        const uint32_t on = c < c1 && 32 * c + 8 * g < K ? ~0u : 0u;
+        const u32x4 wm = {wq[i].x & on, wq[i].y & on, wq[i].z & on, wq[i].w & on};
+        const int cx = min(c, chunks - 1) * 4 + g;
+        acc[0] = T::mfma(__builtin_bit_cast(s16x8, wm), *reinterpret_cast<const s16x8*>(x + ((cx ^ (xt & 15)) << 4)), acc[0]);
     };
     int c = c0;
     for (; c + AHEAD < c1; c += AHEAD)
@@ -466,37 +481,100 @@ __global__ __launch_bounds__(64 * W) void ffn_skinny_kernel(FfnArgs a) {
             multiply(i, c + i);
             request(i, c + AHEAD + i);
         }
-    if (c0 < c1) {
 #pragma unroll
-        for (int i = 0; i < AHEAD; ++i) multiply(i, c + i);
-    }
-    // a lane holds weight rows 4 g + 0..3 of token l16
+    for (int i = 0; i < AHEAD; ++i) multiply(i, c + i);
+    skinny_finish<T, KIND, 1, 64 * SKINNY_WAVES>(a, reinterpret_cast<float*>(smem), n0, acc);
+}
+
+// Few rows (m <= ROWS): GATEUP or DOWN with the weights read straight into registers, since
+// nothing would be read twice. A workgroup owns 16 weight rows (GATEUP: eight of Wg and the
+// same eight of Wu); eight wavefronts split every slab of KS k between them, and their sums
+// are joined through LDS in wavefront order. x comes into LDS a slab at a time, whole lines of
+// it (a load that gathers 16 rows takes about 90 cycles of a CU's load path, one of whole
+// lines 16, so that x straight from the L2s cost as much as the weights). Two wavefronts of
+// their own load it: loads complete in the order of a wavefront's requests, so that one which
+// waited for x would wait for every weight that it had requested before.
+constexpr int skinny_slab(int rows) { return rows <= 16 ? 512 : 256; }
+template <typename T, Kind KIND, int ROWS>
+__global__ __launch_bounds__(64 * (SKINNY_WAVES + SKINNY_LOADERS)) void ffn_skinny_kernel(FfnArgs a) {
+    constexpr int RB = KIND == GATEUP ? 8 : 16, NT = (ROWS + 15) / 16;   // RB: output columns
+    constexpr int KS = skinny_slab(ROWS), PER = KS / 32 / SKINNY_WAVES, ROW = KS * 2, RUN = 1024 / ROW;   // RUN: rows per load into LDS
+    constexpr int AHEAD = KS == 512 ? 5 : 8;   // slabs of weights in flight
+    extern __shared__ __align__(16) uint8_t smem[];   // RING slabs of x [token][KS]; then sums [wavefront][NT][256]
+    const int tid = threadIdx.x, lane = tid & 63, wv = __builtin_amdgcn_readfirstlane(tid >> 6), l16 = lane & 15, g = lane >> 4;
+    const int K = KIND == GATEUP ? a.D : a.I, N = KIND == GATEUP ? a.I : a.D, n0 = blockIdx.x * RB;
+    const int slabs = (K + KS - 1) / KS;
+    const int64_t ldx = KIND == GATEUP ? a.ldx : a.I;
+    f32x4 acc[NT];
 #pragma unroll
-    for (int r = 0; r < RT; ++r)
+    for (int t = 0; t < NT; ++t) acc[t] = (f32x4){0.f, 0.f, 0.f, 0.f};
+    if (wv >= SKINNY_WAVES) {
+        constexpr int LOADS = ROWS / RUN / SKINNY_LOADERS;   // of one loader and slab
+        const auto X = buffer_rsrc(KIND == GATEUP ? a.x : a.h, (uint32_t)((a.m - 1) * ldx + K) * 2);
+        const int in_run = lane / (64 / RUN), slot = lane % (64 / RUN);
+        auto stage = [&](int b) {   // (past the last slab, past m or K: zeros)
 #pragma unroll
-        for (int t = 0; t < NT; ++t) *reinterpret_cast<f32x4*>(&red[((wv * RT + r) * NT + t) * 256 + lane * 4]) = acc[r][t];
-    __syncthreads();
-    auto total = [&](int tok, int r, int row) {
-        float v = 0.f;
-#pragma unroll
-        for (int i = 0; i < W; ++i) v += red[((i * RT + r) * NT + (tok >> 4)) * 256 + ((row >> 2) * 16 + (tok & 15)) * 4 + (row & 3)];
-        return v;
-    };
-    for (int e = tid; e < a.m * RB; e += 64 * W) {
-        const int tok = e / RB, c = e % RB, n = n0 + c;
-        if (n >= N) continue;
-        if (KIND == GATEUP) {
-            const float gv = total(tok, 0, c), uv = RT == 1 ? total(tok, 0, c + 8) : total(tok, RT - 1, c);
-            if (a.saved != nullptr) {
-                float* s = a.saved + saved_at(tok >> 4, n >> 4, a.I) + (((n & 15) >> 2) * 16 + (tok & 15)) * 4 + (n & 3);
-                s[0] = gv;
-                s[256] = uv;
+            for (int i = 0; i < LOADS; ++i) {
+                const int r = ((wv - SKINNY_WAVES) * LOADS + i) * RUN, tok = r + in_run;
+                // 16-byte chunk c of a token's row lies at c ^ (token & 15)
+                const int k = b * KS + (slot ^ (tok & 15)) * 8;
+                buffer_load_lds16(X, smem + (b % SKINNY_RING * ROWS + r) * ROW, tok < a.m && k < K ? (uint32_t)(tok * ldx + k) * 2 : PAST);
             }
-            a.h[(size_t)tok * a.I + n] = T::store(act_value(clamp_gate(gv, a.limit), a.act) * clamp_up(uv, a.limit));
-        } else {
-            a.y[(size_t)tok * a.ldy + n] = T::store(total(tok, c >> 4, c & 15));
+        };
+#pragma unroll
+        for (int b = 0; b < SKINNY_RING - 1; ++b) stage(b);
+        for (int b = 0; b < slabs; ++b) {
+            wait_vm_loads<(SKINNY_RING - 2) * LOADS>();   // slab b has landed
+            barrier_lds();                                // every wavefront is done with slab b - 1
+            stage(b + SKINNY_RING - 1);
         }
+        wait_vm_loads<0>();
+    } else {
+        const int row = min(n0 + (l16 & (RB - 1)), N - 1);
+        const uint16_t* w = (KIND == DOWN ? a.wd : l16 < 8 ? a.wg : a.wu) + (size_t)row * K;
+        auto k_of = [&](int b, int i) { return b * KS + (wv * PER + i) * 32 + 8 * g; };
+        uint4 wq[AHEAD][PER];
+        auto request = [&](int at, int b) {
+#pragma unroll
+            for (int i = 0; i < PER; ++i) wq[at][i] = *reinterpret_cast<const uint4*>(w + min(k_of(b, i), K - 8));
+        };
+        int xrow[NT];   // this lane's token rows
+#pragma unroll
+        for (int t = 0; t < NT; ++t) xrow[t] = min(16 * t + l16, ROWS - 1);
+        auto slab = [&](int at, int b) {
+            barrier_lds();   // slab b of x has landed
+            const uint8_t* x = smem + b % SKINNY_RING * ROWS * ROW;
+#pragma unroll
+            for (int i = 0; i < PER; ++i) {
+                // (a weight past K is another of its row: x is zero there, but a NaN must not come in)
+                const uint32_t on = k_of(b, i) < K ? ~0u : 0u;
+                const u32x4 wm = {wq[at][i].x & on, wq[at][i].y & on, wq[at][i].z & on, wq[at][i].w & on};
+#pragma unroll
+                for (int t = 0; t < NT; ++t) {
+                    const int c = (wv * PER + i) * 4 + g;
+                    const s16x8 xv = *reinterpret_cast<const s16x8*>(x + xrow[t] * ROW + ((c ^ (xrow[t] & 15)) << 4));
+                    acc[t] = T::mfma(__builtin_bit_cast(s16x8, wm), xv, acc[t]);
+                }
+            }
+        };
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) request(i, min(i, slabs - 1));
+        int b = 0;
+        for (; b + 2 * AHEAD <= slabs; b += AHEAD)
+#pragma unroll
+            for (int i = 0; i < AHEAD; ++i) {
+                slab(i, b + i);
+                request(i, b + AHEAD + i);
+            }
+        for (; b < slabs; b += AHEAD)
+#pragma unroll
+            for (int i = 0; i < AHEAD; ++i)
+                if (b + i < slabs) {
+                    slab(i, b + i);
+                    if (b + AHEAD + i < slabs) request(i, b + AHEAD + i);
+                }
     }
+    skinny_finish<T, KIND, NT, 64 * (SKINNY_WAVES + SKINNY_LOADERS)>(a, reinterpret_cast<float*>(smem), n0, acc);
 }
 
 int cdiv(int a, int b) { return (a + b - 1) / b; }
@@ -607,30 +685,24 @@ FfnArgs describe(const moe_ffn* f, int m) {
     return a;
 }
 
-template <typename T, Kind KIND, int NT, int RT, int W, int AHEAD>
+template <typename T, Kind KIND, int ROWS>
 hipError_t launch_skinny(const FfnArgs& a, hipStream_t st) {
-    const int grid = KIND == GATEUP ? cdiv(a.I, 8 * RT) : cdiv(a.D, 16 * RT);
-    return launch_kernel(ffn_skinny_kernel<T, KIND, NT, RT, W, AHEAD>, dim3(grid), dim3(64 * W), sizeof(float) * W * RT * NT * 256, st, a);
+    const size_t lds = std::max<size_t>(SKINNY_RING * ROWS * skinny_slab(ROWS) * 2, sizeof(float) * SKINNY_WAVES * cdiv(ROWS, 16) * 256);
+    return launch_kernel(ffn_skinny_kernel<T, KIND, ROWS>, dim3(KIND == GATEUP ? cdiv(a.I, 8) : cdiv(a.D, 16)),
+                         dim3(64 * (SKINNY_WAVES + SKINNY_LOADERS)), lds, st, a);
 }
 
-// GATEUP or DOWN of the forward pass. Up to 16 rows: the skinny kernel (one row at 5120 x 2304:
-// 14.7 + 7.6 us, tiles 23 + 15). From 17 to 64 rows every workgroup of it reads all of x from
-// the L2s, which bounds it: it is taken where launches count more (up to 2M weights a matrix: 1024 x 1024
-// with 47 rows 13 against 23 us) and where two row tiles per workgroup still give every
-// second CU one (DOWN of 47 rows at 8192 x 2048: 15 against 17.7 us).
+// GATEUP or DOWN of the forward pass
 template <typename T, Kind KIND>
 hipError_t launch_forward(const FfnArgs& a, float* partial, hipStream_t st) {
-    if (a.m <= 16) return launch_skinny<T, KIND, 1, 1, 8, 10>(a, st);
-    if (a.m <= 64 && (size_t)a.D * a.I <= (size_t)1 << 21) {
-        if (a.m <= 32) return launch_skinny<T, KIND, 2, 1, 8, 6>(a, st);
-        return a.m <= 48 ? launch_skinny<T, KIND, 3, 1, 8, 5>(a, st) : launch_skinny<T, KIND, 4, 1, 8, 4>(a, st);
+    if (a.m <= 16 && a.m * (size_t)few_row(KIND == GATEUP ? a.D : a.I) <= FEW_LDS) {
+        const size_t lds = std::max<size_t>(a.m * (size_t)few_row(KIND == GATEUP ? a.D : a.I), sizeof(float) * SKINNY_WAVES * 256);
+        return launch_kernel(ffn_few_kernel<T, KIND>, dim3(KIND == GATEUP ? cdiv(a.I, 8) : cdiv(a.D, 16)), dim3(64 * SKINNY_WAVES), lds, st, a);
     }
-    if constexpr (KIND == DOWN) {
-        if (a.m <= 64 && a.D >= 4096) {
-            if (a.m <= 32) return launch_skinny<T, KIND, 2, 2, 8, 5>(a, st);
-            return a.m <= 48 ? launch_skinny<T, KIND, 3, 2, 8, 4>(a, st) : launch_skinny<T, KIND, 4, 2, 8, 4>(a, st);
-        }
-    }
+    if (a.m <= 16) return launch_skinny<T, KIND, 16>(a, st);
+    if (a.m <= 32) return launch_skinny<T, KIND, 32>(a, st);
+    if (a.m <= 48) return launch_skinny<T, KIND, 48>(a, st);
+    if (a.m <= 64) return launch_skinny<T, KIND, 64>(a, st);
     return launch_product<T, KIND>(a, partial, st);
 }
 
