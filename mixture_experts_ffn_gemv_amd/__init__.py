@@ -230,8 +230,14 @@ def _ptr(t):
     return t.data_ptr()
 
 
+# the current stream's handle without a Stream object around it (0.3 against 2.6 us a call)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream):
     if stream is None:
+        if _raw_stream is not None:
+            return _raw_stream(torch.cuda.current_device())
         return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
     if isinstance(stream, int):
         return ctypes.c_void_p(stream)
@@ -396,7 +402,7 @@ def _rows(t, m, dim, dtype, where):
     """A device matrix [m, dim] with consecutive values in each row -> (pointer, row stride); None -> (None, 0)."""
     if t is None:
         return None, 0
-    if not t.is_cuda or t.dtype is not dtype or t.shape != (m, dim):
+    if t.shape != (m, dim) or t.dtype is not dtype or not t.is_cuda:
         raise MoeError(MOE_EINVAL, where)
     ld, one = t.stride()
     if one != 1 and dim != 1:
