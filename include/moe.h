@@ -476,7 +476,8 @@ int moe_w4_matmul(const moe_w4* w, const void* x, int64_t ldx, int32_t m, void* 
 
 /* h [m, N] = act(gc) uc of g = x Wg^T and u = x Wu^T, clamped as in moe_ffn, in one
  * launch: the first half of the gated block with 4-bit weights (moe_w4_matmul is
- * the second). Wg and Wu have the same rows, cols, group and dtype. */
+ * the second). Wg and Wu have the same rows, cols, group and dtype, and both or neither
+ * have zero points. */
 int moe_w4_gated(const moe_w4* w_gate, const moe_w4* w_up, int32_t act, float limit, const void* x, int64_t ldx,
                  int32_t m, void* h, int64_t ldh, void* stream);
 

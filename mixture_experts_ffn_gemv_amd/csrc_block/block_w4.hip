@@ -10,24 +10,23 @@
 // with ones, in the layout in which it is needed. Scale and zero point are applied
 // in f32 to each group's sum, so that w is never rounded.
 //
-// A workgroup owns 16 rows of W (of both matrices, when gated) and up to 64 rows of
-// x; its wavefronts split the columns, and their sums are joined through LDS in
-// wavefront order. A wavefront takes 128 columns at a time: lane (r = lane % 16,
-// g = lane / 16) loads the 16 bytes of row r, columns 32 g .. 32 g + 31, and four
-// lane-group swaps turn these so that its word j holds columns 32 j + 8 g .. + 7:
-// each matrix instruction then covers 32 consecutive columns, one group or part of
-// one. x is the instruction's first operand, W the second, so that a lane's results
-// all belong to row r, whose scales it holds. Row t of x sits at operand row
-// 4 (t % 4) + t / 4: up to four tokens then leave one result per lane, up to eight
-// two.
+// A workgroup owns RT tiles of 16 rows of W (gated: eight rows of Wg and the same eight of
+// Wu in a tile) and up to 64 rows of x; its wavefronts split the columns, and their sums are
+// joined through LDS in wavefront order. A wavefront takes stages of 128 columns, the
+// next one in flight: lane (r = lane % 16, g = lane / 16) loads the 16 bytes of row r,
+// columns 32 g .. 32 g + 31, and four lane-group swaps turn these so that its word j holds
+// columns 32 j + 8 g .. + 7: each matrix instruction then covers 32 consecutive columns,
+// one group or part of one. x is the instruction's first operand, W the second, so that a
+// lane's results all belong to row r, whose scales it needs. Row t of x sits at operand row
+// 4 (t % 4) + t / 4: up to eight tokens then leave two results per lane instead of four.
+// Scales and zero points come eight stages at a time, in pieces of eight groups, and wait
+// in LDS: loaded stage by stage they were half the time of a wide matrix.
 #include "block_common.h"
 
 namespace moe {
 namespace {
 
 constexpr int STAGE = 128;       // columns a wavefront takes at a time
-constexpr int BATCH = 4;         // stages requested together, one batch ahead
-constexpr int MAX_WAVES = 8;
 constexpr int MAX_ROWS_X = 64;   // rows of x per workgroup
 
 struct W4Mat {
@@ -44,27 +43,26 @@ struct W4Args {
     float limit;
 };
 
+// (a & mask) | c in one instruction: the mask has to be in a vector register
+MOE_DEV uint32_t and_or(uint32_t a, uint32_t mask, uint32_t c) {
+    asm("" : "+v"(mask));
+    return (a & mask) | c;
+}
 // word of eight codes -> the eight values c + q as 16-bit floats, in column order
 MOE_DEV s16x8 codes_to_values(uint32_t w, Bf16) {
     // halves (nibbles 0..3 | nibbles 1..4) and (4..7 | 5..8) of the word
     const uint32_t v = w >> 4;
     const uint32_t p = __builtin_amdgcn_perm(v, w, 0x05040100u), q = __builtin_amdgcn_perm(v, w, 0x07060302u);
-    u32x4 o;
-    o[0] = (p & 0x000F000Fu) | 0x43004300u;
-    o[1] = ((p >> 8) & 0x000F000Fu) | 0x43004300u;
-    o[2] = (q & 0x000F000Fu) | 0x43004300u;
-    o[3] = ((q >> 8) & 0x000F000Fu) | 0x43004300u;
+    const u32x4 o = {and_or(p, 0x000F000Fu, 0x43004300u), and_or(p >> 8, 0x000F000Fu, 0x43004300u),
+                     and_or(q, 0x000F000Fu, 0x43004300u), and_or(q >> 8, 0x000F000Fu, 0x43004300u)};
     return __builtin_bit_cast(s16x8, o);
 }
 MOE_DEV s16x8 codes_to_values(uint32_t w, F16) {
     // as above, each code in bits 4..7: 64 + q
     const uint32_t v = w << 4;
     const uint32_t p = __builtin_amdgcn_perm(w, v, 0x05040100u), q = __builtin_amdgcn_perm(w, v, 0x07060302u);
-    u32x4 o;
-    o[0] = (p & 0x00F000F0u) | 0x54005400u;
-    o[1] = ((p >> 8) & 0x00F000F0u) | 0x54005400u;
-    o[2] = (q & 0x00F000F0u) | 0x54005400u;
-    o[3] = ((q >> 8) & 0x00F000F0u) | 0x54005400u;
+    const u32x4 o = {and_or(p, 0x00F000F0u, 0x54005400u), and_or(p >> 8, 0x00F000F0u, 0x54005400u),
+                     and_or(q, 0x00F000F0u, 0x54005400u), and_or(q >> 8, 0x00F000F0u, 0x54005400u)};
     return __builtin_bit_cast(s16x8, o);
 }
 template <typename T>
@@ -83,151 +81,175 @@ MOE_DEV void turn_words(uint32_t* w) {
     w[0] = c[0], w[1] = c[1], w[2] = d[0], w[3] = d[1];
 }
 
-// One wavefront's 128 columns of one matrix: 16 code bytes, and the scales and zero
-// points of row r's groups there.
-template <int G>
-struct W4Stage {
-    static constexpr int NG = STAGE / G;
-    uint32_t c[4];
-    uint16_t s[NG];
-    uint8_t z[NG];
+// One wavefront's scales and zero points of a tile for SLAB stages: row r's at r * NG * SLAB
+constexpr int SLAB = 8;
+template <int NG>
+struct SlabTile {
+    uint16_t s[16 * NG * SLAB];
+    uint8_t z[16 * NG * SLAB];
 };
 
-// NT: tiles of 16 rows of x. IR: results per lane and tile (tokens g + 4 i, i < IR). NM: matrices (2: gated)
-template <typename T, int G, int NT, int IR, int NM>
-__global__ __launch_bounds__(64 * MAX_WAVES) void w4_kernel(W4Args a) {
-    extern __shared__ float red[];   // [wavefront][matrix][token][16 rows]
-    constexpr int NG = STAGE / G, TOK = 16 * NT;
+// NT: tiles of 16 rows of x. IR: results per lane and tile (tokens g + 4 i, i < IR). RT: tiles of W. WAVES: the most wavefronts
+template <typename T, int G, int NT, int IR, int RT, bool GATED, int WAVES, int AHEAD>
+__global__ __launch_bounds__(64 * WAVES) void w4_kernel(W4Args a) {
+    constexpr int NG = STAGE / G, TOK = 16 * NT, COLS = GATED ? 8 : 16;   // COLS: results per token and tile
+    extern __shared__ __align__(16) uint8_t smem[];   // slabs [wavefront][tile]; then sums [wavefront][tile][token][16 rows]
     const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6, nw = blockDim.x >> 6;
     const int r = lane & 15, g = lane >> 4;
-    const int n0 = blockIdx.x * 16, rows = min(16, a.N - n0);
+    const int n0 = blockIdx.x * COLS * RT;
     const int t0 = blockIdx.y * MAX_ROWS_X, mt = min(MAX_ROWS_X, a.m - t0);
-    const int row = n0 + min(r, rows - 1);
     const int kg = a.K / G;
     const int stages = (a.K + STAGE - 1) / STAGE;
     const int s0 = (int)((int64_t)wv * stages / nw), s1 = (int)((int64_t)(wv + 1) * stages / nw);
     const uint32_t row_bytes = (uint32_t)a.K / 2;
-    __amdgpu_buffer_rsrc_t codes[NM];
+    // row r of tile t: its matrix, and its number there (past the matrix: the last row)
+    auto matrix = [&](int r) { return GATED && r >= 8 ? 1 : 0; };
+    auto row_of = [&](int t, int r) { return min(n0 + COLS * t + (GATED ? r & 7 : r), a.N - 1); };
+    const uint8_t* codes[RT];
 #pragma unroll
-    for (int q = 0; q < NM; ++q) codes[q] = buffer_rsrc(a.w[q].codes + (size_t)n0 * row_bytes, rows * row_bytes);
+    for (int t = 0; t < RT; ++t) codes[t] = a.w[matrix(r)].codes + (size_t)row_of(t, r) * row_bytes;
     const auto X = buffer_rsrc(a.x + (size_t)t0 * a.ldx, (uint32_t)((mt - 1) * a.ldx + a.K) * 2);
-    constexpr uint32_t PAST = 0xFFFFFFF0u;   // an offset past every buffer: zeros
+    constexpr uint32_t PAST = 0xFFFFFFF0u;   // an offset past the buffer: zeros
     uint32_t xoff[NT];
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
         const int tok = 16 * t + (r >> 2) + 4 * (r & 3);
         xoff[t] = tok < mt ? (uint32_t)(tok * a.ldx * 2) : PAST;
     }
+    const bool zeros = a.w[0].zeros != nullptr;   // (of both matrices or of neither)
+    SlabTile<NG>* const slab = reinterpret_cast<SlabTile<NG>*>(smem) + wv * RT;
 
-    auto load = [&](W4Stage<G>(&st)[BATCH][NM], int s) {
+    // Stages s .. s + SLAB - 1: piece lane % NG of row lane / NG, eight groups each. A piece that
+    // would pass the row's end is read from its last eight groups and moved down.
+    auto load_slab = [&](int s) {
+        const int row = lane / NG, piece = lane % NG, first = s * NG + 8 * piece;
+        if (lane >= 16 * NG) return;
 #pragma unroll
-        for (int b = 0; b < BATCH; ++b) {
-            const bool in = s + b < s1;
-            const uint32_t k = (s + b) * STAGE;
-#pragma unroll
-            for (int q = 0; q < NM; ++q) {
-                const uint32_t off = in && k + 32 * g < (uint32_t)a.K && r < rows ? r * row_bytes + k / 2 + 16 * g : PAST;
-                const uint4 v = buffer_load16(codes[q], off);
-                st[b][q].c[0] = v.x, st[b][q].c[1] = v.y, st[b][q].c[2] = v.z, st[b][q].c[3] = v.w;
-                const size_t at = (size_t)row * kg + (s + b) * NG;
-                if (in && (int)k + STAGE <= a.K) {
-                    __builtin_memcpy(st[b][q].s, a.w[q].scales + at, sizeof(st[b][q].s));
-                    if (a.w[q].zeros != nullptr) __builtin_memcpy(st[b][q].z, a.w[q].zeros + at, sizeof(st[b][q].z));
-                } else if (in) {
-                    for (int i = 0; i < NG; ++i) {
-                        const bool have = (s + b) * NG + i < kg;
-                        st[b][q].s[i] = have ? a.w[q].scales[at + i] : 0;
-                        if (a.w[q].zeros != nullptr) st[b][q].z[i] = have ? a.w[q].zeros[at + i] : 0;
+        for (int t = 0; t < RT; ++t) {
+            const W4Mat& w = a.w[matrix(row)];
+            const size_t at = (size_t)row_of(t, row) * kg;
+            unsigned __int128 sc = 0;
+            uint64_t zp = 0;
+            if (first < kg) {
+                if (kg >= 8) {
+                    const int from = min(first, kg - 8), down = first - from;
+                    __builtin_memcpy(&sc, w.scales + at + from, 16);
+                    sc >>= 16 * down;
+                    if (zeros) __builtin_memcpy(&zp, w.zeros + at + from, 8);
+                    zp >>= 8 * down;
+                } else {
+                    for (int i = first; i < kg; ++i) {
+                        sc |= (unsigned __int128)w.scales[at + i] << (16 * (i - first));
+                        if (zeros) zp |= (uint64_t)w.zeros[at + i] << (8 * (i - first));
                     }
                 }
             }
+            *reinterpret_cast<unsigned __int128*>(slab[t].s + (row * NG + piece) * 8) = sc;
+            *reinterpret_cast<uint64_t*>(slab[t].z + (row * NG + piece) * 8) = zp;
         }
     };
 
-    float sum[NM][NT][IR];
+    struct Stage {
+        uint4 x[4][NT], c[RT];
+    } st[AHEAD + 1];
+    auto request = [&](Stage& q, int s) {
+        const int k = min(s, s1 - 1) * STAGE, end = s < s1 ? a.K : 0;
+        // columns past K: x reads as zeros, and finite codes stand in for the missing ones
 #pragma unroll
-    for (int q = 0; q < NM; ++q)
+        for (int t = 0; t < RT; ++t) q.c[t] = *reinterpret_cast<const uint4*>(codes[t] + min((uint32_t)(k / 2 + 16 * g), row_bytes - 16));
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+                const int kx = k + 32 * j + 8 * g;
+                q.x[j][t] = buffer_load16(X, kx < end && xoff[t] != PAST ? xoff[t] + 2 * kx : PAST);
+            }
+    };
+
+    float sum[RT][NT][IR];
+#pragma unroll
+    for (int q = 0; q < RT; ++q)
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
             for (int i = 0; i < IR; ++i) sum[q][t][i] = 0.f;
     const s16x8 ones = __builtin_bit_cast(s16x8, (u32x4){T::ONES, T::ONES, T::ONES, T::ONES});
 
-    auto work = [&](W4Stage<G>(&st)[BATCH][NM], int s) {
+    auto work = [&](Stage& q, int in) {   // in: the stage's place in the slab
+        f32x4 acc[RT][NT], sx[NT];
+        uint32_t c[RT][4];
+        float sc[RT][NG], zp[RT][NG];
 #pragma unroll
-        for (int b = 0; b < BATCH; ++b) {
-            if (s + b >= s1) break;
-            const uint32_t k = (s + b) * STAGE + 8 * g;
+        for (int t = 0; t < RT; ++t) {
+            c[t][0] = q.c[t].x, c[t][1] = q.c[t].y, c[t][2] = q.c[t].z, c[t][3] = q.c[t].w;
+            turn_words(c[t]);
 #pragma unroll
-            for (int q = 0; q < NM; ++q) turn_words(st[b][q].c);
-            f32x4 acc[NM][NT], sx[NT];
+            for (int i = 0; i < NG; ++i) {
+                const int at = (r * SLAB + in) * NG + i;
+                sc[t][i] = T::load(slab[t].s[at]);
+                zp[t][i] = code_offset<T>() + (zeros ? (float)slab[t].z[at] : 8.f);
+            }
+        }
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                s16x8 xv[NT], wv8[NM];
+        for (int j = 0; j < 4; ++j) {
+            const bool first = (32 * j) % G == 0, last = (32 * (j + 1)) % G == 0;
+            const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                for (int t = 0; t < NT; ++t) {
-                    const uint32_t off = xoff[t] != PAST && k + 32 * j < (uint32_t)a.K ? xoff[t] + 2 * (k + 32 * j) : PAST;
-                    const uint4 v = buffer_load16(X, off);
-                    xv[t] = __builtin_bit_cast(s16x8, v);
-                }
+            for (int t = 0; t < NT; ++t) sx[t] = T::mfma(__builtin_bit_cast(s16x8, q.x[j][t]), ones, first ? zero : sx[t]);
 #pragma unroll
-                for (int q = 0; q < NM; ++q) wv8[q] = codes_to_values(st[b][q].c[j], T());
-                const bool first = (32 * j) % G == 0, last = (32 * (j + 1)) % G == 0;
-                const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
+            for (int w = 0; w < RT; ++w) {
+                const s16x8 v = codes_to_values(c[w][j], T());
 #pragma unroll
-                for (int t = 0; t < NT; ++t) {
-                    sx[t] = T::mfma(xv[t], ones, first ? zero : sx[t]);
+                for (int t = 0; t < NT; ++t) acc[w][t] = T::mfma(__builtin_bit_cast(s16x8, q.x[j][t]), v, first ? zero : acc[w][t]);
+            }
+            if (last) {
+                const int i0 = 32 * j / G;
 #pragma unroll
-                    for (int q = 0; q < NM; ++q) acc[q][t] = T::mfma(xv[t], wv8[q], first ? zero : acc[q][t]);
-                }
-                if (last) {
-                    const int i0 = 32 * j / G;
+                for (int w = 0; w < RT; ++w)
 #pragma unroll
-                    for (int q = 0; q < NM; ++q) {
-                        const float sc = T::load(st[b][q].s[i0]);
-                        const float zp = code_offset<T>() + (a.w[q].zeros != nullptr ? (float)st[b][q].z[i0] : 8.f);
+                    for (int t = 0; t < NT; ++t)
 #pragma unroll
-                        for (int t = 0; t < NT; ++t)
-#pragma unroll
-                            for (int i = 0; i < IR; ++i)
-                                sum[q][t][i] = fmaf(sc, fmaf(-zp, sx[t][i], acc[q][t][i]), sum[q][t][i]);
-                    }
-                }
+                        for (int i = 0; i < IR; ++i)
+                            sum[w][t][i] = fmaf(sc[w][i0], fmaf(-zp[w][i0], sx[t][i], acc[w][t][i]), sum[w][t][i]);
             }
         }
     };
-
-    W4Stage<G> cur[BATCH][NM], nxt[BATCH][NM];
-    load(cur, s0);
-    for (int s = s0; s < s1; s += BATCH) {
-        if (s + BATCH < s1) load(nxt, s + BATCH);
-        work(cur, s);
+    // one instance of the loop's body, the stages in flight handed down in registers: unrolled
+    // over them, these short kernels spent more time on fetching their instructions
+    request(st[0], s0);
+    load_slab(s0);
 #pragma unroll
-        for (int b = 0; b < BATCH; ++b)
+    for (int i = 1; i < AHEAD; ++i) request(st[i], s0 + i);
+    int in = 0;
+#pragma unroll 1
+    for (int s = s0; s < s1; ++s) {
+        request(st[AHEAD], s + AHEAD);
+        work(st[0], in);
 #pragma unroll
-            for (int q = 0; q < NM; ++q) cur[b][q] = nxt[b][q];
+        for (int i = 0; i < AHEAD; ++i) st[i] = st[i + 1];
+        if (++in == SLAB && s + 1 < s1) load_slab(s + 1), in = 0;
     }
 
+    __syncthreads();   // the sums take the slabs' place
+    float* const red = reinterpret_cast<float*>(smem);
 #pragma unroll
-    for (int q = 0; q < NM; ++q)
+    for (int q = 0; q < RT; ++q)
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
-            for (int i = 0; i < IR; ++i)
-                red[((wv * NM + q) * TOK + 16 * t + g + 4 * i) * 16 + r] = sum[q][t][i];
+            for (int i = 0; i < IR; ++i) red[((wv * RT + q) * TOK + 16 * t + g + 4 * i) * 16 + r] = sum[q][t][i];
     __syncthreads();
-    for (int e = threadIdx.x; e < mt * 16; e += blockDim.x) {
-        const int tok = e >> 4, rr = e & 15;
-        if (rr >= rows) continue;
-        float v[NM];
-#pragma unroll
-        for (int q = 0; q < NM; ++q) {
-            v[q] = 0.f;
-            for (int w = 0; w < nw; ++w) v[q] += red[((w * NM + q) * TOK + tok) * 16 + rr];
+    for (int e = threadIdx.x; e < mt * COLS * RT; e += blockDim.x) {
+        const int c = e % COLS, tile = e / COLS % RT, tok = e / (COLS * RT), n = n0 + COLS * tile + c;
+        if (n >= a.N) continue;
+        float v[2] = {0.f, 0.f};
+        for (int w = 0; w < nw; ++w) {
+            const float* p = red + ((w * RT + tile) * TOK + tok) * 16 + c;
+            v[0] += p[0];
+            if (GATED) v[1] += p[8];
         }
-        float o = v[0];
-        if (NM == 2) o = act_value(clamp_gate(v[0], a.limit), a.act) * clamp_up(v[NM - 1], a.limit);
-        a.y[(size_t)(t0 + tok) * a.ldy + n0 + rr] = T::store(o);
+        const float o = GATED ? act_value(clamp_gate(v[0], a.limit), a.act) * clamp_up(v[1], a.limit) : v[0];
+        a.y[(size_t)(t0 + tok) * a.ldy + n] = T::store(o);
     }
 }
 
@@ -240,19 +262,23 @@ int check_w4(const moe_w4* w) {
     return MOE_OK;
 }
 
-template <typename T, int G, int NM>
+template <typename T, int G, int NT, int IR, int RT, bool GATED, int WAVES, int AHEAD>
+hipError_t launch_tiles(const W4Args& a, hipStream_t st) {
+    const int nw = std::min(WAVES, (a.K + STAGE - 1) / STAGE);   // (every wavefront has a stage)
+    const int cols = (GATED ? 8 : 16) * RT;
+    const dim3 grid((a.N + cols - 1) / cols, (a.m + MAX_ROWS_X - 1) / MAX_ROWS_X);
+    const size_t lds = nw * RT * std::max(sizeof(SlabTile<STAGE / G>), sizeof(float) * NT * 256);
+    return launch_kernel(w4_kernel<T, G, NT, IR, RT, GATED, WAVES, AHEAD>, grid, dim3(64 * nw), lds, st, a);
+}
+
+template <typename T, int G, bool GATED>
 hipError_t launch_w4(const W4Args& a, hipStream_t st) {
-    const int stages = (a.K + STAGE - 1) / STAGE, nw = std::min(MAX_WAVES, stages);
     const int mt = std::min(a.m, MAX_ROWS_X);
-    const dim3 grid((a.N + 15) / 16, (a.m + MAX_ROWS_X - 1) / MAX_ROWS_X);
-    const int nt = mt <= 16 ? 1 : mt <= 32 ? 2 : 4;
-    const size_t lds = sizeof(float) * nw * NM * nt * 256;
-    void (*k)(W4Args) = mt <= 4    ? w4_kernel<T, G, 1, 1, NM>
-                        : mt <= 8  ? w4_kernel<T, G, 1, 2, NM>
-                        : mt <= 16 ? w4_kernel<T, G, 1, 4, NM>
-                        : mt <= 32 ? w4_kernel<T, G, 2, 4, NM>
-                                   : w4_kernel<T, G, 4, 4, NM>;
-    return launch_kernel(k, grid, dim3(64 * nw), lds, st, a);
+    if (mt <= 8) return launch_tiles<T, G, 1, 2, 1, GATED, 8, 2>(a, st);
+    if (mt <= 16) return launch_tiles<T, G, 1, 4, 1, GATED, 8, 2>(a, st);
+    const bool many = a.N >= (GATED ? 8192 : 16384);
+    if (mt <= 32) return many ? launch_tiles<T, G, 2, 4, 4, GATED, 8, 1>(a, st) : launch_tiles<T, G, 2, 4, 1, GATED, 8, 1>(a, st);
+    return many ? launch_tiles<T, G, 4, 4, 2, GATED, 8, 1>(a, st) : launch_tiles<T, G, 4, 4, 1, GATED, 8, 1>(a, st);
 }
 
 template <int NM>
@@ -263,6 +289,7 @@ int run_w4(const moe_w4* const* w, int act, float limit, const void* x, int64_t 
     if (NM == 2) {
         if (w[0]->rows != w[1]->rows || w[0]->cols != w[1]->cols || w[0]->group != w[1]->group || w[0]->dtype != w[1]->dtype)
             return MOE_EINVAL;
+        if ((w[0]->zeros == nullptr) != (w[1]->zeros == nullptr)) return MOE_EINVAL;
         if ((act != MOE_ACT_SILU && act != MOE_ACT_GELU) || limit != limit) return MOE_EINVAL;
     }
     if (m < 0 || m > MAX_ROWS_X * 65535) return MOE_EINVAL;
@@ -279,8 +306,8 @@ int run_w4(const moe_w4* const* w, int act, float limit, const void* x, int64_t 
     const hipStream_t st = (hipStream_t)stream;
     const int g = w[0]->group;
     if (w[0]->dtype == MOE_BF16)
-        return status_of(g == 32 ? launch_w4<Bf16, 32, NM>(a, st) : g == 64 ? launch_w4<Bf16, 64, NM>(a, st) : launch_w4<Bf16, 128, NM>(a, st));
-    return status_of(g == 32 ? launch_w4<F16, 32, NM>(a, st) : g == 64 ? launch_w4<F16, 64, NM>(a, st) : launch_w4<F16, 128, NM>(a, st));
+        return status_of(g == 32 ? launch_w4<Bf16, 32, NM == 2>(a, st) : g == 64 ? launch_w4<Bf16, 64, NM == 2>(a, st) : launch_w4<Bf16, 128, NM == 2>(a, st));
+    return status_of(g == 32 ? launch_w4<F16, 32, NM == 2>(a, st) : g == 64 ? launch_w4<F16, 64, NM == 2>(a, st) : launch_w4<F16, 128, NM == 2>(a, st));
 }
 
 }  // namespace

@@ -163,7 +163,7 @@ def test_w4_arguments_are_refused(lib):
                               (P, 256, 3, P, 47), (P, 256, 64 * 65535 + 1, P, 48)):
         assert lib.moe_w4_matmul(w, x, ldx, m, y, ldy, None) == moe.MOE_EINVAL
         assert lib.moe_w4_gated(w, w, 0, 0.0, x, ldx, m, y, ldy, None) == moe.MOE_EINVAL
-    for other in (dict(rows=32), dict(cols=128), dict(group=32), dict(dtype=moe.MOE_F16)):
+    for other in (dict(rows=32), dict(cols=128), dict(group=32), dict(dtype=moe.MOE_F16), dict(zeros=P)):
         assert lib.moe_w4_gated(w, ctypes.byref(w4(**other)), 0, 0.0, P, 256, 3, P, 48, None) == moe.MOE_EINVAL
     assert lib.moe_w4_gated(w, w, 2, 0.0, P, 256, 3, P, 48, None) == moe.MOE_EINVAL
     assert lib.moe_w4_gated(w, w, 0, NAN, P, 256, 3, P, 48, None) == moe.MOE_EINVAL
