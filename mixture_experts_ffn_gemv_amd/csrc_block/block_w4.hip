@@ -10,24 +10,31 @@
 // with ones, in the layout in which it is needed. Scale and zero point are applied
 // in f32 to each group's sum, so that w is never rounded.
 //
-// A workgroup owns RT tiles of 16 rows of W (gated: eight rows of Wg and the same eight of
-// Wu in a tile) and up to 64 rows of x; its wavefronts split the columns, and their sums are
-// joined through LDS in wavefront order. A wavefront takes stages of 128 columns, the
-// next one in flight: lane (r = lane % 16, g = lane / 16) loads the 16 bytes of row r,
+// A workgroup owns WR RT tiles of 16 rows of W (gated: eight rows of Wg and the same eight of
+// Wu in a tile) and up to 32 rows of x. Eight wavefronts work: WR of them, with
+// RT tiles each, on each of WK parts of the columns; their sums are joined through LDS in order of the parts. A wavefront takes
+// stages of 128 columns: lane (r = lane % 16, g = lane / 16) loads the 16 bytes of row r,
 // columns 32 g .. 32 g + 31, and four lane-group swaps turn these so that its word j holds
 // columns 32 j + 8 g .. + 7: each matrix instruction then covers 32 consecutive columns,
 // one group or part of one. x is the instruction's first operand, W the second, so that a
 // lane's results all belong to row r, whose scales it needs. Row t of x sits at operand row
-// 4 (t % 4) + t / 4: up to eight tokens then leave two results per lane instead of four.
-// Scales and zero points come eight stages at a time, in pieces of eight groups, and wait
-// in LDS: loaded stage by stage they were half the time of a wide matrix.
+// 4 (t % 4) + t / 4: up to four tokens then leave one result per lane, up to eight two.
+//
+// Two more wavefronts bring x and the codes into LDS, stage by stage of every part, RING - 2
+// steps ahead. A load's four neighbouring lanes read 64 bytes of one row there: where each
+// reads another row, as the matrix instructions want it, a load takes four times as long on
+// a CU's load path, and x straight from the L2s cost four times what the codes did. They are
+// wavefronts of their own because loads complete in the order of a wavefront's requests.
+// Scales and zero points come eight stages at a time, in pieces of eight groups, and wait in
+// LDS: loaded stage by stage they were half the time of a wide matrix.
 #include "block_common.h"
 
 namespace moe {
 namespace {
 
 constexpr int STAGE = 128;       // columns a wavefront takes at a time
-constexpr int MAX_ROWS_X = 64;   // rows of x per workgroup
+constexpr int MAX_ROWS_X = 32;   // rows of x per workgroup
+constexpr int WORKERS = 8, LOADERS = 2;
 
 struct W4Mat {
     const uint8_t* codes;
@@ -89,83 +96,22 @@ struct SlabTile {
     uint8_t z[16 * NG * SLAB];
 };
 
-// NT: tiles of 16 rows of x. IR: results per lane and tile (tokens g + 4 i, i < IR). RT: tiles of W. WAVES: the most wavefronts
-template <typename T, int G, int NT, int IR, int RT, bool GATED, int WAVES, int AHEAD>
-__global__ __launch_bounds__(64 * WAVES) void w4_kernel(W4Args a) {
-    constexpr int NG = STAGE / G, TOK = 16 * NT, COLS = GATED ? 8 : 16;   // COLS: results per token and tile
-    extern __shared__ __align__(16) uint8_t smem[];   // slabs [wavefront][tile]; then sums [wavefront][tile][token][16 rows]
-    const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6, nw = blockDim.x >> 6;
-    const int r = lane & 15, g = lane >> 4;
-    const int n0 = blockIdx.x * COLS * RT;
+// ROWS: rows of x there is room for. WK, WR: parts of the columns, workers on each. RT: tiles of a
+// worker. RING: steps in LDS
+template <typename T, int G, int ROWS, int WK, int WR, int RT, int RING, bool GATED>
+__global__ __launch_bounds__(64 * (WORKERS + LOADERS)) void w4_kernel(W4Args a) {
+    static_assert(WK * WR == WORKERS, "");
+    constexpr int NG = STAGE / G, NT = (ROWS + 15) / 16, TOK = 16 * NT, COLS = GATED ? 8 : 16;   // COLS: results per token and tile
+    constexpr int IR = ROWS <= 4 ? 1 : ROWS <= 8 ? 2 : 4;   // results per lane and tile of x: tokens g + 4 i, i < IR
+    constexpr int X_ROW = STAGE * 2, X_STEP = WK * ROWS * X_ROW, STEP = X_STEP + WORKERS * RT * 1024;
+    // RING steps of x [part][row][128] and codes [worker][tile][16 rows][64 bytes]; slabs [worker][tile];
+    // then the sums [part][tile][token][16 rows]
+    extern __shared__ __align__(16) uint8_t smem[];
+    const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+    const int n0 = blockIdx.x * COLS * WR * RT;
     const int t0 = blockIdx.y * MAX_ROWS_X, mt = min(MAX_ROWS_X, a.m - t0);
-    const int kg = a.K / G;
-    const int stages = (a.K + STAGE - 1) / STAGE;
-    const int s0 = (int)((int64_t)wv * stages / nw), s1 = (int)((int64_t)(wv + 1) * stages / nw);
-    const uint32_t row_bytes = (uint32_t)a.K / 2;
-    // row r of tile t: its matrix, and its number there (past the matrix: the last row)
-    auto matrix = [&](int r) { return GATED && r >= 8 ? 1 : 0; };
-    auto row_of = [&](int t, int r) { return min(n0 + COLS * t + (GATED ? r & 7 : r), a.N - 1); };
-    const uint8_t* codes[RT];
-#pragma unroll
-    for (int t = 0; t < RT; ++t) codes[t] = a.w[matrix(r)].codes + (size_t)row_of(t, r) * row_bytes;
-    const auto X = buffer_rsrc(a.x + (size_t)t0 * a.ldx, (uint32_t)((mt - 1) * a.ldx + a.K) * 2);
-    constexpr uint32_t PAST = 0xFFFFFFF0u;   // an offset past the buffer: zeros
-    uint32_t xoff[NT];
-#pragma unroll
-    for (int t = 0; t < NT; ++t) {
-        const int tok = 16 * t + (r >> 2) + 4 * (r & 3);
-        xoff[t] = tok < mt ? (uint32_t)(tok * a.ldx * 2) : PAST;
-    }
-    const bool zeros = a.w[0].zeros != nullptr;   // (of both matrices or of neither)
-    SlabTile<NG>* const slab = reinterpret_cast<SlabTile<NG>*>(smem) + wv * RT;
-
-    // Stages s .. s + SLAB - 1: piece lane % NG of row lane / NG, eight groups each. A piece that
-    // would pass the row's end is read from its last eight groups and moved down.
-    auto load_slab = [&](int s) {
-        const int row = lane / NG, piece = lane % NG, first = s * NG + 8 * piece;
-        if (lane >= 16 * NG) return;
-#pragma unroll
-        for (int t = 0; t < RT; ++t) {
-            const W4Mat& w = a.w[matrix(row)];
-            const size_t at = (size_t)row_of(t, row) * kg;
-            unsigned __int128 sc = 0;
-            uint64_t zp = 0;
-            if (first < kg) {
-                if (kg >= 8) {
-                    const int from = min(first, kg - 8), down = first - from;
-                    __builtin_memcpy(&sc, w.scales + at + from, 16);
-                    sc >>= 16 * down;
-                    if (zeros) __builtin_memcpy(&zp, w.zeros + at + from, 8);
-                    zp >>= 8 * down;
-                } else {
-                    for (int i = first; i < kg; ++i) {
-                        sc |= (unsigned __int128)w.scales[at + i] << (16 * (i - first));
-                        if (zeros) zp |= (uint64_t)w.zeros[at + i] << (8 * (i - first));
-                    }
-                }
-            }
-            *reinterpret_cast<unsigned __int128*>(slab[t].s + (row * NG + piece) * 8) = sc;
-            *reinterpret_cast<uint64_t*>(slab[t].z + (row * NG + piece) * 8) = zp;
-        }
-    };
-
-    struct Stage {
-        uint4 x[4][NT], c[RT];
-    } st[AHEAD + 1];
-    auto request = [&](Stage& q, int s) {
-        const int k = min(s, s1 - 1) * STAGE, end = s < s1 ? a.K : 0;
-        // columns past K: x reads as zeros, and finite codes stand in for the missing ones
-#pragma unroll
-        for (int t = 0; t < RT; ++t) q.c[t] = *reinterpret_cast<const uint4*>(codes[t] + min((uint32_t)(k / 2 + 16 * g), row_bytes - 16));
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-#pragma unroll
-            for (int t = 0; t < NT; ++t) {
-                const int kx = k + 32 * j + 8 * g;
-                q.x[j][t] = buffer_load16(X, kx < end && xoff[t] != PAST ? xoff[t] + 2 * kx : PAST);
-            }
-    };
-
+    const int stages = (a.K + STAGE - 1) / STAGE, steps = (stages + WK - 1) / WK;
+    auto part = [&](int wk) { return (int)((int64_t)wk * stages / WK); };   // a part's first stage: steps or steps - 1 each
     float sum[RT][NT][IR];
 #pragma unroll
     for (int q = 0; q < RT; ++q)
@@ -173,78 +119,173 @@ __global__ __launch_bounds__(64 * WAVES) void w4_kernel(W4Args a) {
         for (int t = 0; t < NT; ++t)
 #pragma unroll
             for (int i = 0; i < IR; ++i) sum[q][t][i] = 0.f;
-    const s16x8 ones = __builtin_bit_cast(s16x8, (u32x4){T::ONES, T::ONES, T::ONES, T::ONES});
+    const int r = lane & 15, g = lane >> 4, wk = wv % WK, wr = wv / WK;
 
-    auto work = [&](Stage& q, int in) {   // in: the stage's place in the slab
-        f32x4 acc[RT][NT], sx[NT];
-        uint32_t c[RT][4];
-        float sc[RT][NG], zp[RT][NG];
+    const uint32_t row_bytes = (uint32_t)a.K / 2;
+    // the place in the workgroup of a worker's tile, counted over the workers (part wv % WK, rows wv / WK)
+    auto tile_of = [&](int w) { return w / (RT * WK) * RT + w % RT; };
+    // row r of tile t: its matrix, and its number there (past the matrix: the last row)
+    auto matrix = [&](int r) { return GATED && r >= 8 ? 1 : 0; };
+    auto row_of = [&](int t, int r) { return min(n0 + COLS * t + (GATED ? r & 7 : r), a.N - 1); };
+
+    if (wv >= WORKERS) {
+        constexpr int LOADS = WK * ROWS / 4 / LOADERS, CODES = WORKERS * RT / LOADERS;   // of one loader and step: four rows of 256 bytes, a tile's codes
+        static_assert((RING - 2) * (LOADS + CODES) < 64 && LOADS > 0, "");
+        const int id = wv - WORKERS, crow = lane >> 2;
+        const auto X = buffer_rsrc(a.x + (size_t)t0 * a.ldx, (uint32_t)((mt - 1) * a.ldx + a.K) * 2);
+        // 16-byte piece c of a code row lies at c ^ (row / 4)
+        const uint32_t piece = ((lane & 3) ^ (crow >> 2)) * 16;
+        const uint8_t* codes[CODES];
 #pragma unroll
-        for (int t = 0; t < RT; ++t) {
-            c[t][0] = q.c[t].x, c[t][1] = q.c[t].y, c[t][2] = q.c[t].z, c[t][3] = q.c[t].w;
-            turn_words(c[t]);
+        for (int i = 0; i < CODES; ++i)
+            codes[i] = a.w[matrix(crow)].codes + (size_t)row_of(tile_of(id * CODES + i), crow) * row_bytes;
+        auto stage = [&](int b) {
+            uint8_t* const to = smem + b % RING * STEP;
 #pragma unroll
-            for (int i = 0; i < NG; ++i) {
-                const int at = (r * SLAB + in) * NG + i;
-                sc[t][i] = T::load(slab[t].s[at]);
-                zp[t][i] = code_offset<T>() + (zeros ? (float)slab[t].z[at] : 8.f);
+            for (int i = 0; i < CODES; ++i) {
+                // (codes past K, or past the part, are others of the row: x is zero there)
+                const int w = id * CODES + i, s = min(part(w / RT % WK) + b, stages - 1);
+                load_lds16(codes[i] + min(s * (STAGE / 2) + piece, row_bytes - 16), to + X_STEP + w * 1024);
             }
+#pragma unroll
+            for (int i = 0; i < LOADS; ++i) {   // (past the part, past m or K: zeros)
+                const int run = id * LOADS + i, p = run / (ROWS / 4), tok = run % (ROWS / 4) * 4 + (lane >> 4);
+                // 16-byte chunk c of a token's row lies at c ^ (token & 15)
+                const int s = part(p) + b, k = s * STAGE + ((lane & 15) ^ (tok & 15)) * 8;
+                const bool in = tok < mt && k < a.K && s < part(p + 1);
+                buffer_load_lds16(X, to + run * 1024, in ? (uint32_t)(tok * a.ldx + k) * 2 : 0xFFFFFFF0u);
+            }
+        };
+#pragma unroll
+        for (int b = 0; b < RING - 1; ++b) stage(b);
+        for (int b = 0; b < steps; ++b) {
+            wait_vm_loads<(RING - 2) * (LOADS + CODES)>();   // step b has landed
+            barrier_lds();                                   // every worker is done with step b - 1
+            stage(b + RING - 1);
         }
+        wait_vm_loads<0>();
+    } else {
+        const int kg = a.K / G, s0 = part(wk), s1 = part(wk + 1);
+        const bool zeros = a.w[0].zeros != nullptr;   // (of both matrices or of neither)
+        SlabTile<NG>* const slab = reinterpret_cast<SlabTile<NG>*>(smem + RING * STEP) + wv * RT;
+
+        // Stages s .. s + SLAB - 1: piece lane % NG of row lane / NG, eight groups each. A piece that
+        // would pass the row's end is read from its last eight groups and moved down.
+        auto load_slab = [&](int s) {
+            const int row = lane / NG, piece = lane % NG, first = s * NG + 8 * piece;
+            if (lane >= 16 * NG) return;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const bool first = (32 * j) % G == 0, last = (32 * (j + 1)) % G == 0;
-            const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
+            for (int t = 0; t < RT; ++t) {
+                const W4Mat& w = a.w[matrix(row)];
+                const size_t at = (size_t)row_of(wr * RT + t, row) * kg;
+                unsigned __int128 sc = 0;
+                uint64_t zp = 0;
+                if (first < kg) {
+                    if (kg >= 8) {
+                        const int from = min(first, kg - 8), down = first - from;
+                        __builtin_memcpy(&sc, w.scales + at + from, 16);
+                        sc >>= 16 * down;
+                        if (zeros) __builtin_memcpy(&zp, w.zeros + at + from, 8);
+                        else zp = 0x0808080808080808u;
+                        zp >>= 8 * down;
+                    } else {
+                        for (int i = first; i < kg; ++i) {
+                            sc |= (unsigned __int128)w.scales[at + i] << (16 * (i - first));
+                            zp |= (uint64_t)(zeros ? w.zeros[at + i] : 8) << (8 * (i - first));
+                        }
+                    }
+                }
+                *reinterpret_cast<unsigned __int128*>(slab[t].s + (row * NG + piece) * 8) = sc;
+                *reinterpret_cast<uint64_t*>(slab[t].z + (row * NG + piece) * 8) = zp;
+            }
+        };
+        int xrow[NT];
 #pragma unroll
-            for (int t = 0; t < NT; ++t) sx[t] = T::mfma(__builtin_bit_cast(s16x8, q.x[j][t]), ones, first ? zero : sx[t]);
+        for (int t = 0; t < NT; ++t) xrow[t] = min(16 * t + (r >> 2) + 4 * (r & 3), ROWS - 1);
+        const s16x8 ones = __builtin_bit_cast(s16x8, (u32x4){T::ONES, T::ONES, T::ONES, T::ONES});
+
+        const int code_at = X_STEP + wv * RT * 1024 + r * 64 + ((g ^ (r >> 2)) << 4);
+        auto work = [&](int step, int in) {   // in: the stage's place in the slab
+            // everything is requested from LDS before the codes are taken apart
+            const uint8_t* const at = smem + step % RING * STEP;
+            const uint8_t* const x = at + wk * ROWS * X_ROW;
+            uint4 q[RT];
+            s16x8 xv[4][NT];
+            uint16_t sc[RT][NG];
+            uint8_t zp[RT][NG];
+#pragma unroll
+            for (int w = 0; w < RT; ++w) q[w] = *reinterpret_cast<const uint4*>(at + code_at + w * 1024);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+                    xv[j][t] = *reinterpret_cast<const s16x8*>(x + xrow[t] * X_ROW + (((4 * j + g) ^ (xrow[t] & 15)) << 4));
 #pragma unroll
             for (int w = 0; w < RT; ++w) {
-                const s16x8 v = codes_to_values(c[w][j], T());
-#pragma unroll
-                for (int t = 0; t < NT; ++t) acc[w][t] = T::mfma(__builtin_bit_cast(s16x8, q.x[j][t]), v, first ? zero : acc[w][t]);
+                __builtin_memcpy(sc[w], __builtin_assume_aligned(slab[w].s + (r * SLAB + in) * NG, 2 * NG), 2 * NG);
+                __builtin_memcpy(zp[w], __builtin_assume_aligned(slab[w].z + (r * SLAB + in) * NG, NG), NG);
             }
-            if (last) {
-                const int i0 = 32 * j / G;
+            f32x4 acc[RT][NT], sx[NT];
+            uint32_t c[RT][4];
 #pragma unroll
-                for (int w = 0; w < RT; ++w)
-#pragma unroll
-                    for (int t = 0; t < NT; ++t)
-#pragma unroll
-                        for (int i = 0; i < IR; ++i)
-                            sum[w][t][i] = fmaf(sc[w][i0], fmaf(-zp[w][i0], sx[t][i], acc[w][t][i]), sum[w][t][i]);
+            for (int w = 0; w < RT; ++w) {
+                c[w][0] = q[w].x, c[w][1] = q[w].y, c[w][2] = q[w].z, c[w][3] = q[w].w;
+                turn_words(c[w]);
             }
-        }
-    };
-    // one instance of the loop's body, the stages in flight handed down in registers: unrolled
-    // over them, these short kernels spent more time on fetching their instructions
-    request(st[0], s0);
-    load_slab(s0);
 #pragma unroll
-    for (int i = 1; i < AHEAD; ++i) request(st[i], s0 + i);
-    int in = 0;
+            for (int j = 0; j < 4; ++j) {
+                const bool first = (32 * j) % G == 0, last = (32 * (j + 1)) % G == 0;
+                const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int t = 0; t < NT; ++t) sx[t] = T::mfma(xv[j][t], ones, first ? zero : sx[t]);
+#pragma unroll
+                for (int w = 0; w < RT; ++w) {
+                    const s16x8 v = codes_to_values(c[w][j], T());
+#pragma unroll
+                    for (int t = 0; t < NT; ++t) acc[w][t] = T::mfma(xv[j][t], v, first ? zero : acc[w][t]);
+                }
+                if (last) {
+#pragma unroll
+                    for (int w = 0; w < RT; ++w) {
+                        const float s1 = T::load(sc[w][32 * j / G]), z1 = code_offset<T>() + (float)zp[w][32 * j / G];
+#pragma unroll
+                        for (int t = 0; t < NT; ++t)
+#pragma unroll
+                            for (int i = 0; i < IR; ++i) sum[w][t][i] = fmaf(s1, fmaf(-z1, sx[t][i], acc[w][t][i]), sum[w][t][i]);
+                    }
+                }
+            }
+        };
+        if (s0 < s1) load_slab(s0);
+        int in = 0;
 #pragma unroll 1
-    for (int s = s0; s < s1; ++s) {
-        request(st[AHEAD], s + AHEAD);
-        work(st[0], in);
-#pragma unroll
-        for (int i = 0; i < AHEAD; ++i) st[i] = st[i + 1];
-        if (++in == SLAB && s + 1 < s1) load_slab(s + 1), in = 0;
+        for (int step = 0; step < steps; ++step) {
+            barrier_lds();   // the step's codes and x have landed
+            if (s0 + step >= s1) continue;
+            work(step, in);
+            if (++in == SLAB && s0 + step + 1 < s1) load_slab(s0 + step + 1), in = 0;
+        }
     }
 
-    __syncthreads();   // the sums take the slabs' place
+    __syncthreads();   // the sums take the place of x
     float* const red = reinterpret_cast<float*>(smem);
+    if (wv < WORKERS) {
 #pragma unroll
-    for (int q = 0; q < RT; ++q)
+        for (int q = 0; q < RT; ++q)
 #pragma unroll
-        for (int t = 0; t < NT; ++t)
+            for (int t = 0; t < NT; ++t)
 #pragma unroll
-            for (int i = 0; i < IR; ++i) red[((wv * RT + q) * TOK + 16 * t + g + 4 * i) * 16 + r] = sum[q][t][i];
+                for (int i = 0; i < IR; ++i)
+                    red[(((wk * WR + wr) * RT + q) * TOK + 16 * t + g + 4 * i) * 16 + r] = sum[q][t][i];
+    }
     __syncthreads();
-    for (int e = threadIdx.x; e < mt * COLS * RT; e += blockDim.x) {
-        const int c = e % COLS, tile = e / COLS % RT, tok = e / (COLS * RT), n = n0 + COLS * tile + c;
+    for (int e = threadIdx.x; e < mt * COLS * WR * RT; e += blockDim.x) {
+        const int c = e % COLS, tile = e / COLS % (WR * RT), tok = e / (COLS * WR * RT), n = n0 + COLS * tile + c;
         if (n >= a.N) continue;
         float v[2] = {0.f, 0.f};
-        for (int w = 0; w < nw; ++w) {
-            const float* p = red + ((w * RT + tile) * TOK + tok) * 16 + c;
+#pragma unroll
+        for (int w = 0; w < WK; ++w) {
+            const float* p = red + ((w * WR * RT + tile) * TOK + tok) * 16 + c;
             v[0] += p[0];
             if (GATED) v[1] += p[8];
         }
@@ -262,23 +303,22 @@ int check_w4(const moe_w4* w) {
     return MOE_OK;
 }
 
-template <typename T, int G, int NT, int IR, int RT, bool GATED, int WAVES, int AHEAD>
+template <typename T, int G, int ROWS, int WK, int WR, int RT, int RING, bool GATED>
 hipError_t launch_tiles(const W4Args& a, hipStream_t st) {
-    const int nw = std::min(WAVES, (a.K + STAGE - 1) / STAGE);   // (every wavefront has a stage)
-    const int cols = (GATED ? 8 : 16) * RT;
+    const int cols = (GATED ? 8 : 16) * WR * RT;
     const dim3 grid((a.N + cols - 1) / cols, (a.m + MAX_ROWS_X - 1) / MAX_ROWS_X);
-    const size_t lds = nw * RT * std::max(sizeof(SlabTile<STAGE / G>), sizeof(float) * NT * 256);
-    return launch_kernel(w4_kernel<T, G, NT, IR, RT, GATED, WAVES, AHEAD>, grid, dim3(64 * nw), lds, st, a);
+    const size_t lds = std::max<size_t>(RING * (WK * ROWS * STAGE * 2 + WORKERS * RT * 1024) + WORKERS * RT * sizeof(SlabTile<STAGE / G>),
+                                        sizeof(float) * WORKERS * RT * ((ROWS + 15) / 16) * 256);
+    return launch_kernel(w4_kernel<T, G, ROWS, WK, WR, RT, RING, GATED>, grid, dim3(64 * (WORKERS + LOADERS)), lds, st, a);
 }
 
 template <typename T, int G, bool GATED>
 hipError_t launch_w4(const W4Args& a, hipStream_t st) {
-    const int mt = std::min(a.m, MAX_ROWS_X);
-    if (mt <= 8) return launch_tiles<T, G, 1, 2, 1, GATED, 8, 2>(a, st);
-    if (mt <= 16) return launch_tiles<T, G, 1, 4, 1, GATED, 8, 2>(a, st);
-    const bool many = a.N >= (GATED ? 8192 : 16384);
-    if (mt <= 32) return many ? launch_tiles<T, G, 2, 4, 4, GATED, 8, 1>(a, st) : launch_tiles<T, G, 2, 4, 1, GATED, 8, 1>(a, st);
-    return many ? launch_tiles<T, G, 4, 4, 2, GATED, 8, 1>(a, st) : launch_tiles<T, G, 4, 4, 1, GATED, 8, 1>(a, st);
+    if (a.m <= 4) return launch_tiles<T, G, 4, 4, 2, 1, 4, GATED>(a, st);
+    if (a.m <= 8) return launch_tiles<T, G, 8, 4, 2, 1, 4, GATED>(a, st);
+    if (a.m <= 16) return launch_tiles<T, G, 16, 4, 2, 1, 4, GATED>(a, st);
+    if (a.N >= (GATED ? 8192 : 16384)) return launch_tiles<T, G, 32, 2, 4, 2, 3, GATED>(a, st);
+    return launch_tiles<T, G, 32, 4, 2, 1, 3, GATED>(a, st);
 }
 
 template <int NM>
