@@ -54,7 +54,7 @@ MOE_DEV size_t saved_at(int q16, int i16, int I) { return ((size_t)q16 * ((I + 1
 
 // Tiles in LDS. rows x 64 k (128 bytes a row): chunk c of 16 bytes of row r lies at c ^ swz_k(r),
 // so that the 16 rows of an operand read fall on distinct banks.
-MOE_DEV int swz_k(int row) { return (row & 7) ^ ((row >> 3) & 1); }
+MOE_DEV int swz_k(int row) { return row & 7; }
 // 64 k x rows, rows = 128 or 256: runs of 1024 bytes, PIECE apart, each holding rows k that are
 // never read together; a transposing read takes four rows k of two lane groups at a time, and
 // these lie in eight runs, whose distance puts them on distinct banks. Every read of a
