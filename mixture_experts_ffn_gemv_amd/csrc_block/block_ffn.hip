@@ -696,13 +696,14 @@ hipError_t launch_skinny(const FfnArgs& a, hipStream_t st) {
 // 2304 (D x I, both products) take 36.5 against 39.6 us, of 8192 x 2048 33.8 against 46.0, of 1024 x
 // 1024 11.6 against 22.2 (of 8192 x 8192 114.8 against 108.3). Above 32 rows a workgroup's slabs of x
 // (96 KB and more) leave a CU room for one workgroup, and where there are more of them than CUs
-// tiles are faster: 48 rows of 5120 x 2304 41.5 against 47.6, of 8192 x 8192 110 against 145 (of 8192
-// x 2048 44.1 against 43.6); with fewer they are not: of 2048 x 2048 29.0 against 17.3, 64 rows 29.4
-// against 19.5.
+// tiles are faster: 48 rows of 5120 x 2304 41.7 against 47.6, of 8192 x 8192 110 against 145; with
+// fewer they are not: of 2048 x 2048 29.0 against 17.3, 64 rows 29.4 against 19.5; nor are they with 48
+// rows and 2^24 weights at most: DOWN of 8192 x 2048 17.7 against 17.2.
 template <typename T, Kind KIND>
 hipError_t launch_forward(const FfnArgs& a, float* partial, hipStream_t st) {
     const int blocks = KIND == GATEUP ? cdiv(a.I, 8) : cdiv(a.D, 16);
-    if (a.m > 64 || (a.m > 32 && blocks > N_CU)) return launch_product<T, KIND>(a, partial, st);
+    const bool large = a.m > 48 || (size_t)(KIND == GATEUP ? 2 : 1) * a.D * a.I > 1 << 24;
+    if (a.m > 64 || (a.m > 32 && blocks > N_CU && large)) return launch_product<T, KIND>(a, partial, st);
     // up to 16 rows that fit into LDS whole: one row of 5120 x 2304 21.8 against 27.7 us in slabs, of
     // 8192 x 2048 23.7 against 27.0, 16 rows of 1024 x 1024 7.9 against 11.4
     const size_t whole = a.m * (size_t)few_row(KIND == GATEUP ? a.D : a.I);
