@@ -373,14 +373,14 @@ typedef struct moe_ffn {
 } moe_ffn;
 
 /* Bytes that calls with m rows need: `forward` and `backward`, the workspaces of
- * the two calls, and `saved`, what a forward call leaves for its backward call
+ * the two calls (operands between the products and sums of split products), and `saved`, what a forward call leaves for its backward call
  * (g and u in f32). Each a multiple of 256, possibly 0. MOE_EINVAL for a bad
  * description, m < 0, m > 2^24 or NULL. */
 int moe_ffn_workspace(const moe_ffn* f, int32_t m, size_t* forward, size_t* saved, size_t* backward);
 
 /* y = block(x) for m rows. x [m, D] with row stride ldx, y [m, D] with row stride
- * ldy (both >= D and multiples of 8; device, 16-byte aligned; y does not overlap
- * x or the weights). saved: NULL, or the `saved` bytes that moe_ffn_backward
+ * ldy (both >= D, multiples of 8 and at most 2^22; device, 16-byte aligned; y does not
+ * overlap x or the weights). saved: NULL, or the `saved` bytes that moe_ffn_backward
  * takes (256-byte aligned, as work is). m = 0 does nothing. MOE_EINVAL for a bad
  * description, size, stride, NULL or misaligned pointer; MOE_ESCRATCH when
  * work_bytes (or, with saved, saved_bytes) is less than moe_ffn_workspace says;
@@ -432,8 +432,7 @@ int moe_norm_workspace(const moe_norm* f, int32_t m, size_t* backward);
  * wanted. stats: NULL, or f32 [m, 2] for the backward pass: 1 / rms(y) and
  * 1 / rms(r') (0 where there is no such norm). r_out may be r itself and n may
  * be y itself (same stride); no other overlap. Pointers are aligned to their
- * value type (rows whose pointers and strides are multiples of 16 bytes move
- * fastest). m = 0 does nothing. MOE_EINVAL, MOE_EHIP. */
+ * value type. m = 0 does nothing. MOE_EINVAL, MOE_EHIP. */
 int moe_norm_forward(const moe_norm* f, const void* r, int64_t ldr, const void* y, int64_t ldy, const void* gate,
                      int32_t gate_kind, int32_t m, void* r_out, int64_t ldro, void* n, int64_t ldn, float* stats,
                      void* stream);
@@ -444,7 +443,8 @@ int moe_norm_forward(const moe_norm* f, const void* r, int64_t ldr, const void* 
  *   dp = gate e;  b = w_post dp;  dy = rs1 (b - y rs1^2 mean(y b))  (dp without w_post)
  *   dgate = e p, summed over what the gate is broadcast over
  *   dw_post = sum over rows of dp y rs1;   dw_pre = sum over rows of dn r' rs2
- * r, y, gate and stats as in the forward call (r' is computed again from them).
+ * r, y, gate and stats as in the forward call (r' is computed again from them;
+ * stats is required unless m = 0).
  * Any output may be NULL and is then not computed. Sums over rows are made in
  * f32 in a fixed order. dr may be dr_out itself and dy may be dn itself (same
  * stride); no other overlap. m = 0 writes zeros to the gradients that are sums
@@ -468,9 +468,10 @@ typedef struct moe_w4 {
 } moe_w4;
 
 /* y [m, N] = x W^T, summed in f32 with the exact w and rounded once. x [m, K] with
- * row stride ldx (a multiple of 8; 16-byte aligned), y with row stride ldy >= N
- * (2-byte aligned). Made for few rows: each 64 rows of x read the weights once.
- * A row of x that holds an infinity gives NaN. m = 0 does nothing. MOE_EINVAL,
+ * row stride ldx (a multiple of 8, at most 2^24; 16-byte aligned), y with row stride
+ * ldy >= N (2-byte aligned); m is at most 2097120. Made for few rows: each 32 rows of
+ * x read the weights once. A row of x that holds an infinity gives NaN, and one with
+ * values past 2^110 may. m = 0 does nothing. MOE_EINVAL,
  * MOE_EHIP. */
 int moe_w4_matmul(const moe_w4* w, const void* x, int64_t ldx, int32_t m, void* y, int64_t ldy, void* stream);
 

@@ -4,9 +4,9 @@
 // A row lives in the registers of the threads that own it from its first load to
 // its last store, so each array passes through memory once in each direction. A
 // thread holds C chunks of V consecutive values (16 bytes, wherever the row starts);
-// chunk j of thread t is chunk t + j * tpr of the row. A row is owned by tpr threads: a power of two up to 64 (several rows per
-// wavefront, sums by lane exchange) or a multiple of 64 (a workgroup per row, sums
-// over the wavefronts through LDS). A workgroup takes rows blockIdx, blockIdx +
+// chunk j of thread t is chunk t + j * tpr of the row. A row is owned by tpr threads:
+// a power of two up to 64 (several rows per wavefront, sums by lane exchange) or a
+// multiple of 64 (a workgroup per row, sums over the wavefronts through LDS). A workgroup takes rows blockIdx, blockIdx +
 // grid, ... and requests its next row, as it lies in memory, before it works on the
 // current one; the weights and a per-channel gate stay in registers.
 //
@@ -28,8 +28,7 @@
 namespace moe {
 namespace {
 
-constexpr int EPT = 16;             // values of a row that one thread holds at most
-constexpr int MAX_DIM = 16384;      // EPT * 1024
+constexpr int MAX_DIM = 16384;   // 1024 threads with 16 values each
 // wavefronts per CU for which workgroups are launched: about as many as are resident, so that
 // each workgroup keeps requesting rows ahead from the first to the last
 constexpr int FWD_WAVES = 20, BWD_WAVES = 12;

@@ -10,10 +10,15 @@
 // with ones, in the layout in which it is needed. Scale and zero point are applied
 // in f32 to each group's sum, so that w is never rounded.
 //
+// Bound, for few rows, by the codes' bytes. 65536 x 2048, one row of x: 23.7 us, 3.0 TB/s of
+// codes and scales; 8192 x 8192 11.4 us, 3.1 TB/s (a stream of reads from HBM reaches about 6); 5120 x
+// 5120 7.6 us, of which a launch, the first loads and the sums' join are about 4. From 16 rows
+// on x, which every workgroup brings into its LDS, costs more than the codes.
+//
 // A workgroup owns WR RT tiles of 16 rows of W (gated: eight rows of Wg and the same eight of
-// Wu in a tile) and up to 32 rows of x. Eight wavefronts work: WR of them, with
-// RT tiles each, on each of WK parts of the columns; their sums are joined through LDS in order of the parts. A wavefront takes
-// stages of 128 columns: lane (r = lane % 16, g = lane / 16) loads the 16 bytes of row r,
+// Wu in a tile) and up to 32 rows of x. Eight wavefronts work: WR of them, with RT tiles
+// each, on each of WK parts of the columns; their sums are joined through LDS in order of
+// the parts. A wavefront takes stages of 128 columns: lane (r = lane % 16, g = lane / 16) loads the 16 bytes of row r,
 // columns 32 g .. 32 g + 31, and four lane-group swaps turn these so that its word j holds
 // columns 32 j + 8 g .. + 7: each matrix instruction then covers 32 consecutive columns,
 // one group or part of one. x is the instruction's first operand, W the second, so that a
@@ -312,13 +317,22 @@ hipError_t launch_tiles(const W4Args& a, hipStream_t st) {
     return launch_kernel(w4_kernel<T, G, ROWS, WK, WR, RT, RING, GATED>, grid, dim3(64 * (WORKERS + LOADERS)), lds, st, a);
 }
 
+// LDS room for 4, 8, 16 or 32 rows of x, since a step's x is loaded whether its rows exist or not (8 rows
+// of 5120 x 5120, group 64: 7.8 us, in room for 16 rows 9.6; 16 rows 9.6, in room for 32 14.8; 1 row
+// 7.6, in room for 8 8.0, of 65536 x 2048 23.7 against 25.1). With more than 16 rows one workgroup fits a
+// CU. Two wavefronts on rows make the most workgroups, and the shortest where those are one round of
+// the CUs at most (32 rows of 5120 x 5120 15.0 us against 24.5, of 8192 x 8192 20.6 against 37); beyond,
+// four with two tiles each read x a quarter as often (16384 x 5120 26.2 against 29.6, 65536 x 2048
+// 28.5 against 69.5, 64 rows of 8192 x 2048 12.8 against 18.1).
 template <typename T, int G, bool GATED>
 hipError_t launch_w4(const W4Args& a, hipStream_t st) {
     if (a.m <= 4) return launch_tiles<T, G, 4, 4, 2, 1, 4, GATED>(a, st);
     if (a.m <= 8) return launch_tiles<T, G, 8, 4, 2, 1, 4, GATED>(a, st);
     if (a.m <= 16) return launch_tiles<T, G, 16, 4, 2, 1, 4, GATED>(a, st);
-    if (a.N >= (GATED ? 8192 : 16384)) return launch_tiles<T, G, 32, 2, 4, 2, 3, GATED>(a, st);
-    return launch_tiles<T, G, 32, 4, 2, 1, 3, GATED>(a, st);
+    constexpr int COLS = 2 * (GATED ? 8 : 16);
+    const int64_t blocks = (int64_t)((a.N + COLS - 1) / COLS) * ((a.m + MAX_ROWS_X - 1) / MAX_ROWS_X);
+    if (blocks <= 256) return launch_tiles<T, G, 32, 4, 2, 1, 3, GATED>(a, st);
+    return launch_tiles<T, G, 32, 2, 4, 2, 3, GATED>(a, st);
 }
 
 template <int NM>
