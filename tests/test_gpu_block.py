@@ -103,6 +103,16 @@ def test_ffn_same_bits_with_and_without_saving_and_again():
         assert torch.equal(a[k], b[k]), k
 
 
+@pytest.mark.parametrize("m,dim,inter", [(50, 4136, 72), (35, 4072, 2064), (64, 4104, 2088)])
+def test_ffn_few_rows_in_tiles_against_float64(m, dim, inter):
+    # more workgroups than CUs if split by weight rows: the second product, the first, both in tiles
+    c = ffn_case(m, dim, inter, BF16 if m % 2 else F16, "silu", 10.0, seed=m)
+    want, got = ref.ffn(c[0], c[2], c[3], c[4], "silu", 10.0, dy=c[1]), ffn_run(c, extra=8)
+    for k, (v, e) in want.items():
+        ref.check(got[k], v, e, f"{k} of m={m}")
+    assert untouched(got["y"])
+
+
 @pytest.mark.parametrize("want", [("dx",), ("dw_gate",), ("dw_up", "dw_down"), ("dw_down",), ("dw_gate", "dw_down")])
 def test_ffn_backward_of_some_outputs(want):
     c = ffn_case(40, 264, 392, F16, "gelu", 0.0, seed=9)
@@ -414,6 +424,19 @@ def test_w4_matmul_against_float64(m, rows, cols, group, zeros, dtype):
         moe.moe_w4_matmul(w4_make(c, group), strided(x, extra), y)
         ref.check(y, v, e + ref.U[dtype] * (v.abs() + e) + ref.TINY[dtype], f"[{m}, {cols}] x [{rows}]")
         assert untouched(y)
+
+
+W4_MANY = [(17, 8225, 160, 32, True, BF16), (70, 2740, 256, 64, False, F16), (32, 8200, 384, 128, True, F16)]
+
+
+@pytest.mark.parametrize("m,rows,cols,group,zeros,dtype", W4_MANY)
+def test_w4_matmul_of_many_workgroups_against_float64(m, rows, cols, group, zeros, dtype):
+    test_w4_matmul_against_float64(m, rows, cols, group, zeros, dtype)
+
+
+@pytest.mark.parametrize("m,rows,cols,group,zeros,dtype", [(m, rows // 2 + 1, *rest) for m, rows, *rest in W4_MANY])
+def test_w4_gated_of_many_workgroups_against_float64(m, rows, cols, group, zeros, dtype):
+    test_w4_gated_against_float64(m, rows, cols, group, zeros, dtype, "silu", 0.5)
 
 
 @pytest.mark.parametrize("act,limit", [("silu", 0.0), ("silu", 0.5), ("gelu", 0.0)])
