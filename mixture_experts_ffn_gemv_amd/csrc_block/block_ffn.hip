@@ -14,10 +14,19 @@
 // eight k) or p / q (tiles of 64 k x rows; two transposing 8-byte LDS reads), so no
 // operand is ever transposed in memory.
 //
-// Tiles come into LDS by buffer loads straight to LDS, 16 bytes per lane, one K step of
-// 64 ahead. What lies past an operand's rows or past K lands as zeros: rows by the
-// buffer's length, a K tail by an offset past it. Chunks of 16 bytes are stored
-// permuted so that the LDS reads of a matrix operand fall on distinct banks.
+// Tiles come into LDS by buffer loads straight to LDS, 16 bytes per lane, a K step of 64
+// ahead. What lies past an operand's rows or past K lands as zeros: rows by the buffer's
+// length, a K tail by an offset past it. Chunks of 16 bytes are stored permuted so that
+// the LDS reads of a matrix operand fall on distinct banks.
+//
+// Bound, for many rows, by the matrix cores: at 8192 rows of 5120 x 2304 (bf16, a training
+// step 1.72 ms) GATEUP takes 333 us (1.16 PFLOP/s), DOWN 187 (1.03), DH 266 (0.73), DX 346
+// (1.12), DW 533 (1.09), where a library product of 8192^3 reaches 1.51 (either operand's
+// k consecutive), 1.32 or 1.16 (as in DX and DW). A round of whole tiles runs at 1.3; the rest
+// is the last round, which is not full, and DH's epilogue: it reads 151 MB of g and u and
+// writes 113 MB of dg, du and h, after the products of its tile. Counters: no LDS
+// conflicts, matrix cores busy 0.58 (GATEUP) and 0.47 (DW) of the cycles.
+// Few rows are bound by the weights' bytes: one token of 5120 x 2304 20.2 us, 70.8 MB, 3.5 TB/s.
 #include "block_common.h"
 
 namespace moe {
@@ -437,8 +446,12 @@ MOE_DEV void skinny_finish(const FfnArgs& a, float* red, int n0, const f32x4 (&a
     }
 }
 
-// The same for up to 16 rows whose x fits into LDS whole: one wait for it, and the wavefronts
-// then go their own ways through k, AHEAD chunks of 32 of their weights in flight
+// Up to 16 rows whose x fits into LDS whole: GATEUP or DOWN with the weights read straight into
+// registers, since nothing would be read twice. A workgroup owns 16 weight rows (GATEUP: eight
+// of Wg and the same eight of Wu), each of its eight wavefronts a part of k, and their sums are
+// joined through LDS in wavefront order. There is one wait for x, and the wavefronts then
+// go their own ways through k, AHEAD chunks of 32 of their weights in flight. One token of 5120 x
+// 2304: 12.4 us (47 MB, 3.8 TB/s) and 6.6 us.
 constexpr size_t FEW_LDS = 64 << 10;
 MOE_DEV __host__ int few_row(int K) { return (K + 511) / 512 * 1024; }   // bytes of a token's row there
 template <typename T, Kind KIND>
@@ -486,14 +499,14 @@ __global__ __launch_bounds__(64 * SKINNY_WAVES) void ffn_few_kernel(FfnArgs a) {
     skinny_finish<T, KIND, 1, 64 * SKINNY_WAVES>(a, reinterpret_cast<float*>(smem), n0, acc);
 }
 
-// Few rows (m <= ROWS): GATEUP or DOWN with the weights read straight into registers, since
-// nothing would be read twice. A workgroup owns 16 weight rows (GATEUP: eight of Wg and the
-// same eight of Wu); eight wavefronts split every slab of KS k between them, and their sums
-// are joined through LDS in wavefront order. x comes into LDS a slab at a time, whole lines of
+// Few rows (m <= ROWS) whose x does not: the same weight rows, but the eight wavefronts split
+// every slab of KS k between them. x comes into LDS a slab at a time, whole lines of
 // it (a load that gathers 16 rows takes about 90 cycles of a CU's load path, one of whole
 // lines 16, so that x straight from the L2s cost as much as the weights). Two wavefronts of
 // their own load it: loads complete in the order of a wavefront's requests, so that one which
-// waited for x would wait for every weight that it had requested before.
+// waited for x would wait for every weight that it had requested before. 47 rows of 8192 x 2048:
+// 25.2 us (67 MB, 2.7 TB/s) and 17.4 us; 32 rows 34.0 us together. A slab of
+// x is three times its weights there, and is what bounds it.
 constexpr int skinny_slab(int rows) { return rows <= 16 ? 512 : 256; }
 template <typename T, Kind KIND, int ROWS>
 __global__ __launch_bounds__(64 * (SKINNY_WAVES + SKINNY_LOADERS)) void ffn_skinny_kernel(FfnArgs a) {
@@ -587,10 +600,12 @@ struct Product {
     size_t bytes;     // of plan.partial
 };
 
-// How a product is cut up. Costs in units of one K step of a 256 x 256 tile on a CU (1.65 us): a
-// 128 x 128 tile's step takes 0.33 of it (a quarter of the products, at three quarters of the rate);
-// the split tiles' sums pass through memory twice (0.06 a 256 x 256 tile and split, and 4 for the
-// second launch).
+// How a product is cut up: 256 x 256 or 128 x 128 tiles, and by how much the tiles past the last full
+// round of the CUs are split along k. Costs in units of one K step of a 256 x 256 tile on a CU
+// (1.65 us): a 128 x 128 tile's step takes 0.33 of it (a quarter of the products, at three quarters
+// of the rate); the split tiles' sums pass through memory twice (0.06 a 256 x 256 tile and split, and 4 for
+// the second launch). 8192 rows of 5120 x 2304 in the large tiles and in the small: GATEUP 334 and
+// 377 us, DOWN 187 and 196, DH 266 and 271, DX 346 and 422, DW 533 and 624.
 Product plan_product(Kind kind, int m, int D, int I, int wide, bool down) {
     Product best{};
     double best_cost = 1e30;

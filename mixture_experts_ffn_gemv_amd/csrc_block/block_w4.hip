@@ -93,6 +93,12 @@ MOE_DEV void turn_words(uint32_t* w) {
     w[0] = c[0], w[1] = c[1], w[2] = d[0], w[3] = d[1];
 }
 
+// Chunks of 16 bytes in LDS lie at c ^ swz(row), rows of 256 bytes, or c ^ swz(row / 4), rows of 64. A
+// read of 16 bytes per lane takes sixteen lanes at a time: 0..3 and 12..15 of one group of sixteen
+// and 4..11 of the next, which want chunk c of their rows and chunk c + 1 of theirs. So
+// two bits of the row number go 0, 3, 1, 2 -> 0, 1, 2, 3, which keeps the two apart.
+MOE_DEV int swz(int row) { return (row & 12) | (((row ^ (row >> 1)) & 1) << 1) | ((row >> 1) & 1); }
+
 // One wavefront's scales and zero points of a tile for SLAB stages: row r's at r * NG * SLAB
 constexpr int SLAB = 8;
 template <int NG>
@@ -138,8 +144,7 @@ __global__ __launch_bounds__(64 * (WORKERS + LOADERS)) void w4_kernel(W4Args a) 
         static_assert((RING - 2) * (LOADS + CODES) < 64 && LOADS > 0, "");
         const int id = wv - WORKERS, crow = lane >> 2;
         const auto X = buffer_rsrc(a.x + (size_t)t0 * a.ldx, (uint32_t)((mt - 1) * a.ldx + a.K) * 2);
-        // 16-byte piece c of a code row lies at c ^ (row / 4)
-        const uint32_t piece = ((lane & 3) ^ (crow >> 2)) * 16;
+        const uint32_t piece = ((lane & 3) ^ swz(crow >> 2)) * 16;
         const uint8_t* codes[CODES];
 #pragma unroll
         for (int i = 0; i < CODES; ++i)
@@ -155,8 +160,7 @@ __global__ __launch_bounds__(64 * (WORKERS + LOADERS)) void w4_kernel(W4Args a) 
 #pragma unroll
             for (int i = 0; i < LOADS; ++i) {   // (past the part, past m or K: zeros)
                 const int run = id * LOADS + i, p = run / (ROWS / 4), tok = run % (ROWS / 4) * 4 + (lane >> 4);
-                // 16-byte chunk c of a token's row lies at c ^ (token & 15)
-                const int s = part(p) + b, k = s * STAGE + ((lane & 15) ^ (tok & 15)) * 8;
+                const int s = part(p) + b, k = s * STAGE + ((lane & 15) ^ swz(tok)) * 8;
                 const bool in = tok < mt && k < a.K && s < part(p + 1);
                 buffer_load_lds16(X, to + run * 1024, in ? (uint32_t)(tok * a.ldx + k) * 2 : 0xFFFFFFF0u);
             }
@@ -209,7 +213,7 @@ __global__ __launch_bounds__(64 * (WORKERS + LOADERS)) void w4_kernel(W4Args a) 
         for (int t = 0; t < NT; ++t) xrow[t] = min(16 * t + (r >> 2) + 4 * (r & 3), ROWS - 1);
         const s16x8 ones = __builtin_bit_cast(s16x8, (u32x4){T::ONES, T::ONES, T::ONES, T::ONES});
 
-        const int code_at = X_STEP + wv * RT * 1024 + r * 64 + ((g ^ (r >> 2)) << 4);
+        const int code_at = X_STEP + wv * RT * 1024 + r * 64 + ((g ^ swz(r >> 2)) << 4);
         auto work = [&](int step, int in) {   // in: the stage's place in the slab
             // everything is requested from LDS before the codes are taken apart
             const uint8_t* const at = smem + step % RING * STEP;
@@ -224,7 +228,7 @@ __global__ __launch_bounds__(64 * (WORKERS + LOADERS)) void w4_kernel(W4Args a) 
             for (int j = 0; j < 4; ++j)
 #pragma unroll
                 for (int t = 0; t < NT; ++t)
-                    xv[j][t] = *reinterpret_cast<const s16x8*>(x + xrow[t] * X_ROW + (((4 * j + g) ^ (xrow[t] & 15)) << 4));
+                    xv[j][t] = *reinterpret_cast<const s16x8*>(x + xrow[t] * X_ROW + (((4 * j + g) ^ swz(xrow[t])) << 4));
 #pragma unroll
             for (int w = 0; w < RT; ++w) {
                 __builtin_memcpy(sc[w], __builtin_assume_aligned(slab[w].s + (r * SLAB + in) * NG, 2 * NG), 2 * NG);
@@ -322,8 +326,8 @@ hipError_t launch_tiles(const W4Args& a, hipStream_t st) {
 // 7.6, in room for 8 8.0, of 65536 x 2048 23.7 against 25.1). With more than 16 rows one workgroup fits a
 // CU. Two wavefronts on rows make the most workgroups, and the shortest where those are one round of
 // the CUs at most (32 rows of 5120 x 5120 15.0 us against 24.5, of 8192 x 8192 20.6 against 37); beyond,
-// four with two tiles each read x a quarter as often (16384 x 5120 26.2 against 29.6, 65536 x 2048
-// 28.5 against 69.5, 64 rows of 8192 x 2048 12.8 against 18.1).
+// four with two tiles each read x a quarter as often (16384 x 5120 26.1 against 29.6, 65536 x 2048
+// 26.9 against 69, 64 rows of 8192 x 2048 12.5 against 18.1).
 template <typename T, int G, bool GATED>
 hipError_t launch_w4(const W4Args& a, hipStream_t st) {
     if (a.m <= 4) return launch_tiles<T, G, 4, 4, 2, 1, 4, GATED>(a, st);
