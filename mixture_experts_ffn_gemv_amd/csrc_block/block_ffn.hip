@@ -25,7 +25,7 @@
 // k consecutive), 1.32 or 1.16 (as in DX and DW). A round of whole tiles runs at 1.3; the rest
 // is the last round, which is not full, and DH's epilogue: it reads 151 MB of g and u and
 // writes 113 MB of dg, du and h, after the products of its tile. Counters: no LDS
-// conflicts, matrix cores busy 0.58 (GATEUP) and 0.47 (DW) of the cycles.
+// conflicts, matrix cores busy 0.59 (GATEUP) and 0.48 (DW) of the cycles.
 // Few rows are bound by the weights' bytes: one token of 5120 x 2304 20.2 us, 70.8 MB, 3.5 TB/s.
 #include "block_common.h"
 
