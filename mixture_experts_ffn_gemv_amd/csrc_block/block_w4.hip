@@ -107,13 +107,16 @@ struct SlabTile {
     uint8_t z[16 * NG * SLAB];
 };
 
+// results of a lane for tile t of x that are any token's
+constexpr int results_of(int rows, int t) { return rows - 16 * t <= 4 ? 1 : rows - 16 * t <= 8 ? 2 : 4; }
+
 // ROWS: rows of x there is room for. WK, WR: parts of the columns, workers on each. RT: tiles of a
 // worker. RING: steps in LDS
 template <typename T, int G, int ROWS, int WK, int WR, int RT, int RING, bool GATED>
 __global__ __launch_bounds__(64 * (WORKERS + LOADERS)) void w4_kernel(W4Args a) {
     static_assert(WK * WR == WORKERS, "");
     constexpr int NG = STAGE / G, NT = (ROWS + 15) / 16, TOK = 16 * NT, COLS = GATED ? 8 : 16;   // COLS: results per token and tile
-    constexpr int IR = ROWS <= 4 ? 1 : ROWS <= 8 ? 2 : 4;   // results per lane and tile of x: tokens g + 4 i, i < IR
+    constexpr int IR = results_of(ROWS, 0);   // results per lane and tile of x: tokens g + 4 i, i < IR
     constexpr int X_ROW = STAGE * 2, X_STEP = WK * ROWS * X_ROW, STEP = X_STEP + WORKERS * RT * 1024;
     // RING steps of x [part][row][128] and codes [worker][tile][16 rows][64 bytes]; slabs [worker][tile];
     // then the sums [part][tile][token][16 rows]
@@ -260,7 +263,7 @@ __global__ __launch_bounds__(64 * (WORKERS + LOADERS)) void w4_kernel(W4Args a) 
 #pragma unroll
                         for (int t = 0; t < NT; ++t)
 #pragma unroll
-                            for (int i = 0; i < IR; ++i) sum[w][t][i] = fmaf(s1, fmaf(-z1, sx[t][i], acc[w][t][i]), sum[w][t][i]);
+                            for (int i = 0; i < results_of(ROWS, t); ++i) sum[w][t][i] = fmaf(s1, fmaf(-z1, sx[t][i], acc[w][t][i]), sum[w][t][i]);
                     }
                 }
             }
@@ -284,7 +287,7 @@ __global__ __launch_bounds__(64 * (WORKERS + LOADERS)) void w4_kernel(W4Args a) 
 #pragma unroll
             for (int t = 0; t < NT; ++t)
 #pragma unroll
-                for (int i = 0; i < IR; ++i)
+                for (int i = 0; i < results_of(ROWS, t); ++i)
                     red[(((wk * WR + wr) * RT + q) * TOK + 16 * t + g + 4 * i) * 16 + r] = sum[q][t][i];
     }
     __syncthreads();
@@ -321,9 +324,10 @@ hipError_t launch_tiles(const W4Args& a, hipStream_t st) {
     return launch_kernel(w4_kernel<T, G, ROWS, WK, WR, RT, RING, GATED>, grid, dim3(64 * (WORKERS + LOADERS)), lds, st, a);
 }
 
-// LDS room for 4, 8, 16 or 32 rows of x, since a step's x is loaded whether its rows exist or not (8 rows
+// LDS room for 4, 8, 16, 24 or 32 rows of x, since a step's x is loaded whether its rows exist or not (8 rows
 // of 5120 x 5120, group 64: 7.8 us, in room for 16 rows 9.6; 16 rows 9.6, in room for 32 14.8; 1 row
-// 7.6, in room for 8 8.0, of 65536 x 2048 23.7 against 25.1). With more than 16 rows one workgroup fits a
+// 7.6, in room for 8 8.0, of 65536 x 2048 23.7 against 25.1; 20 rows 13.1, in room for 32 15.5, of 65536 x
+// 2048 25.7 against 26.6). With more than 16 rows one workgroup fits a
 // CU. Two wavefronts on rows make the most workgroups, and the shortest where those are one round of
 // the CUs at most (32 rows of 5120 x 5120 15.0 us against 24.5, of 8192 x 8192 20.6 against 37); beyond,
 // four with two tiles each read x a quarter as often (16384 x 5120 26.1 against 29.6, 65536 x 2048
@@ -335,6 +339,8 @@ hipError_t launch_w4(const W4Args& a, hipStream_t st) {
     if (a.m <= 16) return launch_tiles<T, G, 16, 4, 2, 1, 4, GATED>(a, st);
     constexpr int COLS = 2 * (GATED ? 8 : 16);
     const int64_t blocks = (int64_t)((a.N + COLS - 1) / COLS) * ((a.m + MAX_ROWS_X - 1) / MAX_ROWS_X);
+    if (a.m <= 24)
+        return blocks <= 256 ? launch_tiles<T, G, 24, 4, 2, 1, 4, GATED>(a, st) : launch_tiles<T, G, 24, 2, 4, 2, 3, GATED>(a, st);
     if (blocks <= 256) return launch_tiles<T, G, 32, 4, 2, 1, 3, GATED>(a, st);
     return launch_tiles<T, G, 32, 2, 4, 2, 3, GATED>(a, st);
 }

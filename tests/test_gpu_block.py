@@ -411,7 +411,8 @@ W4 = [(1, 16, 32, 32, True, BF16), (1, 1, 128, 128, False, F16), (2, 33, 96, 32,
       (5, 48, 1024, 128, False, BF16), (8, 17, 160, 32, False, F16), (9, 64, 2304, 128, True, F16),
       (16, 31, 320, 64, True, BF16), (17, 80, 4096, 32, True, BF16), (32, 47, 192, 64, False, F16),
       (33, 16, 1280, 128, True, BF16), (64, 65, 256, 32, True, F16), (65, 40, 512, 64, True, BF16),
-      (150, 24, 1152, 128, False, BF16), (1, 50, 65536, 64, True, BF16)]
+      (150, 24, 1152, 128, False, BF16), (1, 50, 65536, 64, True, BF16),
+      (24, 33, 640, 32, True, F16), (20, 48, 896, 128, False, BF16)]
 
 
 @pytest.mark.parametrize("m,rows,cols,group,zeros,dtype", W4)
@@ -426,7 +427,7 @@ def test_w4_matmul_against_float64(m, rows, cols, group, zeros, dtype):
         assert untouched(y)
 
 
-W4_MANY = [(17, 8225, 160, 32, True, BF16), (70, 2740, 256, 64, False, F16), (32, 8200, 384, 128, True, F16)]
+W4_MANY = [(17, 8225, 160, 32, True, BF16), (24, 8196, 192, 64, True, BF16), (27, 8210, 96, 32, False, BF16), (70, 2740, 256, 64, False, F16), (32, 8200, 384, 128, True, F16)]
 
 
 @pytest.mark.parametrize("m,rows,cols,group,zeros,dtype", W4_MANY)
@@ -440,7 +441,7 @@ def test_w4_gated_of_many_workgroups_against_float64(m, rows, cols, group, zeros
 
 
 @pytest.mark.parametrize("act,limit", [("silu", 0.0), ("silu", 0.5), ("gelu", 0.0)])
-@pytest.mark.parametrize("m,rows,cols,group,zeros,dtype", [W4[i] for i in (0, 3, 6, 8, 11, 12)])
+@pytest.mark.parametrize("m,rows,cols,group,zeros,dtype", [W4[i] for i in (0, 3, 6, 8, 11, 12, 15, 16)])
 def test_w4_gated_against_float64(m, rows, cols, group, zeros, dtype, act, limit):
     cg, cu = (w4_case(rows, cols, group, zeros, dtype, seed=s) for s in (rows, cols + 1))
     x = ref.normal(ref.generator(m), (m, cols), dtype)
