@@ -710,10 +710,10 @@ hipError_t launch_skinny(const FfnArgs& a, hipStream_t st) {
 // GATEUP or DOWN of the forward pass. Few rows go by weight rows, more in tiles: 32 rows of 5120 x
 // 2304 (D x I, both products) take 36.5 against 39.6 us, of 8192 x 2048 33.8 against 46.0, of 1024 x
 // 1024 11.6 against 22.2 (of 8192 x 8192 114.8 against 108.3). Above 32 rows a workgroup's slabs of x
-// (96 KB and more) leave a CU room for one workgroup, and where there are more of them than CUs
-// tiles are faster: 48 rows of 5120 x 2304 41.7 against 47.6, of 8192 x 8192 110 against 145; with
-// fewer they are not: of 2048 x 2048 29.0 against 17.3, 64 rows 29.4 against 19.5; nor are they with 48
-// rows and 2^24 weights at most: DOWN of 8192 x 2048 17.7 against 17.2.
+// (80 KB and more) leave a CU room for two workgroups or one, and where there are more of them than CUs
+// tiles are faster: 48 rows of 5120 x 2304 41.7 against 47.6, of 8192 x 8192 110 against 145, 40 rows
+// 120 against 131; with fewer they are not: 48 rows of 2048 x 2048 29.0 against 17.3, 64 rows 29.4
+// against 19.5; nor are they with 48 rows and 2^24 weights at most: DOWN of 8192 x 2048 17.7 against 17.2.
 template <typename T, Kind KIND>
 hipError_t launch_forward(const FfnArgs& a, float* partial, hipStream_t st) {
     const int blocks = KIND == GATEUP ? cdiv(a.I, 8) : cdiv(a.D, 16);
@@ -726,7 +726,11 @@ hipError_t launch_forward(const FfnArgs& a, float* partial, hipStream_t st) {
         return launch_kernel(ffn_few_kernel<T, KIND>, dim3(blocks), dim3(64 * SKINNY_WAVES),
                              std::max<size_t>(whole, sizeof(float) * SKINNY_WAVES * 256), st, a);
     if (a.m <= 16) return launch_skinny<T, KIND, 16>(a, st);
+    // (room for 24 and 40 rows: 20 rows of 5120 x 2304 33.8 against 35.1 us in room for 32, 36 rows of 8192
+    // x 2048 36.6 against 40.3 in room for 48, which two workgroups of a CU do not have)
+    if (a.m <= 24) return launch_skinny<T, KIND, 24>(a, st);
     if (a.m <= 32) return launch_skinny<T, KIND, 32>(a, st);
+    if (a.m <= 40) return launch_skinny<T, KIND, 40>(a, st);
     return a.m <= 48 ? launch_skinny<T, KIND, 48>(a, st) : launch_skinny<T, KIND, 64>(a, st);
 }
 

@@ -103,6 +103,12 @@ def test_ffn_same_bits_with_and_without_saving_and_again():
         assert torch.equal(a[k], b[k]), k
 
 
+@pytest.mark.parametrize("m,dim,inter", [(17, 2056, 520), (24, 520, 2056), (33, 1544, 264), (40, 264, 1544), (41, 520, 776)])
+def test_ffn_few_rows_by_weight_rows_against_float64(m, dim, inter):
+    # the edges of what a workgroup has room for, k past the last whole slab
+    test_ffn_few_rows_in_tiles_against_float64(m, dim, inter)
+
+
 @pytest.mark.parametrize("m,dim,inter", [(50, 4136, 72), (35, 4072, 2064), (64, 4104, 2088)])
 def test_ffn_few_rows_in_tiles_against_float64(m, dim, inter):
     # more workgroups than CUs if split by weight rows: the second product, the first, both in tiles
