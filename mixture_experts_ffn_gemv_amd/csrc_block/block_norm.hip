@@ -286,7 +286,8 @@ __global__ __launch_bounds__(MAXT) void norm_backward_kernel(NormArgs a) {
         for (int i = 0; i < V; ++i) s_post[j][i] = s_pre[j][i] = 0.f;
     }
     for (int turn = 0; row < a.m; row += step, turn ^= 1) {
-        // t: r'; yn: y rs1; d: dn, then b = w_post dp; e: dr_out, then e
+        // t: r'; yn: y rs1; d: dn, then b = w_post dp; e: dr_out, then e. With no norm after r', or no
+        // gradient of it, w_pre and r' read as zeros: what they hold must not reach e, finite or not
         float tv[C][V], yn[C][V], dv[C][V], ev[C][V];
         Raw<T> g_[C];   // this row's gate, as it lies in memory
         const float rs1 = has_post ? q.rs1 : 1.f, rs2 = has_pre ? q.rs2 : 0.f, gt = token ? T::load(q.gate) : 1.f;
@@ -300,12 +301,13 @@ __global__ __launch_bounds__(MAXT) void norm_backward_kernel(NormArgs a) {
             q.dr[j].template get<TAIL>(ev[j], skip[j], a.has_dr);
             keep(wp[j]), keep(wn[j]);
             wp[j].template get<WHOLE>(w, skip[j]);
-            wn[j].template get<WHOLE>(n, skip[j]);
+            wn[j].template get<WHOLE>(n, skip[j], has_pre);
             if (G != SCALAR) g_[j] = G == MOE_GATE_FULL ? q.g[j] : gc[j], keep(g_[j]), g_[j].template get<WHOLE>(g, skip[j]);
 #pragma unroll
             for (int i = 0; i < V; ++i) {
                 yn[j][i] *= rs1;
                 tv[j][i] = a.res_scale * tv[j][i] + (G != SCALAR ? g[i] : gt) * (has_post ? yn[j][i] * w[i] : yn[j][i]);
+                tv[j][i] = has_pre ? tv[j][i] : 0.f;
                 s += tv[j][i] * (n[i] * dv[j][i]);
             }
         }
@@ -317,7 +319,7 @@ __global__ __launch_bounds__(MAXT) void norm_backward_kernel(NormArgs a) {
             float w[V], n[V], g[V], o[V];
             keep(wp[j]), keep(wn[j]);
             wp[j].template get<WHOLE>(w, skip[j]);
-            wn[j].template get<WHOLE>(n, skip[j]);
+            wn[j].template get<WHOLE>(n, skip[j], has_pre);
             if (G != SCALAR) keep(g_[j]), g_[j].template get<WHOLE>(g, skip[j]);
 #pragma unroll
             for (int i = 0; i < V; ++i) {

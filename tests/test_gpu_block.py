@@ -348,6 +348,21 @@ def test_norm_keeps_what_is_not_finite_in_its_row():
     assert got["r_out"][5, 199] == float("inf") and torch.isnan(got["n"][5, 199])
 
 
+@pytest.mark.parametrize("gate", ["none", "channel", "token", "full"])
+@pytest.mark.parametrize("m,dim,dtype", [(8, 7, BF16), (8, 200, BF16), (9, 1111, F32), (8, 5120, F16), (8, 8200, BF16)])
+@pytest.mark.parametrize("without", ["w_pre", "dn"])
+def test_norm_backward_with_nothing_after_the_residual_does_not_read_it(without, m, dim, dtype, gate):
+    # e = dr_out there: no gradient depends on r, whatever r holds
+    c = norm_case(m, dim, dtype, gate, seed=dim, pre=without == "dn")
+    c["dn"] = None
+    clean = norm_run(c, 0.5)
+    c["r"][0, 3], c["r"][0, dim - 1], c["r"][5, 2], c["r"][7, 1] = float("inf"), float("nan"), float("-inf"), float("nan")
+    got = norm_run(c, 0.5)
+    for k in set(got) - {"r_out", "n"}:
+        assert torch.isfinite(got[k]).all(), k
+        assert torch.equal(got[k], clean[k]), k
+
+
 def test_norm_of_no_rows():
     c = norm_case(0, 72, F16, "channel", seed=1)
     got = norm_run(c, 1.0)
