@@ -605,9 +605,11 @@ int moe_norm_backward(const moe_norm* f, const void* r, int64_t ldr, const void*
     if (!sums) return MOE_OK;
     const dim3 grid((f->dim + 31) / 32, 2);
     const float* part = reinterpret_cast<const float*>(work);
-    const void* const channel = gate_kind == MOE_GATE_CHANNEL ? gate : nullptr;
+    // (no rows: zeros, whatever the factors hold)
+    const void* const channel = gate_kind == MOE_GATE_CHANNEL && m > 0 ? gate : nullptr;
+    const void* const w_post = m > 0 ? f->w_post : nullptr;
     auto* const k = f->dtype == MOE_BF16 ? norm_sums_kernel<Bf16> : f->dtype == MOE_F16 ? norm_sums_kernel<F16> : norm_sums_kernel<F32>;
-    return status_of(launch_kernel(k, grid, dim3(1024), 0, st, part, backward_blocks(p, m), f->dim, channel, f->w_post, dw_post,
+    return status_of(launch_kernel(k, grid, dim3(1024), 0, st, part, backward_blocks(p, m), f->dim, channel, w_post, dw_post,
                                    d_channel, dw_pre));
 }
 

@@ -370,6 +370,15 @@ def test_norm_of_no_rows():
         assert not got[k].any(), k
 
 
+@pytest.mark.parametrize("value", [float("inf"), float("nan")])
+def test_norm_of_no_rows_with_weights_that_are_not_finite(value):
+    c = norm_case(0, 72, F32, "channel", seed=1)
+    c["gate"][3], c["w_post"][5] = value, value
+    got = norm_run(c, 1.0)
+    for k in ("dgate", "dw_post", "dw_pre"):
+        assert torch.isfinite(got[k]).all() and not got[k].any(), k
+
+
 def test_norm_same_bits_again_on_a_stream_and_in_a_graph():
     c = norm_case(700, 1024, BF16, "channel", seed=2)
     want = norm_run(c, 1.0)
