@@ -67,8 +67,15 @@ struct F32 {
     static MOE_DEV bits store(float f) { return f; }
 };
 
-// act(v) and its derivative. SILU: v s(v), s the logistic function. GELU: the tanh
-// form. Beyond |v| = 100 tanh is 1 to the last bit, and the argument is held
+// the clamps of the gated product, which keep a NaN (limit <= 0: none)
+MOE_DEV float clamp_gate(float g, float limit) { return limit > 0.f && g > limit ? limit : g; }
+MOE_DEV float clamp_up(float u, float limit) {
+    if (limit > 0.f) u = u > limit ? limit : (u < -limit ? -limit : u);
+    return u;
+}
+
+// act(v) and its derivative, NaN where v is. SILU: v s(v), s the logistic function. GELU:
+// the tanh form. Beyond |v| = 100 tanh is 1 to the last bit, and the argument is held
 // there so that v^3 does not overflow.
 MOE_DEV float act_value(float v, int act) {
     if (act == MOE_ACT_SILU) return v / (1.0f + __expf(-v));
@@ -83,19 +90,12 @@ MOE_DEV void act_both(float v, int act, float& a, float& da) {
         da = s * (1.f + v * (1.f - s));
         return;
     }
-    const float c = fminf(fmaxf(v, -100.f), 100.f);
+    const float c = clamp_up(v, 100.f);   // (fminf and fmaxf would make a number of a NaN)
     const float z = 0.7978845608028654f * (c + 0.044715f * c * c * c);
     // (1 + tanh z) / 2 and (1 - tanh z) / 2, neither as a difference
     const float s = 1.f / (1.f + __expf(-2.f * z)), q = 1.f / (1.f + __expf(2.f * z));
     a = v * s;
     da = s + 2.f * c * s * q * 0.7978845608028654f * (1.f + 0.134145f * c * c);
-}
-
-// the clamps of the gated product, which keep a NaN (limit <= 0: none)
-MOE_DEV float clamp_gate(float g, float limit) { return limit > 0.f && g > limit ? limit : g; }
-MOE_DEV float clamp_up(float u, float limit) {
-    if (limit > 0.f) u = u > limit ? limit : (u < -limit ? -limit : u);
-    return u;
 }
 
 inline bool aligned_to(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }

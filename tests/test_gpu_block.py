@@ -188,6 +188,22 @@ def test_ffn_keeps_a_nan_in_its_row():
     assert torch.equal(y[rest], clean[rest])
 
 
+@pytest.mark.parametrize("m", [5, 70])
+@pytest.mark.parametrize("act,limit", [("silu", 0.0), ("gelu", 0.0), ("gelu", 1.0)])
+def test_ffn_backward_keeps_a_nan_of_one_gate(act, limit, m):
+    # one row of Wg is NaN: g is NaN in that column alone, and so are dg and du
+    c = list(ffn_case(m, 72, 136, F16, act, limit, seed=m))
+    clean = ffn_run(c)
+    c[2] = c[2].clone()
+    c[2][37] = float("nan")
+    got = ffn_run(c)
+    rest = torch.arange(136, device=DEV) != 37
+    for k in ("dw_gate", "dw_up"):
+        assert torch.isnan(got[k][37]).all(), k
+        assert torch.equal(got[k][rest], clean[k][rest]), k
+    assert torch.isnan(got["dw_down"][:, 37]).all() and torch.isnan(got["dx"]).all()
+
+
 def test_ffn_gradient_against_differences():
     # (loss(x + e v) - loss(x - e v)) / 2e for loss = <dy, y>, along v = the gradient's own direction, at e = 1/16 and
     # 1/32 of |x|, joined so that the cubic term cancels: y's rounding (2^-11, independent) is far below the difference
