@@ -481,10 +481,10 @@ __global__ __launch_bounds__(64 * SKINNY_WAVES) void ffn_few_kernel(FfnArgs a) {
     const uint8_t* x = smem + xt * row_bytes;
     f32x4 acc[1] = {{0.f, 0.f, 0.f, 0.f}};
     auto multiply = [&](int i, int c) {
-        // a weight that stands in for one past K, or past this wavefront's part, is not one
-        const uint32_t on = c < c1 && 32 * c + 8 * g < K ? ~0u : 0u;
+        // a weight that stands in for one past K is not one (x is zero there)
+        const uint32_t on = 32 * c + 8 * g < K ? ~0u : 0u;
         const u32x4 wm = {wq[i].x & on, wq[i].y & on, wq[i].z & on, wq[i].w & on};
-        const int cx = min(c, chunks - 1) * 4 + g;
+        const int cx = c * 4 + g;
         acc[0] = T::mfma(__builtin_bit_cast(s16x8, wm), *reinterpret_cast<const s16x8*>(x + ((cx ^ (xt & 15)) << 4)), acc[0]);
     };
     int c = c0;
@@ -495,7 +495,8 @@ __global__ __launch_bounds__(64 * SKINNY_WAVES) void ffn_few_kernel(FfnArgs a) {
             request(i, c + AHEAD + i);
         }
 #pragma unroll
-    for (int i = 0; i < AHEAD; ++i) multiply(i, c + i);
+    for (int i = 0; i < AHEAD; ++i)
+        if (c + i < c1) multiply(i, c + i);   // (a chunk of another's part is left out: its x times a zero weight is NaN if infinite)
     skinny_finish<T, KIND, 1, 64 * SKINNY_WAVES>(a, reinterpret_cast<float*>(smem), n0, acc);
 }
 

@@ -204,6 +204,26 @@ def test_ffn_backward_keeps_a_nan_of_one_gate(act, limit, m):
     assert torch.isnan(got["dw_down"][:, 37]).all() and torch.isnan(got["dx"]).all()
 
 
+@pytest.mark.parametrize("m,dim,inter", [(1, 264, 264), (3, 40, 1040), (6, 1544, 520), (16, 512, 264), (20, 520, 264), (70, 264, 136)])
+def test_ffn_of_infinite_values(m, dim, inter):
+    # an infinity of x under positive weights: g and u are clamped, as they are with a large x. Without clamps h is
+    # infinite, and so is y under positive weights
+    for at in (0, dim // 2, dim - 1):
+        c = list(ffn_case(m, dim, inter, BF16, "silu", 10.0, seed=m))
+        c[2], c[3], c[4] = (t.abs() + 0.01 for t in c[2:5])
+        clean, row = ffn_run(c, backward=False)["y"], m // 2
+        c[0] = c[0].clone()
+        c[0][row, at] = 1e6
+        large = ffn_run(c, backward=False)["y"]
+        c[0][row, at] = float("inf")
+        y = ffn_run(c, backward=False)["y"]
+        assert torch.isfinite(y).all() and torch.equal(y, large), at
+        c[6] = 0.0
+        assert (ffn_run(c, backward=False)["y"][row] == float("inf")).all(), at
+        rest = torch.arange(m, device=DEV) != row
+        assert torch.equal(y[rest], clean[rest]), at
+
+
 def test_ffn_gradient_against_differences():
     # (loss(x + e v) - loss(x - e v)) / 2e for loss = <dy, y>, along v = the gradient's own direction, at e = 1/16 and
     # 1/32 of |x|, joined so that the cubic term cancels: y's rounding (2^-11, independent) is far below the difference
