@@ -373,9 +373,10 @@ typedef struct moe_ffn {
 } moe_ffn;
 
 /* Bytes that calls with m rows need: `forward` and `backward`, the workspaces of
- * the two calls (operands between the products and sums of split products), and `saved`, what a forward call leaves for its backward call
- * (g and u in f32). Each a multiple of 256, possibly 0. MOE_EINVAL for a bad
- * description, m < 0, m > 2^24 or NULL. */
+ * the two calls (operands between the products, and up to 64 MiB for the sums of split
+ * products), and `saved`, what a forward call leaves for its backward call (g and u in
+ * f32). Each a multiple of 256, possibly 0, and enough for any fewer rows too.
+ * MOE_EINVAL for a bad description, m < 0, m > 2^24 or NULL. */
 int moe_ffn_workspace(const moe_ffn* f, int32_t m, size_t* forward, size_t* saved, size_t* backward);
 
 /* y = block(x) for m rows. x [m, D] with row stride ldx, y [m, D] with row stride
@@ -421,7 +422,7 @@ typedef struct moe_norm {
     const void* w_pre;   /* device, [dim], or NULL: no norm before the next one (n must then be NULL) */
 } moe_norm;
 
-/* Workspace bytes of moe_norm_backward for m rows. MOE_EINVAL for a bad
+/* Workspace bytes of moe_norm_backward for m rows or fewer. MOE_EINVAL for a bad
  * description, m < 0 or NULL. */
 int moe_norm_workspace(const moe_norm* f, int32_t m, size_t* backward);
 

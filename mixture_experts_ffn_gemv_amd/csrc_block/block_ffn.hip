@@ -594,12 +594,38 @@ __global__ __launch_bounds__(64 * (SKINNY_WAVES + SKINNY_LOADERS)) void ffn_skin
 int cdiv(int a, int b) { return (a + b - 1) / b; }
 
 // Tiles of B x B, B = 256 (eight wavefronts, one workgroup per CU) or 128 (four, two per CU)
-constexpr int N_CU = 256;
+constexpr int N_CU = 256, MAX_SPLITS = 16;
 struct Product {
     Plan plan;
     int tile;         // 256 or 128
-    size_t bytes;     // of plan.partial
 };
+// tiles along q and p, all of them, K steps of one, and how many the CUs hold at a time. DW: of
+// `products` outputs
+struct Extent {
+    int nq, np, tiles, steps, slots;
+};
+Extent extent(Kind kind, int m, int D, int I, int products, int B) {
+    Extent e;
+    e.steps = kind == DX ? 2 * cdiv(I, BK) : cdiv(kind == DOWN ? I : kind == DW ? m : D, BK);
+    if (kind == DW) e.nq = cdiv(I, B), e.np = cdiv(D, B);
+    else e.nq = cdiv(m, B), e.np = cdiv(kind == GATEUP ? 2 * I : kind == DH ? I : D, B);
+    e.tiles = e.nq * e.np * (kind == DW ? products : 1);
+    e.slots = B == 256 ? N_CU : 2 * N_CU;
+    return e;
+}
+// Bytes that hold the split tiles' sums of any plan for m rows or fewer: the parts are at most the
+// slots, and at most the tiles times the splits. (The sums of one plan jump with m: 6.8 MB for
+// 1536 rows of 5120 x 2304, 58 MB for 1000, so that a workspace of just that size would be too
+// small for a smaller batch. This is 64 MiB at most.)
+size_t partial_bytes(Kind kind, int m, int D, int I, int products) {
+    size_t most = 0;
+    for (int B : {256, 128}) {
+        const Extent e = extent(kind, m, D, I, products, B);
+        const int splits = std::min(MAX_SPLITS, e.steps / 2);
+        if (splits >= 2) most = std::max(most, (size_t)std::min<int64_t>(e.slots, (int64_t)e.tiles * splits) * B * B * sizeof(float));
+    }
+    return most;
+}
 
 // How a product is cut up: 256 x 256 or 128 x 128 tiles, and by how much the tiles past the last full
 // round of the CUs are split along k. Costs in units of one K step of a 256 x 256 tile on a CU
@@ -607,35 +633,26 @@ struct Product {
 // of the rate); the split tiles' sums pass through memory twice (0.06 a 256 x 256 tile and split, and 4 for
 // the second launch). 8192 rows of 5120 x 2304 in the large tiles and in the small: GATEUP 334 and
 // 377 us, DOWN 187 and 196, DH 266 and 271, DX 346 and 422, DW 533 and 624.
-Product plan_product(Kind kind, int m, int D, int I, int wide, bool down) {
+Product plan_product(Kind kind, int m, int D, int I, int products) {
     Product best{};
     double best_cost = 1e30;
     for (int B : {256, 128}) {
+        const Extent e = extent(kind, m, D, I, products, B);
         Product p{};
         p.tile = B;
-        const int steps = kind == DX ? 2 * cdiv(I, BK) : cdiv(kind == DOWN ? I : kind == DW ? m : D, BK);
-        int tiles;
-        if (kind == DW) {
-            p.plan.nq = cdiv(I, B), p.plan.np = cdiv(D, B);
-            tiles = p.plan.nq * p.plan.np * (wide + (down ? 1 : 0));
-        } else {
-            p.plan.nq = cdiv(m, B), p.plan.np = cdiv(kind == GATEUP ? 2 * I : kind == DH ? I : D, B);
-            tiles = p.plan.nq * p.plan.np;
-        }
-        const int slots = B == 256 ? N_CU : 2 * N_CU;
+        p.plan.nq = e.nq, p.plan.np = e.np;
         const double step = B == 256 ? 1 : 0.66, share = B == 256 ? 0.06 : 0.015;   // (two workgroups share a CU)
-        const int rounds = tiles / slots, rest = tiles % slots;
-        double cost = rounds * (double)steps * step;
-        p.plan.whole = tiles, p.plan.splits = 1;
+        const int rounds = e.tiles / e.slots, rest = e.tiles % e.slots;
+        double cost = rounds * (double)e.steps * step;
+        p.plan.whole = e.tiles, p.plan.splits = 1;
         if (rest > 0) {
-            double tail = steps * step;
-            for (int s = 2; s <= 16 && s * 2 <= steps && rest * s <= slots; ++s) {
-                const double t = cdiv(steps, s) * step + 4 + share * rest * s;
-                if (t < tail) tail = t, p.plan.whole = tiles - rest, p.plan.rest = rest, p.plan.splits = s;
+            double tail = e.steps * step;
+            for (int s = 2; s <= MAX_SPLITS && s * 2 <= e.steps && rest * s <= e.slots; ++s) {
+                const double t = cdiv(e.steps, s) * step + 4 + share * rest * s;
+                if (t < tail) tail = t, p.plan.whole = e.tiles - rest, p.plan.rest = rest, p.plan.splits = s;
             }
             cost += tail;
         }
-        p.bytes = p.plan.rest > 0 ? (size_t)p.plan.rest * p.plan.splits * B * B * sizeof(float) : 0;
         if (cost < best_cost) best_cost = cost, best = p;
     }
     return best;
@@ -654,12 +671,13 @@ hipError_t launch_tiles(const FfnArgs& a, const Plan& plan, hipStream_t st) {
 
 template <typename T, Kind KIND>
 hipError_t launch_product(const FfnArgs& a, float* partial, hipStream_t st) {
-    Product p = plan_product(KIND, a.m, a.D, a.I, (a.dwg != nullptr) + (a.dwu != nullptr), a.dwd != nullptr);
+    Product p = plan_product(KIND, a.m, a.D, a.I, (a.dwg != nullptr) + (a.dwu != nullptr) + (a.dwd != nullptr));
     p.plan.partial = partial;
     return p.tile == 256 ? launch_tiles<T, KIND, 256, 2, 4>(a, p.plan, st) : launch_tiles<T, KIND, 128, 2, 2>(a, p.plan, st);
 }
 
 constexpr int MAX_M = 1 << 24;
+constexpr int TILES_ABOVE = 32;   // as many rows or fewer of a forward pass never go in tiles
 
 int check_ffn(const moe_ffn* f) {
     if (f == nullptr) return MOE_EINVAL;
@@ -680,13 +698,12 @@ bool rows_ok(const void* p, int64_t ld, int dim) {
 size_t rows_bytes(const moe_ffn* f, int m) { return round_up((size_t)m * f->inter * 2, 256); }
 // room for the split tiles' sums of the products of one direction, whichever outputs are wanted
 size_t forward_partial(const moe_ffn* f, int m) {
-    return std::max(plan_product(GATEUP, m, f->dim, f->inter, 0, false).bytes, plan_product(DOWN, m, f->dim, f->inter, 0, false).bytes);
+    if (m <= TILES_ABOVE) return 0;
+    return std::max(partial_bytes(GATEUP, m, f->dim, f->inter, 0), partial_bytes(DOWN, m, f->dim, f->inter, 0));
 }
 size_t backward_partial(const moe_ffn* f, int m) {
-    size_t b = std::max(plan_product(DH, m, f->dim, f->inter, 0, false).bytes, plan_product(DX, m, f->dim, f->inter, 0, false).bytes);
-    for (int wide = 0; wide <= 2; ++wide)
-        for (bool down : {false, true}) b = std::max(b, plan_product(DW, m, f->dim, f->inter, wide, down).bytes);
-    return b;
+    return std::max({partial_bytes(DH, m, f->dim, f->inter, 0), partial_bytes(DX, m, f->dim, f->inter, 0),
+                     partial_bytes(DW, m, f->dim, f->inter, 3)});
 }
 size_t forward_bytes(const moe_ffn* f, int m) { return rows_bytes(f, m) + forward_partial(f, m); }
 size_t backward_bytes(const moe_ffn* f, int m) { return 3 * rows_bytes(f, m) + backward_partial(f, m); }
@@ -719,7 +736,7 @@ template <typename T, Kind KIND>
 hipError_t launch_forward(const FfnArgs& a, float* partial, hipStream_t st) {
     const int blocks = KIND == GATEUP ? cdiv(a.I, 8) : cdiv(a.D, 16);
     const bool large = a.m > 48 || (size_t)(KIND == GATEUP ? 2 : 1) * a.D * a.I > 1 << 24;
-    if (a.m > 64 || (a.m > 32 && blocks > N_CU && large)) return launch_product<T, KIND>(a, partial, st);
+    if (a.m > 64 || (a.m > TILES_ABOVE && blocks > N_CU && large)) return launch_product<T, KIND>(a, partial, st);
     // up to 16 rows that fit into LDS whole: one row of 5120 x 2304 21.8 against 27.7 us in slabs, of
     // 8192 x 2048 23.7 against 27.0, 16 rows of 1024 x 1024 7.9 against 11.4
     const size_t whole = a.m * (size_t)few_row(KIND == GATEUP ? a.D : a.I);

@@ -139,6 +139,20 @@ def test_norm_arguments_are_refused(lib):
     assert norm_forward(lib, f, m=0, r=None, y=None, r_out=None, n=None) == moe.MOE_OK
 
 
+@pytest.mark.parametrize("dim,inter", [(8, 8), (64, 128), (1544, 4104), (5120, 2304), (8192, 2048), (16384, 16384)])
+def test_workspaces_fit_fewer_rows(lib, dim, inter):
+    # what is enough for m rows is enough for any fewer: a program sizes its workspace once, for its largest batch
+    f, n, size = ctypes.byref(ffn(dim=dim, inter=inter)), ctypes.byref(norm(dim=dim)), ctypes.c_size_t()
+    rows = sorted({*range(0, 300), *range(300, 9000, 37), 1000, 1536, 8192, 1 << 20, 1 << 24})
+    last = (0, 0, 0, 0)
+    for m in rows:
+        rc, *sizes = ffn_sizes(lib, f, m)
+        assert rc == moe.MOE_OK and lib.moe_norm_workspace(n, m, ctypes.byref(size)) == moe.MOE_OK
+        sizes.append(size.value)
+        assert all(a <= b and b % 256 == 0 for a, b in zip(last, sizes)), m
+        last = sizes
+
+
 def w4(**kw):
     v = dict(rows=48, cols=256, group=64, dtype=moe.MOE_BF16, codes=P, scales=P, zeros=None)
     v.update(kw)

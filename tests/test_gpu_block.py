@@ -165,6 +165,27 @@ def test_ffn_on_another_stream_and_in_a_graph():
             assert torch.equal(t, want[k]), k
 
 
+def test_ffn_workspace_of_a_larger_batch():
+    # one workspace, sized for the most rows, in calls of fewer; nothing past what moe_ffn_workspace says is written
+    dim, inter, most = 520, 264, 1536
+    c = ffn_case(most, dim, inter, BF16, "silu", 10.0, seed=1)
+    w = [t.to(DEV) for t in c[2:5]]
+    f = moe.make_ffn(*w, act="silu", limit=10.0)
+    sizes = [moe.moe_ffn_workspace(f, most)[i] for i in range(3)]
+    kept = [workspace(n + 256) for n in sizes]
+    forward, saved, backward = (k[:n] for k, n in zip(kept, sizes))
+    for m in (most, 1000, 300, 129, 128, 65, 40, 20, 3):
+        x, dy = (t[:m].to(DEV) for t in c[:2])
+        y, dx = torch.empty_like(x), torch.empty_like(x)
+        dw = [torch.empty_like(t) for t in w]
+        moe.moe_ffn_forward(f, x, y, forward, saved=saved)
+        moe.moe_ffn_backward(f, x, dy, saved, backward, dx=dx, dw_gate=dw[0], dw_up=dw[1], dw_down=dw[2])
+        want = ffn_run((c[0][:m], c[1][:m], *c[2:]))
+        for k, t in zip(("y", "dx", "dw_gate", "dw_up", "dw_down"), (y, dx, *dw)):
+            assert torch.equal(t, want[k]), (m, k)
+    assert all(bool((k[n:] == 0xFF).all()) for k, n in zip(kept, sizes))
+
+
 @pytest.mark.parametrize("act", ["silu", "gelu"])
 def test_ffn_saturated_activations(act):
     # gate values from -1e4 to 1e4: the activation is 0 or its argument, and its derivative 0 or 1
