@@ -407,7 +407,7 @@ def _rows(t, m, dim, dtype, where):
     ld, one = t.stride()
     if one != 1 and dim != 1:
         raise MoeError(MOE_EINVAL, where)
-    return t.data_ptr(), ld if m > 1 else max(ld, dim)
+    return t.data_ptr(), ld if m > 1 else dim   # (one row: its stride leads nowhere)
 
 
 def _whole(t, shape, dtype, where):

@@ -598,3 +598,34 @@ def test_w4_scales_at_any_place():
     zp = torch.zeros(163, dtype=torch.uint8, device=DEV)[3:].view(20, 8).copy_(c[2])
     moe.moe_w4_matmul(moe.make_w4(c[0].to(DEV), s, zp, group=32), x, z)
     assert torch.equal(y, z)
+
+
+# ------------------------------------------------------------------ rows of a larger tensor
+
+def test_one_row_of_any_stride():
+    # the last token of a sequence, [1, dim] out of [1, tokens, dim]: no second row lies anywhere
+    dim, inter, tokens = 64, 128, 70001
+    g = torch.Generator(device=DEV).manual_seed(3)
+    rnd = lambda *s: torch.randn(*s, generator=g, device=DEV).to(BF16)   # noqa: E731
+    last = rnd(1, tokens, dim)[:, -1]
+    odd = rnd(1, 2, 264)[:, 1, :dim].as_strided((1, dim), (1, 1))
+    assert last.stride(0) > 1 << 22 and odd.stride(0) < dim
+    f = moe.make_ffn(rnd(inter, dim), rnd(inter, dim), rnd(dim, inter))
+    nf, ns, nb = moe.moe_ffn_workspace(f, 1)
+    n = moe.make_norm(dim, BF16, w_post=rnd(dim), w_pre=rnd(dim))
+    c = w4_case(48, dim, 32, True, BF16, seed=1)
+    w = w4_make(c, 32)
+
+    def outputs(x):
+        y, dx, r, v, q, h = (torch.full((1, k), float("nan"), dtype=BF16, device=DEV) for k in (dim, dim, dim, dim, 48, 48))
+        saved = workspace(ns)
+        moe.moe_ffn_forward(f, x, y, workspace(nf), saved=saved)
+        moe.moe_ffn_backward(f, x, x, saved, workspace(nb), dx=dx)
+        moe.moe_norm_forward(n, x, x, r, v)
+        moe.moe_w4_matmul(w, x, q)
+        moe.moe_w4_gated(w, w, x, h)
+        return y, dx, r, v, q, h
+
+    for x in (last, odd):
+        for a, b in zip(outputs(x), outputs(x.clone().contiguous())):
+            assert torch.isfinite(a).all() and torch.equal(a, b)
