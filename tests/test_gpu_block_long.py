@@ -4,7 +4,8 @@ import pytest
 import torch
 
 import block_reference as ref
-from test_gpu_block import BF16, DEV, F16, ffn_run, untouched
+import mixture_experts_ffn_gemv_amd as moe
+from test_gpu_block import BF16, DEV, F16, F32, ffn_run, norm_run, untouched, workspace
 
 pytestmark = pytest.mark.gpu
 
@@ -65,3 +66,48 @@ def test_ffn_few_rows_in_slabs(m, dim, inter):
                                          (20, 16384, 16), (31, 16, 16384)])
 def test_ffn_more_rows_in_slabs(m, dim, inter):
     ffn_against_float64(m, dim, inter, BF16 if m % 2 else F16, "gelu", 0.0, extra=16)
+
+
+# ------------------------------------------------------------------ norms around a block
+
+def norm_case(m, dim, dtype, gate, seed):
+    g = generator(seed)
+    c = {k: normal(g, (m, dim), dtype, s) for k, s in (("r", 2.0), ("y", 1.0), ("dr_out", 1.0), ("dn", 1.0))}
+    c["w_post"], c["w_pre"] = (normal(g, (dim,), dtype, 0.2, 1.0) for _ in range(2))
+    shape = {"none": None, "channel": (dim,), "token": (m, 1), "full": (m, dim)}[gate]
+    c["gate"] = None if shape is None else normal(g, shape, dtype, 0.3, 0.5)
+    return c
+
+
+# At least three rows, one after another, for a thread: single values; several rows per wavefront, whole and with a shifted
+# last chunk; a wavefront per row; a workgroup per row with one, two and four chunks per thread, whole and shifted.
+# Past 32 MB an output is stored past the L2s: the last four
+NORM = [(1000003, 7, BF16, "token"), (130001, 64, BF16, "channel"), (61445, 100, F16, "full"), (80003, 257, F16, "channel"),
+        (16001, 512, BF16, "token"), (1601, 5120, BF16, "channel"), (1601, 8192, BF16, "token"), (1601, 5119, F16, "full"),
+        (4003, 1111, F32, "token"), (900, 16384, F16, "channel"),
+        (1601, 8193, F32, "channel"), (900, 16383, F32, "full"), (1100, 16384, BF16, "none"), (130001, 136, BF16, "channel")]
+
+
+@pytest.mark.parametrize("m,dim,dtype,gate", NORM)
+def test_norm_of_many_rows(m, dim, dtype, gate):
+    c, scale = norm_case(m, dim, dtype, gate, seed=dim), 0.7 if m % 2 else 1.0
+    with torch.device(DEV):
+        want = ref.norm(c["r"], c["y"], c["w_post"], c["w_pre"], c["gate"], 1e-6, scale, c["dr_out"], c["dn"])
+    for extra in (0, 3) if dim % 8 else (0, 8):
+        got = norm_run(c, scale, extra=extra)
+        agree(got, want, f"[{m}, {dim}] + {extra}")
+        for k in ("r_out", "n", "dr", "dy"):
+            assert untouched(got[k]), k
+
+
+@pytest.mark.parametrize("m,dim,dtype,gate", [NORM[i] for i in (1, 2, 4, 5, 7, 10, 13)])
+def test_norm_of_many_rows_in_place(m, dim, dtype, gate):
+    c = norm_case(m, dim, dtype, gate, seed=dim)
+    want = norm_run(c, 0.5)
+    f = moe.make_norm(dim, dtype, w_post=c["w_post"], w_pre=c["w_pre"], res_scale=0.5)
+    r, y, dr, dy = (c[k].clone() for k in ("r", "y", "dr_out", "dn"))
+    stats, work = torch.empty(m, 2, device=DEV), workspace(moe.moe_norm_workspace(f, m))
+    moe.moe_norm_forward(f, r, y, r, y, gate=c["gate"], stats=stats)
+    moe.moe_norm_backward(f, c["r"], c["y"], stats, dr, dy, work, gate=c["gate"], dr=dr, dy=dy)
+    for k, t in (("r_out", r), ("n", y), ("dr", dr), ("dy", dy)):
+        assert torch.equal(t, want[k]), k
