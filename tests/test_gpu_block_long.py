@@ -5,7 +5,7 @@ import torch
 
 import block_reference as ref
 import mixture_experts_ffn_gemv_amd as moe
-from test_gpu_block import BF16, DEV, F16, F32, ffn_run, norm_run, untouched, workspace
+from test_gpu_block import BF16, DEV, F16, F32, empty, ffn_run, norm_run, strided, untouched, w4_case, w4_make, workspace
 
 pytestmark = pytest.mark.gpu
 
@@ -111,3 +111,47 @@ def test_norm_of_many_rows_in_place(m, dim, dtype, gate):
     moe.moe_norm_backward(f, c["r"], c["y"], stats, dr, dy, work, gate=c["gate"], dr=dr, dy=dy)
     for k, t in (("r_out", r), ("n", y), ("dr", dr), ("dy", dy)):
         assert torch.equal(t, want[k]), k
+
+
+# ------------------------------------------------------------------ 4-bit weights
+
+# (m, rows, cols, group, zeros, type). More than 256 workgroups of more than 16 rows: two parts of the columns, three steps
+# in LDS, up to 17 steps and three slabs of scales. Then four parts, four or three steps, room for 4, 8, 16, 24 and 32
+# rows, up to 18 steps. The groups of a row are no multiple of eight, so that the last of a slab's pieces is moved
+W4 = [(17, 8225, 4256, 32, True, BF16), (24, 8225, 4288, 64, False, F16), (32, 8225, 4224, 128, True, F16),
+      (29, 8225, 4256, 32, True, F16), (70, 2740, 4288, 64, True, BF16),
+      (3, 100, 8352, 32, True, BF16), (4, 70, 8512, 64, False, F16), (8, 100, 8352, 32, True, F16), (6, 70, 8576, 128, True, BF16),
+      (16, 100, 8352, 32, True, BF16), (11, 70, 8512, 64, True, F16), (24, 100, 8352, 32, True, F16),
+      (20, 70, 8576, 128, False, BF16), (32, 100, 8352, 32, True, BF16), (27, 70, 8512, 64, True, F16),
+      (40, 70, 9088, 128, True, F16)]
+
+
+def w4_on_device(rows, cols, group, zeros, dtype, seed):
+    return [None if t is None else t.to(DEV) for t in w4_case(rows, cols, group, zeros, dtype, seed)]
+
+
+@pytest.mark.parametrize("m,rows,cols,group,zeros,dtype", W4)
+def test_w4_matmul_of_many_steps(m, rows, cols, group, zeros, dtype):
+    c = w4_on_device(rows, cols, group, zeros, dtype, seed=cols)
+    x = normal(generator(m), (m, cols), dtype)
+    v, e = ref.w4_product(x, *c, group)
+    y = empty(m, rows, dtype, 8 + rows % 2)
+    moe.moe_w4_matmul(w4_make(c, group), strided(x, 8), y)
+    ref.check(y, v.cpu(), (e + ref.U[dtype] * (v.abs() + e) + ref.TINY[dtype]).cpu(), f"[{m}, {cols}] x [{rows}]")
+    assert untouched(y)
+
+
+@pytest.mark.parametrize("m,rows,cols,group,zeros,dtype", W4)
+def test_w4_gated_of_many_steps(m, rows, cols, group, zeros, dtype):
+    rows = rows // 2 + 1
+    cg, cu = (w4_on_device(rows, cols, group, zeros, dtype, seed=s) for s in (cols, cols + 1))
+    x = normal(generator(m), (m, cols), dtype)
+    (g, eg), (u, eu) = ref.w4_product(x, *cg, group), ref.w4_product(x, *cu, group)
+    a, da, uc = ref.gated(g, u, "silu", 0.0)
+    v = a * uc
+    # |act''| <= 1.2, as for the dense block: the second order of g's error
+    e = (da * uc).abs() * eg + a.abs() * eu + 2 * eg * eu + 0.6 * eg * eg * uc.abs() + ref.ACC * v.abs()
+    h = empty(m, rows, dtype)
+    moe.moe_w4_gated(w4_make(cg, group), w4_make(cu, group), x, h, act="silu", limit=0.0)
+    ref.check(h, v.cpu(), (e + ref.U[dtype] * (v.abs() + e) + ref.TINY[dtype]).cpu(), f"gated [{m}, {cols}] x [{rows}]")
+    assert untouched(h)
