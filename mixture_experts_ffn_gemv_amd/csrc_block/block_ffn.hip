@@ -725,31 +725,49 @@ hipError_t launch_skinny(const FfnArgs& a, hipStream_t st) {
                          dim3(64 * (SKINNY_WAVES + SKINNY_LOADERS)), lds, st, a);
 }
 
+// LDS room for 16, 24, 32, 40, 48 or 64 rows of x
+constexpr int skinny_room(int m) { return m <= 16 ? 16 : m <= 48 ? (m + 7) / 8 * 8 : 64; }
+
+// 33 to 64 rows: whether weight rows are faster than tiles, by what either costs in us. By weight rows
+// each 256 workgroups take 4 and what a CU loads, K times the room for x and 16 weight rows, at 55
+// bytes a ns, whether a CU has two of them at a time or one after the other. Tiles take 14, or 3 and one for
+// each K step where that is less, and the weights at 5.5 TB/s. Over 155 forward calls (33 to 64 rows, 31 widths of
+// 264 x 4232 to 16384 x 4096) the two choices of a call cost 0.4% more than the best two on average, 6.5% at most; going by
+// the number of workgroups alone cost 7.5% and 64%. GATEUP, weight rows against tiles, 40 and 64 rows: 2048 x
+// 2048 (D x I) 9.1 against 17.0 us, 10.3 against 17.2; 5120 x 2304 28.6 against 24.2, 34.8 against 25.1; 8192 x 2048
+// 23.8 against 27.8, 28.6 against 26.9; 10240 x 2560 55.4 against 34.0, 67.9 against 34.2; 14336 x 1024 36.7
+// against 25.0, 45.3 against 25.5. DOWN: 4096 x 4096 13.9 against 17.7, 16.6 against 18.1; 8192 x 1024 9.5 against
+// 18.7, 14.1 against 18.8; 8192 x 256 7.5 against 5.3, 10.6 against 5.5; 16384 x 2048 29.9 against 25.3, 37.4
+// against 25.7.
+bool by_weight_rows(int m, int K, int blocks) {
+    const double rows = cdiv(blocks, N_CU) * (4 + K * (skinny_room(m) + 16.0) * 2 / 55e3);
+    const double tiles = std::min(14.0, 3 + K / 64.0) + blocks * 16.0 * K * 2 / 5.5e6;
+    return rows < tiles;
+}
+
 // GATEUP or DOWN of the forward pass. Few rows go by weight rows, more in tiles: 32 rows of 5120 x
 // 2304 (D x I, both products) take 36.5 against 39.6 us, of 8192 x 2048 33.8 against 46.0, of 1024 x
-// 1024 11.6 against 22.2 (of 8192 x 8192 114.8 against 108.3). Above 32 rows a workgroup's slabs of x
-// (80 KB and more) leave a CU room for two workgroups or one, and where there are more of them than CUs
-// tiles are faster: 48 rows of 5120 x 2304 41.7 against 47.6, of 8192 x 8192 110 against 145, 40 rows
-// 120 against 131; with fewer they are not: 48 rows of 2048 x 2048 29.0 against 17.3, 64 rows 29.4
-// against 19.5; nor are they with 48 rows and 2^24 weights at most: DOWN of 8192 x 2048 17.7 against 17.2.
+// 1024 11.6 against 22.2 (of 8192 x 8192 114.8 against 108.3).
 template <typename T, Kind KIND>
 hipError_t launch_forward(const FfnArgs& a, float* partial, hipStream_t st) {
-    const int blocks = KIND == GATEUP ? cdiv(a.I, 8) : cdiv(a.D, 16);
-    const bool large = a.m > 48 || (size_t)(KIND == GATEUP ? 2 : 1) * a.D * a.I > 1 << 24;
-    if (a.m > 64 || (a.m > TILES_ABOVE && blocks > N_CU && large)) return launch_product<T, KIND>(a, partial, st);
+    const int K = KIND == GATEUP ? a.D : a.I, blocks = KIND == GATEUP ? cdiv(a.I, 8) : cdiv(a.D, 16);
+    if (a.m > 64 || (a.m > TILES_ABOVE && !by_weight_rows(a.m, K, blocks))) return launch_product<T, KIND>(a, partial, st);
     // up to 16 rows that fit into LDS whole: one row of 5120 x 2304 21.8 against 27.7 us in slabs, of
     // 8192 x 2048 23.7 against 27.0, 16 rows of 1024 x 1024 7.9 against 11.4
-    const size_t whole = a.m * (size_t)few_row(KIND == GATEUP ? a.D : a.I);
+    const size_t whole = a.m * (size_t)few_row(K);
     if (a.m <= 16 && whole <= FEW_LDS)
         return launch_kernel(ffn_few_kernel<T, KIND>, dim3(blocks), dim3(64 * SKINNY_WAVES),
                              std::max<size_t>(whole, sizeof(float) * SKINNY_WAVES * 256), st, a);
-    if (a.m <= 16) return launch_skinny<T, KIND, 16>(a, st);
     // (room for 24 and 40 rows: 20 rows of 5120 x 2304 33.8 against 35.1 us in room for 32, 36 rows of 8192
     // x 2048 36.6 against 40.3 in room for 48, which two workgroups of a CU do not have)
-    if (a.m <= 24) return launch_skinny<T, KIND, 24>(a, st);
-    if (a.m <= 32) return launch_skinny<T, KIND, 32>(a, st);
-    if (a.m <= 40) return launch_skinny<T, KIND, 40>(a, st);
-    return a.m <= 48 ? launch_skinny<T, KIND, 48>(a, st) : launch_skinny<T, KIND, 64>(a, st);
+    switch (skinny_room(a.m)) {
+        case 16: return launch_skinny<T, KIND, 16>(a, st);
+        case 24: return launch_skinny<T, KIND, 24>(a, st);
+        case 32: return launch_skinny<T, KIND, 32>(a, st);
+        case 40: return launch_skinny<T, KIND, 40>(a, st);
+        case 48: return launch_skinny<T, KIND, 48>(a, st);
+        default: return launch_skinny<T, KIND, 64>(a, st);
+    }
 }
 
 template <typename T>

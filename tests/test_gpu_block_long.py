@@ -60,10 +60,14 @@ def test_ffn_few_rows_in_slabs(m, dim, inter):
     ffn_against_float64(m, dim, inter, BF16 if m % 2 else F16, "silu", 10.0, extra=24)
 
 
-# 17 to 64 rows: slabs of 256, eight in flight, up to four rounds of them, room for 24, 32, 40, 48 and 64 rows
+# 17 to 64 rows: slabs of 256, eight in flight, up to eight rounds of them, room for 24, 32, 40, 48 and 64 rows. Above 32
+# rows a product goes by weight rows or in tiles, by its K and its weights: of the last six one goes by weight rows in both,
+# in two rounds of workgroups in the second, the others in one of the two
 @pytest.mark.parametrize("m,dim,inter", [(17, 4360, 520), (24, 520, 4360), (32, 8200, 264), (26, 136, 8200), (33, 4104, 264),
                                          (40, 264, 4232), (48, 4360, 136), (43, 136, 4104), (64, 136, 8200), (49, 8200, 72),
-                                         (20, 16384, 16), (31, 16, 16384)])
+                                         (20, 16384, 16), (31, 16, 16384), (33, 264, 10248),
+                                         (40, 5128, 2312), (40, 8200, 2040), (48, 6152, 2040), (41, 4088, 4104), (56, 4088, 4104),
+                                         (64, 6152, 2040)])
 def test_ffn_more_rows_in_slabs(m, dim, inter):
     ffn_against_float64(m, dim, inter, BF16 if m % 2 else F16, "gelu", 0.0, extra=16)
 
