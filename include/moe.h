@@ -360,7 +360,9 @@ int moe_forward_static(const moe_cfg* cfg, const moe_weights* w, const void* are
  *   g = x Wg^T, u = x Wu^T;  h = act(gc) uc with gc = min(g, limit) and
  *   uc = min(max(u, -limit), limit) (no clamps when limit <= 0);  y = h Wd^T.
  * Products are summed in f32; h is rounded to the value type, as it is the
- * operand of the second product, and nothing else before y is. */
+ * operand of the second product, and nothing else before y is: y has about sqrt(2) of
+ * the error that its own rounding gives it, and in f16 an h past 65504 is infinite. A
+ * NaN is not clamped. */
 typedef struct moe_ffn {
     int32_t dim;        /* D: a multiple of 8, 8..16384 */
     int32_t inter;      /* I: a multiple of 8, 8..16384 */
@@ -396,7 +398,9 @@ int moe_ffn_forward(const moe_ffn* f, const void* x, int64_t ldx, int32_t m, voi
  * x, m, the weights and saved are those of the forward call. dx [m, D] (row
  * stride lddx), dw_gate and dw_up [I, D] and dw_down [D, I] (row-major, 16-byte
  * aligned) are written, not added to; each may be NULL and is then not computed.
- * dg, du and h are rounded to the value type, as operands of the products.
+ * dg, du and h are rounded to the value type, as operands of the products (in f16, past
+ * 65504 they are infinite). Where g or u is NaN it is not clamped: dg or du is
+ * what the formula without the condition gives.
  * m = 0 writes zeros to the weights' gradients. No output may overlap an input.
  * Errors as moe_ffn_forward. */
 int moe_ffn_backward(const moe_ffn* f, const void* x, int64_t ldx, const void* dy, int64_t lddy, int32_t m,
@@ -408,7 +412,8 @@ int moe_ffn_backward(const moe_ffn* f, const void* x, int64_t ldx, const void* d
  *   p = y / rms(y) * w_post  (p = y without w_post),  rms(v) = sqrt(mean(v^2) + eps)
  *   r' = res_scale r + gate p,     n = r' / rms(r') * w_pre
  * Everything is computed in f32 and rounded once, where it is stored; n comes
- * from the unrounded r'. */
+ * from the unrounded r'. (Squares are summed in f32: a row whose sum of squares passes
+ * 3.4e38 has an infinite rms.) */
 #define MOE_GATE_NONE 0     /* 1 */
 #define MOE_GATE_CHANNEL 1  /* gate [dim] */
 #define MOE_GATE_TOKEN 2    /* gate [m] */
@@ -468,7 +473,9 @@ typedef struct moe_w4 {
     const void* zeros;   /* device, [rows, cols / group] bytes of 0..15, or NULL: 8 everywhere */
 } moe_w4;
 
-/* y [m, N] = x W^T, summed in f32 with the exact w and rounded once. x [m, K] with
+/* y [m, N] = x W^T, from the exact w, summed in f32 and rounded once. A group's sum
+ * is taken with the codes shifted by 128 (f16: 64) and that part taken off again, so that
+ * the f32 sums round at the size of 2^-24 143 (79) scale sum |x|. x [m, K] with
  * row stride ldx (a multiple of 8, at most 2^24; 16-byte aligned), y with row stride
  * ldy >= N (2-byte aligned); m is at most 2097120. Made for few rows: each 32 rows of
  * x read the weights once. A row of x that holds an infinity gives NaN, and one with

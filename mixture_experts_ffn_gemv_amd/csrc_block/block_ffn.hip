@@ -19,12 +19,17 @@
 // length, a K tail by an offset past it. Chunks of 16 bytes are stored permuted so that
 // the LDS reads of a matrix operand fall on distinct banks.
 //
+// h, dg and du are rounded to 16 bits, as operands of the matrix cores; in f16 they become infinite past
+// 65504. Rounding one operand of a product once more makes the error of y and of the gradients
+// sqrt(2) of what rounding the result alone gives (bf16 2.3e-3 of the norm, f16 2.9e-4); two products
+// of 16-bit parts of each would cost a second matrix product. g and u stay in f32.
+//
 // Bound, for many rows, by the matrix cores: at 8192 rows of 5120 x 2304 (bf16, a training
 // step 1.72 ms) GATEUP takes 333 us (1.16 PFLOP/s), DOWN 187 (1.03), DH 266 (0.73), DX 346
 // (1.12), DW 533 (1.09), where a library product of 8192^3 reaches 1.51 (either operand's
 // k consecutive), 1.32 or 1.16 (as in DX and DW). A round of whole tiles runs at 1.3; the rest
-// is the last round, which is not full, and DH's epilogue: it reads 151 MB of g and u and
-// writes 113 MB of dg, du and h, after the products of its tile. Counters: no LDS
+// is the last round, which is not full, and the ends of tiles: GATEUP stores 151 MB of g and u in f32, DH reads
+// them and writes 113 MB of dg, du and h, after the products of its tile. Counters: no LDS
 // conflicts, matrix cores busy 0.59 (GATEUP) and 0.48 (DW) of the cycles.
 // Few rows are bound by the weights' bytes: one token of 5120 x 2304 20.2 us, 70.8 MB, 3.5 TB/s.
 #include "block_common.h"
@@ -451,7 +456,7 @@ MOE_DEV void skinny_finish(const FfnArgs& a, float* red, int n0, const f32x4 (&a
 // of Wg and the same eight of Wu), each of its eight wavefronts a part of k, and their sums are
 // joined through LDS in wavefront order. There is one wait for x, and the wavefronts then
 // go their own ways through k, AHEAD chunks of 32 of their weights in flight. One token of 5120 x
-// 2304: 12.4 us (47 MB, 3.8 TB/s) and 6.6 us.
+// 2304: 12.5 us (47 MB, 3.8 TB/s) and 6.7 us.
 constexpr size_t FEW_LDS = 64 << 10;
 MOE_DEV __host__ int few_row(int K) { return (K + 511) / 512 * 1024; }   // bytes of a token's row there
 template <typename T, Kind KIND>
@@ -629,9 +634,11 @@ size_t partial_bytes(Kind kind, int m, int D, int I, int products) {
 
 // How a product is cut up: 256 x 256 or 128 x 128 tiles, and by how much the tiles past the last full
 // round of the CUs are split along k. Costs in units of one K step of a 256 x 256 tile on a CU
-// (1.65 us): a 128 x 128 tile's step takes 0.33 of it (a quarter of the products, at three quarters
+// (about 1.65 us): a 128 x 128 tile's step takes 0.33 of it (a quarter of the products, at three quarters
 // of the rate); the split tiles' sums pass through memory twice (0.06 a 256 x 256 tile and split, and 4 for
-// the second launch). 8192 rows of 5120 x 2304 in the large tiles and in the small: GATEUP 334 and
+// the second launch). What the end of a tile loads and stores is not counted; of a product with few
+// steps it is half the time (GATEUP of 1013 rows of 1544 x 4104, 25 steps in one round: 50 us, its steps
+// alone by these costs 27). 8192 rows of 5120 x 2304 in the large tiles and in the small: GATEUP 334 and
 // 377 us, DOWN 187 and 196, DH 266 and 271, DX 346 and 422, DW 533 and 624.
 Product plan_product(Kind kind, int m, int D, int I, int products) {
     Product best{};

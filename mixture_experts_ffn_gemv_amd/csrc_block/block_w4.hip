@@ -8,10 +8,15 @@
 // cost no subtraction: the code's four bits are set into the mantissa of c (128 for
 // bf16, 64 for f16). The sum of x over a group comes from one more matrix product
 // with ones, in the layout in which it is needed. Scale and zero point are applied
-// in f32 to each group's sum, so that w is never rounded.
+// in f32 to each group's sum, so that w is never rounded. What c adds is taken off again in f32:
+// the sums of a group round at the size of (c + 15) sum |x| rather than 15 sum |x|, three bits (bf16) or
+// two (f16) of the 24. Outputs differ by 1e-4 of their norm from sums of the exact w (bf16, 5120 x
+// 2304), where their own rounding is 1.6e-3; taking c off the codes first would cost an instruction for
+// every one or two of them.
 //
-// Bound, for few rows, by the codes' bytes. 65536 x 2048, one row of x: 23.7 us, 3.0 TB/s of
-// codes and scales; 8192 x 8192 11.4 us, 3.1 TB/s (a stream of reads from HBM reaches about 6); 5120 x
+// Bound, for few rows, by the codes' bytes. 65536 x 2048, one row of x: 24.0 us, 3.1 TB/s of
+// codes, scales and zero points; 8192 x 8192 11.9 us, 3.1 TB/s (a stream of reads from HBM reaches about
+// 6: every code passes through LDS, with a barrier for each 8 KB); 5120 x
 // 5120 7.6 us, of which a launch, the first loads and the sums' join are about 4. From 16 rows
 // on x, which every workgroup brings into its LDS, costs more than the codes.
 //
@@ -325,13 +330,13 @@ hipError_t launch_tiles(const W4Args& a, hipStream_t st) {
 }
 
 // LDS room for 4, 8, 16, 24 or 32 rows of x, since a step's x is loaded whether its rows exist or not (8 rows
-// of 5120 x 5120, group 64: 7.8 us, in room for 16 rows 9.6; 16 rows 9.6, in room for 32 14.8; 1 row
-// 7.6, in room for 8 8.0, of 65536 x 2048 23.7 against 25.1; 20 rows 13.1, in room for 32 15.5, of 65536 x
-// 2048 25.7 against 26.6). With more than 16 rows one workgroup fits a
+// of 5120 x 5120, group 64: 8.1 us, in room for 16 rows 9.6; 16 rows 9.5, in room for 32 14.8; 1 row
+// 7.6, in room for 8 8.0; 20 rows 12.7, in room for 32 15.1, of 65536 x 2048 26.0 against 27.4, of 32768 x
+// 8192 43.6 against 45.2). With more than 16 rows one workgroup fits a
 // CU. Two wavefronts on rows make the most workgroups, and the shortest where those are one round of
-// the CUs at most (32 rows of 5120 x 5120 15.0 us against 24.5, of 8192 x 8192 20.6 against 37); beyond,
-// four with two tiles each read x a quarter as often (16384 x 5120 26.1 against 29.6, 65536 x 2048
-// 26.9 against 69, 64 rows of 8192 x 2048 12.5 against 18.1).
+// the CUs at most (32 rows of 5120 x 5120 15.4 us against 24.5, of 8192 x 8192 21.7 against 37); beyond,
+// four with two tiles each read x a quarter as often (16384 x 5120 26.9 against 29.6, 65536 x 2048
+// 29.6 against 69, 64 rows of 8192 x 2048 12.7 against 18.1).
 template <typename T, int G, bool GATED>
 hipError_t launch_w4(const W4Args& a, hipStream_t st) {
     if (a.m <= 4) return launch_tiles<T, G, 4, 4, 2, 1, 4, GATED>(a, st);
