@@ -361,8 +361,9 @@ int moe_forward_static(const moe_cfg* cfg, const moe_weights* w, const void* are
  *   uc = min(max(u, -limit), limit) (no clamps when limit <= 0);  y = h Wd^T.
  * Products are summed in f32; h is rounded to the value type, as it is the
  * operand of the second product, and nothing else before y is: y has about sqrt(2) of
- * the error that its own rounding gives it, and in f16 an h past 65504 is infinite. A
- * NaN is not clamped. */
+ * the error that its own rounding gives it. Up to 16 rows, where m times inter (rounded up
+ * to a multiple of 512) is 16384 at most, h keeps twice the bits, and y is rounded once.
+ * In f16 an h past 65504 is infinite. A NaN is not clamped. */
 typedef struct moe_ffn {
     int32_t dim;        /* D: a multiple of 8, 8..16384 */
     int32_t inter;      /* I: a multiple of 8, 8..16384 */

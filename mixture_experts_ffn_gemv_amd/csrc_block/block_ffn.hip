@@ -19,8 +19,8 @@
 // length, a K tail by an offset past it. Chunks of 16 bytes are stored permuted so that
 // the LDS reads of a matrix operand fall on distinct banks.
 //
-// h, dg and du are rounded to 16 bits, as operands of the matrix cores; in f16 they become infinite past
-// 65504. Rounding one operand of a product once more makes the error of y and of the gradients
+// h, dg and du are rounded to 16 bits, as operands of the matrix cores (h of a few rows in two parts: see
+// h_in_parts); in f16 they become infinite past 65504. Rounding one operand of a product once more makes the error of y and of the gradients
 // sqrt(2) of what rounding the result alone gives (bf16 2.3e-3 of the norm, f16 2.9e-4); two products
 // of 16-bit parts of each would cost a second matrix product. g and u stay in f32.
 //
@@ -31,7 +31,7 @@
 // is the last round, which is not full, and the ends of tiles: GATEUP stores 151 MB of g and u in f32, DH reads
 // them and writes 113 MB of dg, du and h, after the products of its tile. Counters: no LDS
 // conflicts, matrix cores busy 0.59 (GATEUP) and 0.48 (DW) of the cycles.
-// Few rows are bound by the weights' bytes: one token of 5120 x 2304 20.2 us, 70.8 MB, 3.5 TB/s.
+// Few rows are bound by the weights' bytes: one token of 5120 x 2304 20.7 us, 70.8 MB, 3.4 TB/s.
 #include "block_common.h"
 
 namespace moe {
@@ -52,6 +52,7 @@ struct FfnArgs {
     int64_t ldx, lddy, ldy, lddx;
     int m, D, I, act;
     float limit;
+    bool parts;              // h lies in two parts: see h_in_parts
 };
 
 // one operand of a product: up to two matrices, used side by side (GATEUP) or one
@@ -444,7 +445,13 @@ MOE_DEV void skinny_finish(const FfnArgs& a, float* red, int n0, const f32x4 (&a
                 s[0] = gv;
                 s[256] = uv;
             }
-            a.h[(size_t)tok * a.I + n] = T::store(act_value(clamp_gate(gv, a.limit), a.act) * clamp_up(uv, a.limit));
+            const float h = act_value(clamp_gate(gv, a.limit), a.act) * clamp_up(uv, a.limit);
+            const auto rounded = T::store(h);
+            a.h[(size_t)tok * a.I + n] = rounded;
+            if (a.parts) {
+                const float rest = h - T::load(rounded);
+                a.h[(size_t)(a.m + tok) * a.I + n] = T::store(fabsf(rest) < INFINITY ? rest : 0.f);
+            }
         } else {
             a.y[(size_t)tok * a.ldy + n] = T::store(total(tok, c));
         }
@@ -456,10 +463,26 @@ MOE_DEV void skinny_finish(const FfnArgs& a, float* red, int n0, const f32x4 (&a
 // of Wg and the same eight of Wu), each of its eight wavefronts a part of k, and their sums are
 // joined through LDS in wavefront order. There is one wait for x, and the wavefronts then
 // go their own ways through k, AHEAD chunks of 32 of their weights in flight. One token of 5120 x
-// 2304: 12.5 us (47 MB, 3.8 TB/s) and 6.7 us.
+// 2304: 12.5 us (47 MB, 3.8 TB/s) and 6.7 us, 7.0 with h in two parts.
 constexpr size_t FEW_LDS = 64 << 10;
 MOE_DEV __host__ int few_row(int K) { return (K + 511) / 512 * 1024; }   // bytes of a token's row there
-template <typename T, Kind KIND>
+
+// Where h fits into LDS twice it is held in two 16-bit parts, its rounded value and what that leaves out
+// (rows m and on), and DOWN multiplies both by a weight that it has read once: y is then rounded once. One
+// token of 5120 x 2304: y's error 1.7e-3 of the norm, 2.4e-3 with h rounded, in 20.7 us against 20.2 (both
+// products); 2 rows of 1544 x 4104 14.8 against 14.2. Past that the parts cost more: 8 rows of 5120 x
+// 2304, in slabs, 31.9 against 29.0, 12 of 2048 x 2048 12.6 against 11.0, and many rows a second product.
+bool h_in_parts(int m, int I) { return m <= 16 && 2 * m * (size_t)few_row(I) <= FEW_LDS; }
+// the sums of the two parts: the second is small, and means nothing where it is not finite (an infinite
+// weight times a zero, or with another sign)
+MOE_DEV f32x4 join_parts(f32x4 v, f32x4 rest) {
+#pragma unroll
+    for (int r = 0; r < 4; ++r) v[r] += fabsf(rest[r]) < INFINITY ? rest[r] : 0.f;
+    return v;
+}
+
+// PARTS: of h, DOWN only
+template <typename T, Kind KIND, bool PARTS>
 __global__ __launch_bounds__(64 * SKINNY_WAVES) void ffn_few_kernel(FfnArgs a) {
     constexpr int RB = KIND == GATEUP ? 8 : 16, AHEAD = 5;
     extern __shared__ __align__(16) uint8_t smem[];   // x; then sums [wavefront][256]
@@ -467,11 +490,12 @@ __global__ __launch_bounds__(64 * SKINNY_WAVES) void ffn_few_kernel(FfnArgs a) {
     const int K = KIND == GATEUP ? a.D : a.I, N = KIND == GATEUP ? a.I : a.D, n0 = blockIdx.x * RB;
     const int64_t ldx = KIND == GATEUP ? a.ldx : a.I;
     const int row_bytes = few_row(K), runs = row_bytes / 1024;
-    const auto X = buffer_rsrc(KIND == GATEUP ? a.x : a.h, (uint32_t)((a.m - 1) * ldx + K) * 2);
-    for (int r = wv; r < a.m * runs; r += SKINNY_WAVES) {
-        // 16-byte chunk c of a token's row lies at c ^ (token & 15)
-        const int tok = r / runs, k = (r - tok * runs) * 512 + (lane ^ (tok & 15)) * 8;
-        buffer_load_lds16(X, smem + r * 1024, k < K ? (uint32_t)(tok * ldx + k) * 2 : PAST);
+    const int rows = PARTS ? 2 * a.m : a.m;
+    const auto X = buffer_rsrc(KIND == GATEUP ? a.x : a.h, (uint32_t)((rows - 1) * ldx + K) * 2);
+    for (int r = wv; r < rows * runs; r += SKINNY_WAVES) {
+        // 16-byte chunk c of a row lies at c ^ (row & 15)
+        const int row = r / runs, k = (r - row * runs) * 512 + (lane ^ (row & 15)) * 8;
+        buffer_load_lds16(X, smem + r * 1024, k < K ? (uint32_t)(row * ldx + k) * 2 : PAST);
     }
     const int chunks = (K + 31) / 32, c0 = wv * chunks / SKINNY_WAVES, c1 = (wv + 1) * chunks / SKINNY_WAVES;
     const int row = min(n0 + (l16 & (RB - 1)), N - 1);
@@ -483,14 +507,17 @@ __global__ __launch_bounds__(64 * SKINNY_WAVES) void ffn_few_kernel(FfnArgs a) {
     wait_vm_loads<AHEAD>();   // this wavefront's part of x has landed
     barrier_lds();
     const int xt = min(l16, a.m - 1);   // (a token that does not exist reads another's; its sums are not used)
-    const uint8_t* x = smem + xt * row_bytes;
-    f32x4 acc[1] = {{0.f, 0.f, 0.f, 0.f}};
+    f32x4 acc[1] = {{0.f, 0.f, 0.f, 0.f}}, rest = {0.f, 0.f, 0.f, 0.f};
     auto multiply = [&](int i, int c) {
         // a weight that stands in for one past K is not one (x is zero there)
         const uint32_t on = 32 * c + 8 * g < K ? ~0u : 0u;
         const u32x4 wm = {wq[i].x & on, wq[i].y & on, wq[i].z & on, wq[i].w & on};
         const int cx = c * 4 + g;
-        acc[0] = T::mfma(__builtin_bit_cast(s16x8, wm), *reinterpret_cast<const s16x8*>(x + ((cx ^ (xt & 15)) << 4)), acc[0]);
+        auto product = [&](int row, f32x4 v) {
+            return T::mfma(__builtin_bit_cast(s16x8, wm), *reinterpret_cast<const s16x8*>(smem + row * row_bytes + ((cx ^ (row & 15)) << 4)), v);
+        };
+        acc[0] = product(xt, acc[0]);
+        if (PARTS) rest = product(a.m + xt, rest);
     };
     int c = c0;
     for (; c + AHEAD < c1; c += AHEAD)
@@ -502,6 +529,7 @@ __global__ __launch_bounds__(64 * SKINNY_WAVES) void ffn_few_kernel(FfnArgs a) {
 #pragma unroll
     for (int i = 0; i < AHEAD; ++i)
         if (c + i < c1) multiply(i, c + i);   // (a chunk of another's part is left out: its x times a zero weight is NaN if infinite)
+    if (PARTS) acc[0] = join_parts(acc[0], rest);
     skinny_finish<T, KIND, 1, 64 * SKINNY_WAVES>(a, reinterpret_cast<float*>(smem), n0, acc);
 }
 
@@ -712,7 +740,9 @@ size_t backward_partial(const moe_ffn* f, int m) {
     return std::max({partial_bytes(DH, m, f->dim, f->inter, 0), partial_bytes(DX, m, f->dim, f->inter, 0),
                      partial_bytes(DW, m, f->dim, f->inter, 3)});
 }
-size_t forward_bytes(const moe_ffn* f, int m) { return rows_bytes(f, m) + forward_partial(f, m); }
+// (h: 16 rows in two parts are as many as 32)
+size_t h_bytes(const moe_ffn* f, int m) { return m <= 16 ? 2 * rows_bytes(f, m) : rows_bytes(f, std::max(m, 32)); }
+size_t forward_bytes(const moe_ffn* f, int m) { return h_bytes(f, m) + forward_partial(f, m); }
 size_t backward_bytes(const moe_ffn* f, int m) { return 3 * rows_bytes(f, m) + backward_partial(f, m); }
 size_t saved_bytes_of(const moe_ffn* f, int m) { return (size_t)cdiv(m, 16) * cdiv(f->inter, 16) * 2048; }
 
@@ -761,10 +791,11 @@ hipError_t launch_forward(const FfnArgs& a, float* partial, hipStream_t st) {
     if (a.m > 64 || (a.m > TILES_ABOVE && !by_weight_rows(a.m, K, blocks))) return launch_product<T, KIND>(a, partial, st);
     // up to 16 rows that fit into LDS whole: one row of 5120 x 2304 21.8 against 27.7 us in slabs, of
     // 8192 x 2048 23.7 against 27.0, 16 rows of 1024 x 1024 7.9 against 11.4
-    const size_t whole = a.m * (size_t)few_row(K);
+    const bool parts = KIND == DOWN && a.parts;
+    const size_t whole = (parts ? 2 : 1) * a.m * (size_t)few_row(K);
     if (a.m <= 16 && whole <= FEW_LDS)
-        return launch_kernel(ffn_few_kernel<T, KIND>, dim3(blocks), dim3(64 * SKINNY_WAVES),
-                             std::max<size_t>(whole, sizeof(float) * SKINNY_WAVES * 256), st, a);
+        return launch_kernel(parts ? ffn_few_kernel<T, KIND, KIND == DOWN> : ffn_few_kernel<T, KIND, false>, dim3(blocks),
+                             dim3(64 * SKINNY_WAVES), std::max<size_t>(whole, sizeof(float) * SKINNY_WAVES * 256), st, a);
     // (room for 24 and 40 rows: 20 rows of 5120 x 2304 33.8 against 35.1 us in room for 32, 36 rows of 8192
     // x 2048 36.6 against 40.3 in room for 48, which two workgroups of a CU do not have)
     switch (skinny_room(a.m)) {
@@ -822,7 +853,8 @@ int moe_ffn_forward(const moe_ffn* f, const void* x, int64_t ldx, int32_t m, voi
     a.y = reinterpret_cast<uint16_t*>(y), a.ldy = ldy;
     a.h = reinterpret_cast<uint16_t*>(work);
     a.saved = reinterpret_cast<float*>(saved);
-    float* const partial = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(work) + rows_bytes(f, m));
+    a.parts = h_in_parts(m, f->inter);
+    float* const partial = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(work) + h_bytes(f, m));
     const hipStream_t st = (hipStream_t)stream;
     return status_of(f->dtype == MOE_BF16 ? forward<Bf16>(a, partial, st) : forward<F16>(a, partial, st));
 }

@@ -83,6 +83,44 @@ def test_ffn_against_float64(m, dim, inter, dtype, act, limit):
         assert untouched(got[k]), k
 
 
+@pytest.mark.parametrize("act,limit", [("silu", 0.0), ("gelu", 2.0)])
+@pytest.mark.parametrize("m,dim,inter,dtype", [(1, 256, 264, BF16), (2, 72, 1544, F16), (5, 1032, 2312, BF16), (16, 264, 520, F16),
+                                               (16, 264, 1024, BF16), (1, 72, 16384, BF16), (3, 264, 4104, F16), (6, 136, 2560, BF16)])
+def test_ffn_of_few_rows_rounds_once(m, dim, inter, dtype, act, limit):
+    # h in two parts of 16 bits, where it fits into LDS twice, is off by u^2 of itself (in f16 by half its smallest
+    # step at least): what is left of y's error is its own rounding and f32's sums
+    c = ffn_case(m, dim, inter, dtype, act, limit, seed=inter)
+    x, _, wg, wu, wd = (t.double() for t in c[:5])
+    g, u = x @ wg.t(), x @ wu.t()
+    a, da, uc = ref.gated(g, u, act, limit)
+    eg, eu = ref.ACC * (x.abs() @ wg.abs().t()), ref.ACC * (x.abs() @ wu.abs().t())
+    eh = (da * uc).abs() * eg + a.abs() * eu + (ref.ACC + ref.U[dtype] ** 2) * (a * uc).abs() + ref.TINY[dtype]
+    y = (a * uc) @ wd.t()
+    e = eh @ wd.abs().t() + ref.ACC * ((a * uc).abs() @ wd.abs().t())
+    got = ffn_run(c, extra=8, backward=False)["y"]
+    ref.check(got, y, e + ref.U[dtype] * (y.abs() + e) + ref.TINY[dtype], f"m={m} of {dim} x {inter}")
+    assert untouched(got)
+
+
+def test_ffn_of_infinite_weights_and_h():
+    # the second part of h adds nothing to what is infinite
+    for m, inter in ((2, 136), (14, 4104)):
+        c = list(ffn_case(m, 40, inter, F16, "silu", 0.0, seed=m))
+        c[2], c[3] = c[2].abs() + 0.01, c[3].abs() + 0.01
+        c[0] = c[0].abs() + 0.01
+        c[4] = c[4].clone()
+        clean = ffn_run(c, backward=False)["y"]
+        c[4][3, 5], c[4][7, inter - 1] = float("inf"), float("-inf")
+        y = ffn_run(c, backward=False)["y"]
+        assert (y[:, 3] == float("inf")).all() and (y[:, 7] == float("-inf")).all()
+        rest = torch.tensor([i not in (3, 7) for i in range(40)], device=DEV)
+        assert torch.equal(y[:, rest], clean[:, rest])
+        c[0], c[4] = c[0].clone(), c[4].abs() + 0.01
+        c[0][1] = 3e4   # h past f16's largest value
+        y = ffn_run(c, backward=False)["y"]
+        assert torch.isfinite(y[0, rest]).all() and (y[1] == float("inf")).all()
+
+
 def test_ffn_large_tiles_against_float64():
     # enough output tiles for the largest tiles in every product, none of them whole
     m, dim, inter = 2100, 4360, 2312
