@@ -7,17 +7,7 @@
 //   DX      dx = dg Wg + du Wu, one sum over both
 //   DW      dWg = dg^T x, dWu = du^T x, dWd = dy^T h, the three in one launch
 //
-// Every product is out[q, p] = sum_k P(k, p) Q(k, q) with p the consecutive index of
-// the output. P is the matrix instruction's first operand, so that a lane's four
-// results are four consecutive values of one output row. An operand either has k as
-// its consecutive index (tiles of rows x 64 k; one 16-byte LDS read per lane gives
-// eight k) or p / q (tiles of 64 k x rows; two transposing 8-byte LDS reads), so no
-// operand is ever transposed in memory.
-//
-// Tiles come into LDS by buffer loads straight to LDS, 16 bytes per lane, a K step of 64
-// ahead. What lies past an operand's rows or past K lands as zeros: rows by the buffer's
-// length, a K tail by an offset past it. Chunks of 16 bytes are stored permuted so that
-// the LDS reads of a matrix operand fall on distinct banks.
+// How a product is made of tiles is in block_tiles.h.
 //
 // h, dg and du are rounded to 16 bits, as operands of the matrix cores (h of a few rows in two parts: see
 // h_in_parts); in f16 they become infinite past 65504. Rounding one operand of a product once more makes the error of y and of the gradients
@@ -32,13 +22,10 @@
 // them and writes 113 MB of dg, du and h, after the products of its tile. Counters: no LDS
 // conflicts, matrix cores busy 0.59 (GATEUP) and 0.48 (DW) of the cycles.
 // Few rows are bound by the weights' bytes: one token of 5120 x 2304 20.7 us, 70.8 MB, 3.4 TB/s.
-#include "block_common.h"
+#include "block_tiles.h"
 
 namespace moe {
 namespace {
-
-constexpr int BK = 64;
-constexpr uint32_t PAST = 0xFFFFFFF0u;   // an offset past every buffer: zeros
 
 enum Kind { GATEUP, DOWN, DH, DX, DW };
 constexpr bool p_by_rows(Kind k) { return k == DH || k == DX || k == DW; }   // p (not k) is P's consecutive index
@@ -55,83 +42,39 @@ struct FfnArgs {
     bool parts;              // h lies in two parts: see h_in_parts
 };
 
-// one operand of a product: up to two matrices, used side by side (GATEUP) or one
-// after the other along k (DX)
-struct Operand {
-    const uint16_t *a, *b;
-    int64_t ld;
-    int rows;   // extent of p or q
-};
-
 // saved: block (q / 16, i / 16) holds g then u, 256 f32 each, in the order of the lanes that
 // hold them: four consecutive i of one q per lane
 MOE_DEV size_t saved_at(int q16, int i16, int I) { return ((size_t)q16 * ((I + 15) / 16) + i16) * 512; }
-
-// Tiles in LDS. rows x 64 k (128 bytes a row): chunk c of 16 bytes of row r lies at c ^ swz_k(r),
-// so that the 16 rows of an operand read fall on distinct banks.
-MOE_DEV int swz_k(int row) { return row & 7; }
-// 64 k x rows, rows = 128 or 256: runs of 1024 bytes, PIECE apart, each holding rows k that are
-// never read together; a transposing read takes four rows k of two lane groups at a time, and
-// these lie in eight runs, whose distance puts them on distinct banks. Every read of a
-// lane is then one address and a constant.
-constexpr int PIECE = 1024 + 32;
-constexpr int tile_bytes(int rows, bool by_rows) { return by_rows ? rows / 8 * PIECE : rows * BK * 2; }
-// row k of run c: its part from the wavefront's share of c and the place in the run, and from the unit
-MOE_DEV int run_row_wave(int rows, int waves, int wv, int slot) {
-    const int in = rows == 256 ? 4 * slot : 4 * (slot & 1) + 16 * (slot >> 1);
-    return (wv & 3) + (waves == 8 ? 8 * (wv >> 2) : 0) + in;
-}
-constexpr int run_row_unit(int rows, int waves, int u) {
-    const int far = rows == 256 ? 16 : 32;
-    return waves == 8 ? far * u : 8 * (u & 1) + far * (u >> 1);
-}
-
-MOE_DEV s16x4 read_tr(const uint8_t* p) {
-    return __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)p);
-}
-
-// Asks the compiler for this order of half a step's instructions: READS LDS reads, and
-// the first LOADS of the loads into LDS, spread between MFMAS matrix products
-template <int READS, int MFMAS, int LOADS, int R = 0>
-MOE_DEV void interleave() {
-    if constexpr (R < READS) {
-        __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);   // an LDS read
-        if constexpr (R < LOADS) __builtin_amdgcn_sched_group_barrier(0x20, 1, 0);   // a load
-        constexpr int n = (R + 1) * MFMAS / READS - R * MFMAS / READS;
-        if constexpr (n > 0) __builtin_amdgcn_sched_group_barrier(0x8, n, 0);
-        interleave<READS, MFMAS, LOADS, R + 1>();
-    }
-}
 
 // Where a tile lies and what it multiplies
 struct Tile {
     Operand P, Q;
     uint16_t* out;   // [q, p] with row stride ldo (DOWN, DX, DW)
     int64_t ldo;
-    int K, segs, q0, p0;   // segs matrices one after another, K of k each
+    int segs, q0, p0;   // segs matrices one after another along k
 };
 // Tile `tile` of a product with nq x np tiles of BQ x BP (DW: along I and along D): eight q tiles
 // deep, so that the tiles an XCD works on at a time share their operands in its L2
 template <Kind KIND, int BQ, int BP>
 MOE_DEV Tile locate(const FfnArgs& a, int tile, int nq, int np) {
     Tile t;
-    t.K = a.D, t.segs = 1, t.out = nullptr, t.ldo = 0;
-    if (KIND == GATEUP) t.P = {a.wg, a.wu, a.D, a.I}, t.Q = {a.x, a.x, a.ldx, a.m};
-    if (KIND == DOWN) t.P = {a.wd, a.wd, a.I, a.D}, t.Q = {a.h, a.h, a.I, a.m}, t.K = a.I, t.out = a.y, t.ldo = a.ldy;
-    if (KIND == DH) t.P = {a.wd, a.wd, a.I, a.I}, t.Q = {a.dy, a.dy, a.lddy, a.m};
-    if (KIND == DX) t.P = {a.wg, a.wu, a.D, a.D}, t.Q = {a.dg, a.du, a.I, a.m}, t.K = a.I, t.segs = 2, t.out = a.dx, t.ldo = a.lddx;
+    t.segs = 1, t.out = nullptr, t.ldo = 0;
+    if (KIND == GATEUP) t.P = {a.wg, a.wu, a.D, a.I, a.D}, t.Q = {a.x, a.x, a.ldx, a.m, a.D};
+    if (KIND == DOWN) t.P = {a.wd, a.wd, a.I, a.D, a.I}, t.Q = {a.h, a.h, a.I, a.m, a.I}, t.out = a.y, t.ldo = a.ldy;
+    if (KIND == DH) t.P = {a.wd, a.wd, a.I, a.I, a.D}, t.Q = {a.dy, a.dy, a.lddy, a.m, a.D};
+    if (KIND == DX)
+        t.P = {a.wg, a.wu, a.D, a.D, a.I}, t.Q = {a.dg, a.du, a.I, a.m, a.I}, t.segs = 2, t.out = a.dx, t.ldo = a.lddx;
     if (KIND == DW) {
         // products whose output is not wanted have no tiles
-        t.K = a.m;
         const int each = nq * np, n0 = a.dwg != nullptr ? each : 0, n1 = a.dwu != nullptr ? each : 0;
         if (tile < n0 + n1) {
             const bool up = tile >= n0;
             if (up) tile -= n0;
-            t.P = {a.x, a.x, a.ldx, a.D}, t.Q = {up ? a.du : a.dg, nullptr, a.I, a.I};
+            t.P = {a.x, a.x, a.ldx, a.D, a.m}, t.Q = {up ? a.du : a.dg, nullptr, a.I, a.I, a.m};
             t.out = up ? a.dwu : a.dwg, t.ldo = a.D;
         } else {
             tile -= n0 + n1;
-            t.P = {a.h, a.h, a.I, a.I}, t.Q = {a.dy, a.dy, a.lddy, a.D};
+            t.P = {a.h, a.h, a.I, a.I, a.m}, t.Q = {a.dy, a.dy, a.lddy, a.D, a.m};
             t.out = a.dwd, t.ldo = a.I;
             nq = (a.D + BQ - 1) / BQ, np = (a.I + BP - 1) / BP;
         }
@@ -212,17 +155,16 @@ struct Plan {
     float* partial;      // [split][rest][j][i][thread] of the split tiles' sums, four f32 each
 };
 
+template <typename T, Kind KIND, int BQ, int BP, int WQ, int WP>
+using FfnTile = TileProduct<T, p_by_rows(KIND), q_by_rows(KIND), KIND == GATEUP, BQ, BP, WQ, WP>;
+
 // BQ x BP tile of the output, WQ x WP wavefronts
 template <typename T, Kind KIND, int BQ, int BP, int WQ, int WP>
 __global__ __launch_bounds__(64 * WQ * WP) void ffn_gemm_kernel(FfnArgs a, Plan plan) {
     extern __shared__ __align__(16) uint8_t smem[];
-    constexpr int TH = 64 * WQ * WP, TQ = BQ / WQ, TP = BP / WP, NI = TP / 16, NJ = TQ / 16;
-    constexpr int UP = BP * 8 / TH, UQ = BQ * 8 / TH, NW = TH / 64;   // 16-byte units per thread
-    constexpr bool PR = p_by_rows(KIND), QR = q_by_rows(KIND);
-    constexpr int P_BYTES = tile_bytes(BP, PR), STEP = P_BYTES + tile_bytes(BQ, QR);
-    static_assert(NW == 8 || NW == 4, "");
-    const int tid = threadIdx.x, lane = tid & 63, wv = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int l16 = lane & 15, g = lane >> 4, wq = wv / WP, wp = wv % WP;
+    typedef FfnTile<T, KIND, BQ, BP, WQ, WP> Product;
+    constexpr int TH = Product::TH, NI = Product::NI, NJ = Product::NJ;
+    const int tid = threadIdx.x, wv = __builtin_amdgcn_readfirstlane(tid >> 6), wq = wv / WP, wp = wv % WP;
 
     // consecutive tiles (of a split part: those of one part of k) on one XCD
     const int whole_blocks = (plan.whole + 7) / 8 * 8;
@@ -237,146 +179,11 @@ __global__ __launch_bounds__(64 * WQ * WP) void ffn_gemm_kernel(FfnArgs a, Plan 
         tile = plan.whole + item - split * plan.rest;
     }
     const Tile t = locate<KIND, BQ, BP>(a, tile, plan.nq, plan.np);
-    const Operand &P = t.P, &Q = t.Q;
-    const int K = t.K, segs = t.segs, q0 = t.q0, p0 = t.p0;
-    constexpr int PSPAN = KIND == GATEUP ? BP / 2 : BP;
-
-    // This thread's first unit of each tile: its byte offset from the tile's corner; unit u is
-    // unit_rows(u) rows further. A K-contiguous tile's units of a thread share their chunk of k.
-    const int slot_p = PR ? lane / (BP / 8) : 0, slot_q = QR ? lane / (BQ / 8) : 0;
-    const int row_k = wv * 8 + (lane >> 3), chunk = (lane & 7) ^ swz_k(row_k);
-    const int first = KIND == GATEUP ? (row_k & 31) : row_k;
-    const uint32_t off_p = PR ? (uint32_t)(run_row_wave(BP, NW, wv, slot_p) * P.ld + lane % (BP / 8) * 8) * 2
-                              : (uint32_t)(first * P.ld + chunk * 8) * 2;
-    const uint32_t off_q = QR ? (uint32_t)(run_row_wave(BQ, NW, wv, slot_q) * Q.ld + lane % (BQ / 8) * 8) * 2
-                              : (uint32_t)(row_k * Q.ld + chunk * 8) * 2;
-
-    const int seg_steps = (K + BK - 1) / BK, steps = seg_steps * segs;
+    const int steps = (t.P.k + BK - 1) / BK * t.segs;
     const int kt0 = split < 0 ? 0 : (int)((int64_t)split * steps / plan.splits);
     const int nk = (split < 0 ? steps : (int)((int64_t)(split + 1) * steps / plan.splits)) - kt0;
-    auto stage = [&](int kt, uint8_t* buf) {
-        const bool past = kt >= nk;
-        kt += kt0;
-        const int seg = segs == 2 && kt >= seg_steps ? 1 : 0;
-        const int k0 = (kt - seg * seg_steps) * BK, kleft = min(BK, K - k0);
-        const uint32_t beyond = chunk * 8 >= kleft ? PAST : 0u;   // a K tail's missing chunks
-        auto side = [&](uint32_t off, const Operand& o, bool by_rows, int R, int at, int span, bool paired, int U, uint8_t* dst) {
-            const uint16_t* base = seg ? o.b : o.a;
-            const int left = min(o.rows - at, span);
-            if (by_rows) {
-                const auto buffer = buffer_rsrc(base + (size_t)k0 * o.ld + at, past ? 0u : (uint32_t)((kleft - 1) * o.ld + left) * 2);
-#pragma unroll
-                for (int u = 0; u < U; ++u)
-                    buffer_load_lds16(buffer, dst + (u * NW + wv) * PIECE, off + (uint32_t)(run_row_unit(R, NW, u) * o.ld * 2));
-            } else {
-                const uint32_t bytes = past ? 0u : (uint32_t)((left - 1) * o.ld + kleft) * 2;
-                const size_t corner = (size_t)at * o.ld + k0;
-                // GATEUP: rows 32..63 of every 64 are the second matrix's: with eight wavefronts those
-                // of wavefronts 4..7, with four those of every second unit
-                const bool second = paired && NW == 8 && (wv & 4);
-                const auto buffer = buffer_rsrc((second ? o.b : base) + corner, bytes);
-                const auto other = paired && NW == 4 ? buffer_rsrc(o.b + corner, bytes) : buffer;
-#pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    const int rows = paired ? (u * NW * 8 >> 6) * 32 : u * NW * 8;
-                    const uint32_t v = (off + (uint32_t)(rows * o.ld * 2)) | beyond;
-                    uint8_t* to = dst + (u * NW + wv) * 1024;
-                    if (paired && NW == 4 && (u & 1)) buffer_load_lds16(other, to, v);
-                    else buffer_load_lds16(buffer, to, v);
-                }
-            }
-        };
-        side(off_p, P, PR, BP, p0, PSPAN, KIND == GATEUP, UP, buf);
-        side(off_q, Q, QR, BQ, q0, BQ, false, UQ, buf + P_BYTES);
-    };
-
-    // LDS byte offset of this lane's operand reads for half kk of a step; operand i lies 16 rows
-    // further, which is a constant in either layout
-    auto read_base = [&](bool by_rows, int R, int base, int kk) {
-        if (by_rows) {
-            const int run = (l16 >> 2) + 4 * (g & 1) + (R == 256 ? 8 * (g >> 1) : 0);
-            return (run + kk * (R / 16)) * PIECE + (R == 256 ? 0 : (g >> 1) * 512) + base * 2 + (l16 & 3) * 8;
-        }
-        return (base + l16) * (BK * 2) + (((g + 4 * kk) ^ swz_k(l16)) << 4);
-    };
-    const int rdp0 = read_base(PR, BP, wp * TP, 0), rdp1 = read_base(PR, BP, wp * TP, 1);
-    const int rdq0 = read_base(QR, BQ, wq * TQ, 0), rdq1 = read_base(QR, BQ, wq * TQ, 1);
-    auto fragment = [&](const uint8_t* p, bool by_rows, int R, int i) -> s16x8 {
-        if (by_rows) {
-            const s16x4 lo = read_tr(p + i * 32), hi = read_tr(p + i * 32 + R * 2);   // k + 0..3, k + 4..7
-            return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
-        }
-        return *reinterpret_cast<const s16x8*>(p + i * 16 * BK * 2);
-    };
-
     f32x4 acc[NI][NJ];
-#pragma unroll
-    for (int i = 0; i < NI; ++i)
-#pragma unroll
-        for (int j = 0; j < NJ; ++j) acc[i][j] = (f32x4){0.f, 0.f, 0.f, 0.f};
-
-    // Half a K step (32 k) at a time: while one half is multiplied, the operands of the
-    // next are read from LDS into registers. A step's buffer is free once its second half
-    // is in registers, in the middle of its products: the barrier there lets the loads of
-    // the step after next go into it, a whole step before they are needed.
-    s16x8 fp[2][NI], fq[2][NJ];
-    auto read_half = [&](const uint8_t* buf, int kk, int to) {
-        const uint8_t *bp = buf + (kk ? rdp1 : rdp0), *bq = buf + P_BYTES + (kk ? rdq1 : rdq0);
-#pragma unroll
-        for (int i = 0; i < NI; ++i) fp[to][i] = fragment(bp, PR, BP, i);
-#pragma unroll
-        for (int j = 0; j < NJ; ++j) fq[to][j] = fragment(bq, QR, BQ, j);
-    };
-    auto multiply = [&](int from) {
-#pragma unroll
-        for (int j = 0; j < NJ; ++j)
-#pragma unroll
-            for (int i = 0; i < NI; ++i) acc[i][j] = T::mfma(fp[from][i], fq[from][j], acc[i][j]);
-    };
-    constexpr int READS = NI * (PR ? 2 : 1) + NJ * (QR ? 2 : 1), MFMAS = NI * NJ;
-    // Two steps, one of each buffer. The buffers are the lambda's own restricted pointers so
-    // that the compiler sees that the loads into one do not touch what is read from the other:
-    // it would wait for every load before the next LDS read.
-    auto two_steps = [&](uint8_t* __restrict b0, uint8_t* __restrict b1, int kt) {
-        read_half(b0, 1, 1);
-        multiply(0);
-        interleave<READS, MFMAS, 0>();
-        wait_vm_loads<0>();   // step kt + 1 has landed
-        barrier_lds();        // for every wavefront, and every one has read the last of step kt
-        stage(kt + 2, b0);
-        read_half(b1, 0, 0);
-        multiply(1);
-        interleave<READS, MFMAS, UP + UQ>();
-        read_half(b1, 1, 1);
-        multiply(0);
-        interleave<READS, MFMAS, 0>();
-        wait_vm_loads<0>();
-        barrier_lds();
-        stage(kt + 3, b1);    // (past the last step: zeros)
-        read_half(b0, 0, 0);
-        multiply(1);
-        interleave<READS, MFMAS, UP + UQ>();
-    };
-    if (nk > 0) {
-        stage(0, smem);
-        stage(1, smem + STEP);
-        wait_vm_loads<UP + UQ>();
-        barrier_lds();
-        read_half(smem, 0, 0);
-        int kt = 0;
-        for (; kt + 2 < nk; kt += 2) two_steps(smem, smem + STEP, kt);
-        read_half(smem, 1, 1);
-        multiply(0);
-        multiply(1);
-        wait_vm_loads<0>();   // (no load into LDS outlives the workgroup)
-        if (kt + 1 < nk) {
-            barrier_lds();
-            read_half(smem + STEP, 0, 0);
-            read_half(smem + STEP, 1, 1);
-            multiply(0);
-            multiply(1);
-        }
-    }
+    Product::run(t.P, t.Q, t.segs, t.q0, t.p0, kt0, nk, smem, acc);
 
     if (split >= 0) {
         f32x4* o = reinterpret_cast<f32x4*>(plan.partial) + (size_t)(split * plan.rest + tile - plan.whole) * NI * NJ * TH + tid;
@@ -391,7 +198,7 @@ __global__ __launch_bounds__(64 * WQ * WP) void ffn_gemm_kernel(FfnArgs a, Plan 
         f32x4 v[NI];
 #pragma unroll
         for (int i = 0; i < NI; ++i) v[i] = acc[i][j];
-        finish<T, KIND, NI>(a, t, q0 + wq * TQ + 16 * j, wp * TP, v);
+        finish<T, KIND, NI>(a, t, t.q0 + wq * Product::TQ + 16 * j, wp * Product::TP, v);
     }
 }
 
@@ -699,7 +506,7 @@ hipError_t launch_tiles(const FfnArgs& a, const Plan& plan, hipStream_t st) {
     if (grid == 0) return hipSuccess;
     constexpr int NJ = B / WQ / 16;
     const hipError_t e = launch_kernel(ffn_gemm_kernel<T, KIND, B, B, WQ, WP>, dim3(grid), dim3(64 * WQ * WP),
-                                       2 * (tile_bytes(B, p_by_rows(KIND)) + tile_bytes(B, q_by_rows(KIND))), st, a, plan);
+                                       FfnTile<T, KIND, B, B, WQ, WP>::LDS, st, a, plan);
     if (e != hipSuccess || plan.rest == 0) return e;
     return launch_kernel(ffn_join_kernel<T, KIND, B, B, WQ, WP>, dim3(plan.rest * NJ), dim3(64 * WQ * WP), 0, st, a, plan);
 }

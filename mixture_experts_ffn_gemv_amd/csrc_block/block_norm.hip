@@ -23,7 +23,7 @@
 // short calls slower: 1003 x 1111 f32 16 against 11 us), 30 wavefronts of workgroups
 // per CU instead of 20 (forward 86 us), single values where rows are not 16-byte
 // aligned (107 and 173 us, since the tail's loads stood in branches).
-#include "block_common.h"
+#include "block_rows.h"
 
 namespace moe {
 namespace {
@@ -49,80 +49,6 @@ struct NormArgs {
     bool has_y, has_dn, has_dr;
     float* partial;   // [grid][2][dim]; NULL: no sum over rows is wanted
 };
-
-// How a row of dim values falls into chunks of V. WHOLE: V divides dim. SHIFTED: the
-// last chunk is the row's last V values, the first `skip` of which belong to the
-// chunk before it: they read as zeros here, so that they add nothing, and are not
-// stored. SHORT: dim < V, one chunk of single values. A thread without a chunk loads
-// the row's first and reads it as zeros (skip = V): every load is unconditional, so
-// that the compiler's waits for one row leave the next rows' loads in flight.
-enum Tail { WHOLE, SHIFTED, SHORT };
-
-// A chunk as it lies in memory: 16 bytes, which need not be aligned to more than a value
-template <typename T>
-struct Raw {
-    static constexpr int V = 16 / sizeof(typename T::bits);
-    union {
-        uint4 q;
-        typename T::bits b[V];
-    };
-    template <Tail TAIL>
-    MOE_DEV void load(const void* base, int64_t row, int col, int dim) {
-        const typename T::bits* p = reinterpret_cast<const typename T::bits*>(base) + row;
-        if (TAIL == SHORT) {
-            q = make_uint4(0, 0, 0, 0);
-            for (int i = 0; i < dim; ++i) b[i] = p[i];
-        } else {
-            __builtin_memcpy(&q, p + col, 16);
-        }
-    }
-    // (used: the array is there at all)
-    template <Tail TAIL>
-    MOE_DEV void get(float* v, int skip, bool used = true) const {
-        const uint32_t on = skip < V && used ? ~0u : 0u;
-        const uint32_t w[4] = {q.x & on, q.y & on, q.z & on, q.w & on};
-        if constexpr (V == 4) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) v[i] = __uint_as_float(w[i]);
-        } else {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) v[2 * i] = T::lo(w[i]), v[2 * i + 1] = T::hi(w[i]);
-        }
-        if (TAIL == SHIFTED) {
-#pragma unroll
-            for (int i = 0; i < V - 1; ++i) v[i] = i < skip ? 0.f : v[i];
-        }
-    }
-};
-template <typename T, Tail TAIL>
-MOE_DEV void store_chunk(void* base, int64_t row, int col, int dim, int skip, bool past_l2, const float* v) {
-    constexpr int V = Raw<T>::V;
-    typename T::bits* p = reinterpret_cast<typename T::bits*>(base) + row + col;
-    if (skip >= V) return;
-    if (TAIL == SHORT || (TAIL == SHIFTED && skip != 0)) {
-#pragma unroll
-        for (int i = 0; i < V; ++i)
-            if (i >= skip && col + i < dim) p[i] = T::store(v[i]);
-        return;
-    }
-    uint4 q;
-    if constexpr (V == 4)
-        q = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
-    else
-        q = make_uint4(T::pack2(v[0], v[1]), T::pack2(v[2], v[3]), T::pack2(v[4], v[5]), T::pack2(v[6], v[7]));
-    typedef uint32_t words __attribute__((ext_vector_type(4), aligned(2)));
-    const words w = {q.x, q.y, q.z, q.w};
-    if (past_l2) __builtin_nontemporal_store(w, reinterpret_cast<words*>(p));
-    else *reinterpret_cast<words*>(p) = w;
-}
-// where chunk c of a row starts, and how many of its values belong to the chunk before it
-template <Tail TAIL>
-MOE_DEV void place_chunk(int c, int v, int dim, int& col, int& skip) {
-    col = c * v;
-    skip = 0;
-    if (col >= dim) skip = v, col = 0;
-    else if (TAIL == SHIFTED && col + v > dim) skip = col + v - dim, col = dim - v;
-}
 
 // Holds a chunk as it lies in memory: unpacked anew for each row, it takes fewer registers
 template <typename T>
@@ -454,7 +380,6 @@ int check_norm(const moe_norm* f) {
     return MOE_OK;
 }
 
-size_t value_bytes(int dtype) { return dtype == MOE_F32 ? 4 : 2; }
 
 bool past_l2(const moe_norm* f, int m) { return (size_t)m * f->dim * value_bytes(f->dtype) > (32u << 20); }
 
