@@ -337,7 +337,9 @@ int moe_forward_static(const moe_cfg* cfg, const moe_weights* w, const void* are
 
 /* ------------------------------------------------------------------------
  * Operators around the layer: the norms before and after a block, a dense gated
- * feed-forward block with its backward pass, and products with 4-bit weights.
+ * feed-forward block with its backward pass, products with 4-bit weights, tokens
+ * sorted by expert and back, products with 16-bit weights of one matrix or of one per
+ * expert, and dropout.
  * They need no context. The caller owns every buffer, the workspaces included;
  * a workspace holds nothing between calls, may be shared by calls that follow
  * each other on one stream, and must not be shared by calls that may overlap.
@@ -490,6 +492,114 @@ int moe_w4_matmul(const moe_w4* w, const void* x, int64_t ldx, int32_t m, void* 
  * have zero points. */
 int moe_w4_gated(const moe_w4* w_gate, const moe_w4* w_up, int32_t act, float limit, const void* x, int64_t ldx,
                  int32_t m, void* h, int64_t ldh, void* stream);
+
+/* Tokens sorted by the experts they picked, and back, with the routing weights applied. The
+ * picks are those of moe_route (idx [m, topk], weights [m, topk]); a pick outside 0..n_experts - 1
+ * (a padded or dropped token's) has no row anywhere. */
+
+/* Workspace bytes of moe_sort for m tokens. MOE_EINVAL for m < 0, topk outside 1..64, n_experts
+ * outside 1..1024, more than 2^26 picks, or NULL. Enough for fewer tokens too. */
+int moe_sort_workspace(int32_t m, int32_t topk, int32_t n_experts, size_t* bytes);
+
+/* The order of the picks by expert, equal experts by token and pick:
+ *   row_of [m, topk]       the sorted row of each pick, -1 where it has none
+ *   pick_of [m * topk]     the pick (token * topk + j) of each sorted row, -1 behind the last; may be NULL
+ *   offsets [n_experts + 1]  the first row of each expert, and the number of rows
+ * All device memory, row-major, 4-byte aligned; work 256-byte aligned. An expert may be picked twice by a
+ * token. m = 0 writes zeros to offsets. MOE_EINVAL, MOE_ESCRATCH, MOE_EHIP. */
+int moe_sort(const int32_t* idx, int32_t m, int32_t topk, int32_t n_experts, int32_t* row_of, int32_t* pick_of,
+             int32_t* offsets, void* work, size_t work_bytes, void* stream);
+
+/* In the next four: rows of dim values (1..2^20) of type dtype (MOE_BF16, MOE_F16 or MOE_F32) with
+ * row strides >= dim, pointers aligned to their value type; row_of [m, topk] as moe_sort writes it, no
+ * row twice; `rows` (up to 2^26) is how many sorted rows there is room for: a pick whose row_of is
+ * outside 0..rows - 1 takes no part. Sums are made in f32, in the order of a token's picks, and rounded
+ * once. No output overlaps an input. m = 0 does nothing. MOE_EINVAL, MOE_EHIP. */
+
+/* xs[row_of[t, j]] = x[t]. Sorted rows that no pick has are left as they are. */
+int moe_dispatch_forward(int32_t dtype, int32_t dim, const void* x, int64_t ldx, const int32_t* row_of, int32_t m,
+                         int32_t topk, void* xs, int64_t ldxs, int32_t rows, void* stream);
+
+/* Its gradient: dx[t] = sum over j of dxs[row_of[t, j]] (0 for a token without a row). */
+int moe_dispatch_backward(int32_t dtype, int32_t dim, const void* dxs, int64_t lddxs, int32_t rows,
+                          const int32_t* row_of, int32_t m, int32_t topk, void* dx, int64_t lddx, void* stream);
+
+/* y[t] = sum over j of weights[t, j] e[row_of[t, j]] (0 for a token without a row); weights f32 [m, topk]. */
+int moe_combine_forward(int32_t dtype, int32_t dim, const void* e, int64_t lde, int32_t rows, const float* weights,
+                        const int32_t* row_of, int32_t m, int32_t topk, void* y, int64_t ldy, void* stream);
+
+/* Its gradients: de[row_of[t, j]] = weights[t, j] dy[t] (rows that no pick has are left as they are) and
+ * dweights[t, j] = dy[t] . e[row_of[t, j]] (f32 [m, topk]; 0 for a pick without a row). Either may be NULL. */
+int moe_combine_backward(int32_t dtype, int32_t dim, const void* dy, int64_t lddy, const void* e, int64_t lde,
+                         int32_t rows, const float* weights, const int32_t* row_of, int32_t m, int32_t topk, void* de,
+                         int64_t ldde, float* dweights, void* stream);
+
+/* A product with a bias, an activation and a residual in its epilogue, of one matrix or of one per expert:
+ *   z = x W^T + bias;  y = act(z) + residual
+ * With offsets [experts + 1] (device, int32, rising from 0 to at most m, as moe_sort writes them), the rows
+ * offsets[e]..offsets[e + 1] - 1 of x, residual and y are those of expert e, and rows from offsets[experts] on are
+ * neither read nor written. Without (NULL; experts must be 1) all m rows are the one matrix's. Sums are made in
+ * f32, and y is rounded once. */
+#define MOE_ACT_NONE 2   /* v; moe_linear only */
+typedef struct moe_linear {
+    int32_t cols;       /* K: a multiple of 8, 8..65536 */
+    int32_t rows;       /* N: 1..131072 */
+    int32_t experts;    /* matrices: 1..1024 */
+    int32_t dtype;      /* MOE_BF16 or MOE_F16: x, y, residual, the weights and every gradient */
+    int32_t act;        /* MOE_ACT_* */
+    const void* w;      /* device, [experts, N, K] row-major, 16-byte aligned */
+    const void* bias;   /* device, [experts, N], or NULL */
+} moe_linear;
+
+/* Bytes that calls with m rows need: the workspaces of the two calls, and `saved`, what a forward call
+ * leaves for its backward call (z in f32; 0 without an activation). Each a multiple of 256, possibly 0, and
+ * enough for any fewer rows too. MOE_EINVAL for a bad description, m < 0, m > 2^24 or NULL. */
+int moe_linear_workspace(const moe_linear* f, int32_t m, size_t* forward, size_t* saved, size_t* backward);
+
+/* y for m rows. x [m, K] with row stride ldx (a multiple of 8, at most 2^22; 16-byte aligned); residual
+ * [m, N] or NULL and y [m, N] with any row strides >= N (2-byte aligned). y may be residual itself (same
+ * stride); no other overlap. saved: NULL, or the `saved` bytes that moe_linear_backward takes (256-byte
+ * aligned, as work is). m = 0 does nothing. MOE_EINVAL for a bad description, size, stride, NULL or misaligned
+ * pointer; MOE_ESCRATCH when work_bytes (or, with saved, saved_bytes) is less than moe_linear_workspace says;
+ * MOE_EHIP on a runtime error. */
+int moe_linear_forward(const moe_linear* f, const void* x, int64_t ldx, const int32_t* offsets, int32_t m,
+                       const void* residual, int64_t ldr, void* y, int64_t ldy, void* saved, size_t saved_bytes,
+                       void* work, size_t work_bytes, void* stream);
+
+/* Gradients from dy [m, N] (any row stride >= N): dz = dy act'(z); dx = dz W; dW = dz^T x; dbias = the sum of
+ * dz over an expert's rows. (The residual's is dy itself.) x, offsets, m, the weights and saved are those of the
+ * forward call. dx [m, K] (row stride lddx as ldx), dw [experts, N, K] (16-byte aligned) and dbias [experts, N] are
+ * written, not added to; each may be NULL and is then not computed. An expert without rows gets zeros. dz is
+ * rounded to the value type, as an operand of the products (in f16, past 65504 it is infinite); dbias is summed
+ * in f32 before that. m = 0 writes zeros to dw and dbias. No output may overlap an input. Errors as
+ * moe_linear_forward. */
+int moe_linear_backward(const moe_linear* f, const void* x, int64_t ldx, const int32_t* offsets, int32_t m,
+                        const void* dy, int64_t lddy, const void* saved, size_t saved_bytes, void* dx, int64_t lddx,
+                        void* dw, void* dbias, void* work, size_t work_bytes, void* stream);
+
+/* Dropout before the residual's addition, with a mask that is not stored: y = residual + keep x / (1 - p), with p
+ * rounded to a multiple of 2^-16 (p = 1: y = residual). What is dropped takes no part, whatever it holds.
+ * Value (row, col) is kept where its 16 random bits are at least 2^16 p: the eight values of columns 8 c .. 8 c + 7
+ * share the four words of Philox-4x32-10 (Salmon et al., 2011) with the counter (c, row, use & 2^32 - 1, use >> 32)
+ * and the key (seed & 2^32 - 1, seed >> 32), the even column in a word's low half. The mask depends on
+ * nothing else. */
+typedef struct moe_dropout {
+    int32_t dim;     /* 1..2^20 */
+    int32_t dtype;   /* MOE_BF16, MOE_F16 or MOE_F32 */
+    double p;        /* 0..1: the share that is dropped */
+} moe_dropout;
+
+/* y [m, dim] from x and residual [m, dim] (NULL: none), row strides >= dim, pointers aligned to their value
+ * type. rng: device, {seed, use}, 8-byte aligned, read when the call runs: a captured graph that is replayed makes a
+ * new mask once the caller has written another use there. y may be x or residual itself (same stride); no other
+ * overlap. m (up to 2^30) = 0 does nothing. MOE_EINVAL, MOE_EHIP. */
+int moe_dropout_forward(const moe_dropout* f, const uint64_t* rng, const void* x, int64_t ldx, const void* residual,
+                        int64_t ldr, int32_t m, void* y, int64_t ldy, void* stream);
+
+/* dx = keep dy / (1 - p) with the mask of the forward call, whose rng has to hold what it held then. (The
+ * residual's gradient is dy itself.) dx may be dy itself (same stride). */
+int moe_dropout_backward(const moe_dropout* f, const uint64_t* rng, const void* dy, int64_t lddy, int32_t m, void* dx,
+                         int64_t lddx, void* stream);
 
 /* Static text for a status code. */
 const char* moe_strerror(int code);

@@ -45,6 +45,7 @@ MOE_F32 = 2
 
 MOE_ACT_SILU = 0
 MOE_ACT_GELU = 1
+MOE_ACT_NONE = 2
 
 MOE_GATE_NONE = 0
 MOE_GATE_CHANNEL = 1
@@ -60,6 +61,10 @@ EXPORTED = (
     "moe_ffn_workspace", "moe_ffn_forward", "moe_ffn_backward",
     "moe_norm_workspace", "moe_norm_forward", "moe_norm_backward",
     "moe_w4_matmul", "moe_w4_gated",
+    "moe_sort_workspace", "moe_sort", "moe_dispatch_forward", "moe_dispatch_backward",
+    "moe_combine_forward", "moe_combine_backward",
+    "moe_linear_workspace", "moe_linear_forward", "moe_linear_backward",
+    "moe_dropout_forward", "moe_dropout_backward",
 )
 
 KERNEL_CLASSES = ("router", "quant_h", "topk", "bucket", "gateup", "shared_gateup", "down", "shared_down",
@@ -152,6 +157,26 @@ class moe_w4(ctypes.Structure):
     ]
 
 
+class moe_linear(ctypes.Structure):
+    _fields_ = [
+        ("cols", ctypes.c_int32),
+        ("rows", ctypes.c_int32),
+        ("experts", ctypes.c_int32),
+        ("dtype", ctypes.c_int32),
+        ("act", ctypes.c_int32),
+        ("w", ctypes.c_void_p),
+        ("bias", ctypes.c_void_p),
+    ]
+
+
+class moe_dropout(ctypes.Structure):
+    _fields_ = [
+        ("dim", ctypes.c_int32),
+        ("dtype", ctypes.c_int32),
+        ("p", ctypes.c_double),
+    ]
+
+
 class MoeError(RuntimeError):
     def __init__(self, code, where):
         self.code = code
@@ -201,6 +226,17 @@ def lib():
                                   vp, vp, vp, vp, sz, vp],
             "moe_w4_matmul": [P(moe_w4), vp, i64, i32, vp, i64, vp],
             "moe_w4_gated": [P(moe_w4), P(moe_w4), i32, ctypes.c_float, vp, i64, i32, vp, i64, vp],
+            "moe_sort_workspace": [i32, i32, i32, P(sz)],
+            "moe_sort": [vp, i32, i32, i32, vp, vp, vp, vp, sz, vp],
+            "moe_dispatch_forward": [i32, i32, vp, i64, vp, i32, i32, vp, i64, i32, vp],
+            "moe_dispatch_backward": [i32, i32, vp, i64, i32, vp, i32, i32, vp, i64, vp],
+            "moe_combine_forward": [i32, i32, vp, i64, i32, vp, vp, i32, i32, vp, i64, vp],
+            "moe_combine_backward": [i32, i32, vp, i64, vp, i64, i32, vp, vp, i32, i32, vp, i64, vp, vp],
+            "moe_linear_workspace": [P(moe_linear), i32, P(sz), P(sz), P(sz)],
+            "moe_linear_forward": [P(moe_linear), vp, i64, vp, i32, vp, i64, vp, i64, vp, sz, vp, sz, vp],
+            "moe_linear_backward": [P(moe_linear), vp, i64, vp, i32, vp, i64, vp, sz, vp, i64, vp, vp, vp, sz, vp],
+            "moe_dropout_forward": [P(moe_dropout), vp, vp, i64, vp, i64, i32, vp, i64, vp],
+            "moe_dropout_backward": [P(moe_dropout), vp, vp, i64, i32, vp, i64, vp],
         }
         for name, args in sigs.items():
             fn = getattr(L, name)
@@ -545,3 +581,143 @@ def moe_w4_gated(w_gate, w_up, x, h, act="silu", limit=0.0, stream=None):
     return _check(lib().moe_w4_gated(ctypes.byref(w_gate), ctypes.byref(w_up), _act(act, me), limit,
                                      *_rows(x, m, w_gate.cols, dt, me), m, *_rows(h, m, w_gate.rows, dt, me),
                                      _stream(stream)), me)
+
+
+def _matrix(t, rows, dim, dtype, where):
+    """A device matrix whose type and width the call takes from it -> (rows, dim, dtype); rows, dim: as given, or any."""
+    if t is None or t.dim() != 2 or (rows is not None and t.shape[0] != rows) or (dim is not None and t.shape[1] != dim):
+        raise MoeError(MOE_EINVAL, where)
+    if dtype is not None and t.dtype is not dtype:
+        raise MoeError(MOE_EINVAL, where)
+    return t.shape[0], t.shape[1], t.dtype
+
+
+def moe_sort_workspace(m, topk, n_experts):
+    """-> the bytes that moe_sort works in."""
+    size = ctypes.c_size_t()
+    _check(lib().moe_sort_workspace(m, topk, n_experts, ctypes.byref(size)), "moe_sort_workspace")
+    return size.value
+
+
+def moe_sort(idx, n_experts, row_of, pick_of, offsets, work, stream=None):
+    """The order by expert of the picks idx int32 [m, topk]: row_of [m, topk], pick_of [m * topk] (or None) and
+    offsets [n_experts + 1], all int32."""
+    me = "moe_sort"
+    m, topk, _ = _matrix(idx, None, None, torch.int32, me)
+    return _check(lib().moe_sort(
+        _whole(idx, (m, topk), torch.int32, me), m, topk, n_experts, _whole(row_of, (m, topk), torch.int32, me),
+        _whole(pick_of, (m * topk,), torch.int32, me), _whole(offsets, (n_experts + 1,), torch.int32, me), *_bytes(work, me),
+        _stream(stream)), me)
+
+
+def moe_dispatch_forward(x, row_of, xs, stream=None):
+    """xs[row_of[t, j]] = x[t]: x [m, dim], row_of [m, topk], xs [rows, dim]."""
+    me = "moe_dispatch_forward"
+    m, topk, _ = _matrix(row_of, None, None, torch.int32, me)
+    _, dim, dt = _matrix(x, m, None, None, me)
+    rows = _matrix(xs, None, dim, dt, me)[0]
+    return _check(lib().moe_dispatch_forward(_dtype(dt, me), dim, *_rows(x, m, dim, dt, me), _whole(row_of, (m, topk), torch.int32, me),
+                                             m, topk, *_rows(xs, rows, dim, dt, me), rows, _stream(stream)), me)
+
+
+def moe_dispatch_backward(dxs, row_of, dx, stream=None):
+    """dx[t] = sum over j of dxs[row_of[t, j]]."""
+    me = "moe_dispatch_backward"
+    m, topk, _ = _matrix(row_of, None, None, torch.int32, me)
+    _, dim, dt = _matrix(dx, m, None, None, me)
+    rows = _matrix(dxs, None, dim, dt, me)[0]
+    return _check(lib().moe_dispatch_backward(_dtype(dt, me), dim, *_rows(dxs, rows, dim, dt, me), rows,
+                                              _whole(row_of, (m, topk), torch.int32, me), m, topk, *_rows(dx, m, dim, dt, me),
+                                              _stream(stream)), me)
+
+
+def moe_combine_forward(e, weights, row_of, y, stream=None):
+    """y[t] = sum over j of weights[t, j] e[row_of[t, j]]: e [rows, dim], weights f32 [m, topk], y [m, dim]."""
+    me = "moe_combine_forward"
+    m, topk, _ = _matrix(row_of, None, None, torch.int32, me)
+    _, dim, dt = _matrix(y, m, None, None, me)
+    rows = _matrix(e, None, dim, dt, me)[0]
+    return _check(lib().moe_combine_forward(_dtype(dt, me), dim, *_rows(e, rows, dim, dt, me), rows,
+                                            _whole(weights, (m, topk), torch.float32, me),
+                                            _whole(row_of, (m, topk), torch.int32, me), m, topk, *_rows(y, m, dim, dt, me),
+                                            _stream(stream)), me)
+
+
+def moe_combine_backward(dy, e, weights, row_of, de=None, dweights=None, stream=None):
+    """Gradients of moe_combine_forward into the tensors that are given."""
+    me = "moe_combine_backward"
+    m, topk, _ = _matrix(row_of, None, None, torch.int32, me)
+    _, dim, dt = _matrix(dy, m, None, None, me)
+    rows = _matrix(e, None, dim, dt, me)[0]
+    return _check(lib().moe_combine_backward(
+        _dtype(dt, me), dim, *_rows(dy, m, dim, dt, me), *_rows(e, rows, dim, dt, me), rows,
+        _whole(weights, (m, topk), torch.float32, me), _whole(row_of, (m, topk), torch.int32, me), m, topk,
+        *_rows(de, rows, dim, dt, me), _whole(dweights, (m, topk), torch.float32, me), _stream(stream)), me)
+
+
+_LINEAR_ACTS = {**_ACTS, "none": MOE_ACT_NONE, None: MOE_ACT_NONE}
+
+
+def make_linear(w, bias=None, act="none"):
+    """Describe a product with bias and activation: w [rows, cols] and bias [rows], or a matrix per expert, w [experts,
+    rows, cols] and bias [experts, rows] (kept alive by the result); act "none", "silu" or "gelu"."""
+    me = "make_linear"
+    if w.dim() not in (2, 3):
+        raise MoeError(MOE_EINVAL, me)
+    rows, cols = w.shape[-2:]
+    experts, dt = w.shape[0] if w.dim() == 3 else 1, w.dtype
+    act = _LINEAR_ACTS.get(act, act)
+    if act not in (MOE_ACT_SILU, MOE_ACT_GELU, MOE_ACT_NONE):
+        raise MoeError(MOE_EINVAL, me)
+    f = moe_linear(cols, rows, experts, _dtype(dt, me), act, _whole(w, w.shape, dt, me), _whole(bias, w.shape[:-1], dt, me))
+    f.torch_dtype, f.tensors = dt, (w, bias)
+    return f
+
+
+def moe_linear_workspace(f, m):
+    """-> (forward, saved, backward) bytes for m rows."""
+    out = [ctypes.c_size_t() for _ in range(3)]
+    _check(lib().moe_linear_workspace(ctypes.byref(f), m, *[ctypes.byref(o) for o in out]), "moe_linear_workspace")
+    return tuple(o.value for o in out)
+
+
+def moe_linear_forward(f, x, y, work, offsets=None, residual=None, saved=None, stream=None):
+    """y = act(x W^T + bias) + residual, x [m, cols], y and residual [m, rows]; offsets int32 [experts + 1]: the rows of
+    each expert; saved: what moe_linear_backward takes."""
+    me, m, dt = "moe_linear_forward", x.shape[0], f.torch_dtype
+    return _check(lib().moe_linear_forward(
+        ctypes.byref(f), *_rows(x, m, f.cols, dt, me), _whole(offsets, (f.experts + 1,), torch.int32, me), m,
+        *_rows(residual, m, f.rows, dt, me), *_rows(y, m, f.rows, dt, me), *_bytes(saved, me), *_bytes(work, me),
+        _stream(stream)), me)
+
+
+def moe_linear_backward(f, x, dy, saved, work, offsets=None, dx=None, dw=None, dbias=None, stream=None):
+    """Gradients of moe_linear_forward into the tensors that are given; dw and dbias have the shapes of w and bias."""
+    me, m, dt = "moe_linear_backward", x.shape[0], f.torch_dtype
+    w, bias = f.tensors
+    return _check(lib().moe_linear_backward(
+        ctypes.byref(f), *_rows(x, m, f.cols, dt, me), _whole(offsets, (f.experts + 1,), torch.int32, me), m,
+        *_rows(dy, m, f.rows, dt, me), *_bytes(saved, me), *_rows(dx, m, f.cols, dt, me), _whole(dw, w.shape, dt, me),
+        _whole(dbias, w.shape[:-1], dt, me), *_bytes(work, me), _stream(stream)), me)
+
+
+def make_dropout(dim, dtype, p):
+    """Describe dropout of rows of dim values of that type with probability p."""
+    f = moe_dropout(dim, _dtype(dtype, "make_dropout"), p)
+    f.torch_dtype = dtype
+    return f
+
+
+def moe_dropout_forward(f, rng, x, y, residual=None, stream=None):
+    """y = residual + keep x / (1 - p); rng int64 [2]: seed and use, on the device."""
+    me, m, dt = "moe_dropout_forward", x.shape[0], f.torch_dtype
+    return _check(lib().moe_dropout_forward(
+        ctypes.byref(f), _whole(rng, (2,), torch.int64, me), *_rows(x, m, f.dim, dt, me), *_rows(residual, m, f.dim, dt, me), m,
+        *_rows(y, m, f.dim, dt, me), _stream(stream)), me)
+
+
+def moe_dropout_backward(f, rng, dy, dx, stream=None):
+    """dx = keep dy / (1 - p) with the mask of the forward call."""
+    me, m, dt = "moe_dropout_backward", dy.shape[0], f.torch_dtype
+    return _check(lib().moe_dropout_backward(ctypes.byref(f), _whole(rng, (2,), torch.int64, me), *_rows(dy, m, f.dim, dt, me), m,
+                                             *_rows(dx, m, f.dim, dt, me), _stream(stream)), me)
