@@ -183,7 +183,7 @@ __global__ __launch_bounds__(64 * WQ * WP) void ffn_gemm_kernel(FfnArgs a, Plan 
     const int kt0 = split < 0 ? 0 : (int)((int64_t)split * steps / plan.splits);
     const int nk = (split < 0 ? steps : (int)((int64_t)(split + 1) * steps / plan.splits)) - kt0;
     f32x4 acc[NI][NJ];
-    Product::run(t.P, t.Q, t.segs, t.q0, t.p0, kt0, nk, smem, acc);
+    Product::run({t.P, t.Q, t.segs, t.q0, t.p0, kt0, nk}, smem, acc);
 
     if (split >= 0) {
         f32x4* o = reinterpret_cast<f32x4*>(plan.partial) + (size_t)(split * plan.rest + tile - plan.whole) * NI * NJ * TH + tid;

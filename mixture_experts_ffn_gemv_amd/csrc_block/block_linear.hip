@@ -24,20 +24,33 @@ constexpr bool q_by_rows(Kind k) { return k == DW; }
 
 struct LinArgs {
     const uint16_t *x, *w, *bias, *residual, *dy, *dz;
-    float* z;              // [m, z_ld(N)]
+    float* z;              // [m, padded(N)]
     uint16_t *y, *dx, *dw, *dbias, *dz_out;
     const int32_t* offsets;   // [experts + 1]; NULL: one matrix for all rows
     int64_t ldx, ldr, ldy, lddy, lddz, lddx;
     int m, N, K, experts, act;
     float* partial;        // column sums, [chunk + expert][N]
 };
-MOE_DEV __host__ int z_ld(int N) { return (N + 3) / 4 * 4; }
-MOE_DEV __host__ int dz_ld(int N) { return (N + 7) / 8 * 8; }
+// rows of z and dz are padded to whole chunks of eight values
+MOE_DEV __host__ int padded(int N) { return (N + 7) / 8 * 8; }
 
-MOE_DEV float act_any(float v, int act) { return act == MOE_ACT_NONE ? v : act_value(v, act); }
+// act(v) with the hardware's reciprocal, which is off by 2^-23 (a division is ten instructions)
+template <int ACT>
+MOE_DEV float act_of(float v) {
+    if (ACT == MOE_ACT_NONE) return v;
+    float z = v;
+    if (ACT == MOE_ACT_GELU) {
+        const float c = fminf(fmaxf(v, -100.f), 100.f);   // (there tanh is 1 to the last bit, and c^3 finite)
+        z = 2.f * 0.7978845608028654f * (c + 0.044715f * c * c * c);
+    }
+    return v * __builtin_amdgcn_rcpf(1.0f + __expf(-z));
+}
 
 // 64 offsets at a time, one per lane; what lies outside 0..m or goes back does not count
 MOE_DEV int offset_at(const LinArgs& a, int i) { return min(max(a.offsets[min(i, a.experts)], 0), a.m); }
+
+// the same of one i for the whole wavefront
+MOE_DEV int offset_of(const LinArgs& a, int i) { return __builtin_amdgcn_readfirstlane(offset_at(a, i)); }
 
 // A tile among those of `rows`-row tiles of the experts' rows: which expert, where it begins, its
 // rows; np tiles side by side. Every lane of the wavefront calls it.
@@ -73,28 +86,44 @@ MOE_DEV Slice find_slice(const LinArgs& a, int rows, int np, int tile) {
     return s;
 }
 
-// four consecutive values at p + 0..3 of a row, of which `left` are there; no alignment but the values'
-template <typename T>
-MOE_DEV void load4(const uint16_t* p, int left, float (&v)[4]) {
-    uint2 q = make_uint2(0, 0);
-    if (left >= 4) __builtin_memcpy(&q, p, 8);
-    else {
-        uint16_t b[4] = {0, 0, 0, 0};
-        for (int i = 0; i < 3; ++i)
-            if (i < left) b[i] = p[i];
-        q = make_uint2(b[0] | (uint32_t)b[1] << 16, b[2] | (uint32_t)b[3] << 16);
+// eight consecutive 16-bit values of a row, of which `left` > 0 are there; no alignment but a value's
+MOE_DEV uint4 load8(const uint16_t* p, int left) {
+    uint4 q = make_uint4(0, 0, 0, 0);
+    if (left >= 8) {
+        __builtin_memcpy(&q, p, 16);
+    } else {   // four, two and one of them
+        if (left & 4) __builtin_memcpy(&q, p, 8);
+        uint32_t two = 0;
+        if (left & 2) __builtin_memcpy(&two, p + (left & 4), 4);
+        const uint32_t one = left & 1 ? p[left - 1] : 0u, at = left & 6;
+        if (left & 4) q.z = two;
+        else q.x = two;
+        if (at == 0) q.x = one;
+        if (at == 2) q.y = one;
+        if (at == 4) q.z = one;
+        if (at == 6) q.w = one;
     }
-    v[0] = T::lo(q.x), v[1] = T::hi(q.x), v[2] = T::lo(q.y), v[3] = T::hi(q.y);
+    return q;
+}
+MOE_DEV void store8(uint16_t* p, int left, uint4 q) {
+    if (left >= 8) {
+        __builtin_memcpy(p, &q, 16);
+    } else {
+        if (left & 4) __builtin_memcpy(p, &q, 8);
+        const uint32_t two = left & 4 ? q.z : q.x, at = left & 6;
+        if (left & 2) __builtin_memcpy(p + (left & 4), &two, 4);
+        if (left & 1) p[left - 1] = (uint16_t)(at == 0 ? q.x : at == 2 ? q.y : at == 4 ? q.z : q.w);
+    }
 }
 template <typename T>
-MOE_DEV void store4(uint16_t* p, int left, const float (&v)[4]) {
-    const uint2 q = make_uint2(T::pack2(v[0], v[1]), T::pack2(v[2], v[3]));
-    if (left >= 4) __builtin_memcpy(p, &q, 8);
-    else {
-        const uint16_t b[4] = {(uint16_t)q.x, (uint16_t)(q.x >> 16), (uint16_t)q.y, (uint16_t)(q.y >> 16)};
-        for (int i = 0; i < 3; ++i)
-            if (i < left) p[i] = b[i];
-    }
+MOE_DEV void unpack8(const uint4& q, float (&v)[8]) {
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[2 * i] = T::lo(w[i]), v[2 * i + 1] = T::hi(w[i]);
+}
+template <typename T>
+MOE_DEV uint4 pack8(const float (&v)[8]) {
+    return make_uint4(T::pack2(v[0], v[1]), T::pack2(v[2], v[3]), T::pack2(v[4], v[5]), T::pack2(v[6], v[7]));
 }
 
 // Where a tile lies and what it multiplies
@@ -113,8 +142,8 @@ MOE_DEV Tile locate(const LinArgs& a, int tile, int nq, int np) {
             const int each = nq * np;
             t.expert = tile / each;
             tile -= t.expert * each;
-            t.row0 = offset_at(a, t.expert);
-            rows = max(offset_at(a, t.expert + 1) - t.row0, 0);
+            t.row0 = offset_of(a, t.expert);
+            rows = max(offset_of(a, t.expert + 1) - t.row0, 0);
         } else {
             const Slice s = find_slice(a, BQ, np, tile);
             t.expert = s.expert, t.row0 = s.row0, rows = s.rows, tile = s.tile;
@@ -126,8 +155,8 @@ MOE_DEV Tile locate(const LinArgs& a, int tile, int nq, int np) {
     const uint16_t* const dz = a.dz + t.row0 * a.lddz;
     // (dz's rows are padded to whole chunks with zeros)
     if (KIND == FWD) t.P = {w, w, a.K, a.N, a.K}, t.Q = {x, x, a.ldx, rows, a.K};
-    if (KIND == DX) t.P = {w, w, a.K, a.K, a.N}, t.Q = {dz, dz, a.lddz, rows, dz_ld(a.N)};
-    if (KIND == DW) t.P = {x, x, a.ldx, a.K, rows}, t.Q = {dz, dz, a.lddz, dz_ld(a.N), rows};
+    if (KIND == DX) t.P = {w, w, a.K, a.K, a.N}, t.Q = {dz, dz, a.lddz, rows, padded(a.N)};
+    if (KIND == DW) t.P = {x, x, a.ldx, a.K, rows}, t.Q = {dz, dz, a.lddz, padded(a.N), rows};
     // eight q tiles deep, so that the tiles an XCD works on at a time share their operands in its L2
     const int deep = 8 * np, gr = tile / deep, gq = min(8, nq - gr * 8), in = tile - gr * deep;
     t.q0 = (gr * 8 + in % gq) * BQ;
@@ -135,47 +164,79 @@ MOE_DEV Tile locate(const LinArgs& a, int tile, int nq, int np) {
     return t;
 }
 
-// What a wavefront does with the sums of 16 q (q = qw + l16) and its TP p: a lane holds p =
-// 16 i + 4 g + 0..3 in v[i], counted from pw
-template <typename T, Kind KIND, int NI>
-MOE_DEV void finish(const LinArgs& a, const Tile& t, int qw, int pw, const f32x4 (&v)[NI]) {
-    const int lane = threadIdx.x & 63, l16 = lane & 15, g = lane >> 4, q = qw + l16;
-    const int extent = KIND == FWD ? a.N : a.K;
-    if (q >= (KIND == DW ? a.N : t.Q.rows)) return;
-#pragma unroll
-    for (int i = 0; i < NI; ++i) {
-        const int p = t.p0 + pw + 16 * i + 4 * g, left = extent - p;
-        if (left <= 0) continue;
-        float o[4] = {v[i][0], v[i][1], v[i][2], v[i][3]};
-        if constexpr (KIND == FWD) {
-            const int64_t row = t.row0 + q;
-            if (a.bias != nullptr) {
-                float b[4];
-                load4<T>(a.bias + (size_t)t.expert * a.N + p, left, b);
-#pragma unroll
-                for (int r = 0; r < 4; ++r) o[r] += b[r];
-            }
-            if (a.z != nullptr) *reinterpret_cast<f32x4*>(a.z + row * z_ld(a.N) + p) = (f32x4){o[0], o[1], o[2], o[3]};
-#pragma unroll
-            for (int r = 0; r < 4; ++r) o[r] = act_any(o[r], a.act);
-            if (a.residual != nullptr) {
-                float b[4];
-                load4<T>(a.residual + row * a.ldr + p, left, b);
-#pragma unroll
-                for (int r = 0; r < 4; ++r) o[r] += b[r];
-            }
-            store4<T>(a.y + row * a.ldy + p, left, o);
-        } else if constexpr (KIND == DX) {
-            store4<T>(a.dx + (t.row0 + q) * a.lddx + p, 4, o);   // (K is a multiple of 8)
-        } else {
-            store4<T>(a.dw + ((size_t)t.expert * a.N + q) * a.K + p, 4, o);
-        }
+// What a wavefront does with its sums of 16 NJ q (from qw) and TP p (from pw): v[i][j] of a lane is p = 16 i +
+// 4 g + 0..3 of q = 16 j + l16. They pass through the wavefront's own piece of LDS, SLAB bytes, a few rows at
+// a time, so that a lane has eight values of one row, and its neighbours the ones beside them: memory is
+// read and written in whole lines (four values a lane wrote quarters of them).
+// what other lanes of the wavefront wrote to LDS before is read after, and the other way round
+MOE_DEV void wave_fence() {
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+}
+template <int TP>
+struct Slab {
+    static constexpr int LPR = TP / 8, ROWS = 64 / LPR >= 16 ? 16 : 8, STRIDE = TP + 4;   // lanes per row
+    static constexpr int BYTES = ROWS * STRIDE * 4;
+};
+template <typename T, Kind KIND, int ACT, int TP, int NI, int NJ>
+MOE_DEV void finish(const LinArgs& a, const Tile& t, int qw, int pw, const f32x4 (&v)[NI][NJ], float* slab) {
+    typedef Slab<TP> S;
+    // (opaque, so that what follows from it is not kept in registers while the next piece is multiplied)
+    int lane = threadIdx.x & 63;
+    asm volatile("" : "+v"(lane));
+    const int l16 = lane & 15, g = lane >> 4;
+    const int r = lane / S::LPR, c = lane % S::LPR * 8;
+    const int rows = KIND == DW ? a.N : t.Q.rows, p = t.p0 + pw + c, left = (KIND == FWD ? a.N : a.K) - p;
+    if (qw >= rows) return;
+    const bool mine = lane < S::ROWS * S::LPR && left > 0;
+    float b[8];
+    if (KIND == FWD) {
+        const uint4 q = a.bias != nullptr && mine ? load8(a.bias + (size_t)t.expert * a.N + p, left) : make_uint4(0, 0, 0, 0);
+        unpack8<T>(q, b);
     }
+    auto residual = [&](int q) { return a.residual != nullptr && mine && q < rows ? load8(a.residual + (t.row0 + q) * a.ldr + p, left) : make_uint4(0, 0, 0, 0); };
+    uint4 next = KIND == FWD ? residual(qw + r) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int j = 0; j < NJ; ++j)
+#pragma unroll
+        for (int h = 0; h < 16 / S::ROWS; ++h) {
+            if (S::ROWS == 16 || (l16 >> 3) == h) {
+#pragma unroll
+                for (int i = 0; i < NI; ++i) *reinterpret_cast<f32x4*>(&slab[(l16 & (S::ROWS - 1)) * S::STRIDE + 16 * i + 4 * g]) = v[i][j];
+            }
+            wave_fence();
+            const int at = mine ? r * S::STRIDE + c : 0;
+            const f32x4 lo = *reinterpret_cast<const f32x4*>(&slab[at]), hi = *reinterpret_cast<const f32x4*>(&slab[at + 4]);
+            wave_fence();
+            const int q = qw + 16 * j + S::ROWS * h + r;
+            const int64_t row = t.row0 + q;
+            float o[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+            if constexpr (KIND == FWD) {
+                const uint4 here = next;
+                next = residual(q + S::ROWS);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) o[i] += b[i];
+                if (mine && q < rows) {
+                    if (ACT != MOE_ACT_NONE && a.z != nullptr) {
+                        float* z = a.z + row * padded(a.N) + p;
+                        *reinterpret_cast<f32x4*>(z) = (f32x4){o[0], o[1], o[2], o[3]};
+                        *reinterpret_cast<f32x4*>(z + 4) = (f32x4){o[4], o[5], o[6], o[7]};
+                    }
+                    float res[8];
+                    unpack8<T>(here, res);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) o[i] = act_of<ACT>(o[i]) + res[i];
+                    store8(a.y + row * a.ldy + p, left, pack8<T>(o));
+                }
+            } else if (mine && q < rows) {   // (K is a multiple of 8)
+                uint16_t* const to = KIND == DX ? a.dx + row * a.lddx : a.dw + ((size_t)t.expert * a.N + q) * a.K;
+                *reinterpret_cast<uint4*>(to + p) = pack8<T>(o);
+            }
+        }
 }
 
-// The work of one launch: the first `whole` tiles by a workgroup each, the `rest` (what does
-// not fill the CUs once more) by `splits` workgroups each, every one with its part of k. With an
-// expert's rows per tile `whole` is only a bound.
+// The work of one launch: the first `whole` tiles, each in one piece, and the `rest` (what does not fill the
+// CUs once more) in `splits` pieces along k. With an expert's rows per tile `whole` is only a bound.
 struct Plan {
     int nq, np;          // tiles along q and p
     int whole, rest, splits;
@@ -185,70 +246,92 @@ struct Plan {
 template <typename T, Kind KIND, int BQ, int BP, int WQ, int WP>
 using LinTile = TileProduct<T, p_by_rows(KIND), q_by_rows(KIND), false, BQ, BP, WQ, WP>;
 
-template <typename T, Kind KIND, int BQ, int BP, int WQ, int WP>
+// A workgroup takes one piece after another. The loads of the next piece's first two steps are under way while it
+// finishes the one before, and its stores while it multiplies the next.
+template <typename T, Kind KIND, int ACT, int BQ, int BP, int WQ, int WP>
 __global__ __launch_bounds__(64 * WQ * WP) void linear_kernel(LinArgs a, Plan plan) {
     extern __shared__ __align__(16) uint8_t smem[];
     typedef LinTile<T, KIND, BQ, BP, WQ, WP> Product;
     constexpr int TH = Product::TH, NI = Product::NI, NJ = Product::NJ;
     const int tid = threadIdx.x, wv = __builtin_amdgcn_readfirstlane(tid >> 6), wq = wv / WP, wp = wv % WP;
+    float* const slab = reinterpret_cast<float*>(smem + Product::LDS + wv * Slab<Product::TP>::BYTES);
 
-    // consecutive tiles (of a split part: those of one part of k) on one XCD
-    const int whole_blocks = (plan.whole + 7) / 8 * 8;
-    int tile, split = -1;
-    if ((int)blockIdx.x < whole_blocks) {
-        const int whole = a.offsets != nullptr && KIND != DW ? tiles_total(a, BQ) * plan.np : plan.whole;
-        tile = xcd_logical_block(blockIdx.x, whole);
-        if (tile >= whole) return;
-    } else {
-        const int items = plan.rest * plan.splits, item = xcd_logical_block(blockIdx.x - whole_blocks, items);
-        if (item >= items) return;
-        split = item / plan.rest;
-        tile = plan.whole + item - split * plan.rest;
-    }
-    const Tile t = locate<KIND, BQ, BP>(a, tile, plan.nq, plan.np);
-    const int steps = (t.P.k + BK - 1) / BK;
-    const int kt0 = split < 0 ? 0 : (int)((int64_t)split * steps / plan.splits);
-    const int nk = (split < 0 ? steps : (int)((int64_t)(split + 1) * steps / plan.splits)) - kt0;
-    f32x4 acc[NI][NJ];
-    Product::run(t.P, t.Q, 1, t.q0, t.p0, kt0, nk, smem, acc);
-
-    if (split >= 0) {
-        f32x4* o = reinterpret_cast<f32x4*>(plan.partial) + (size_t)(split * plan.rest + tile - plan.whole) * NI * NJ * TH + tid;
+    // An eighth of the tiles, side by side, and of the pieces for each XCD, whose workgroups take them in turn
+    const int whole = a.offsets != nullptr && KIND != DW ? tiles_total(a, BQ) * plan.np : plan.whole;
+    const int pieces = plan.rest * plan.splits, xcd = blockIdx.x & 7, step = gridDim.x >> 3;
+    const int w0 = xcd * ((whole + 7) >> 3), w1 = min(w0 + ((whole + 7) >> 3), whole);
+    const int s0 = xcd * ((pieces + 7) >> 3), s1 = min(s0 + ((pieces + 7) >> 3), pieces);
+    struct Piece {
+        Tile t;
+        int tile, split, kt0, nk;   // split < 0: a whole tile
+    };
+    int at = blockIdx.x >> 3;
+    auto take = [&](Piece& x) -> bool {
+        const int n = max(w1 - w0, 0);
+        if (at < n) {
+            x.tile = w0 + at, x.split = -1;
+        } else {
+            const int item = s0 + at - n;
+            if (item >= s1) return false;
+            x.split = item / plan.rest;
+            x.tile = plan.whole + item - x.split * plan.rest;
+        }
+        at += step;
+        x.t = locate<KIND, BQ, BP>(a, x.tile, plan.nq, plan.np);
+        const int steps = (x.t.P.k + BK - 1) / BK;
+        x.kt0 = x.split < 0 ? 0 : (int)((int64_t)x.split * steps / plan.splits);
+        x.nk = (x.split < 0 ? steps : (int)((int64_t)(x.split + 1) * steps / plan.splits)) - x.kt0;
+        return true;
+    };
+    Piece now;
+    if (!take(now)) return;
+    Product::begin({now.t.P, now.t.Q, 1, now.t.q0, now.t.p0, now.kt0, now.nk}, smem);
+    for (;;) {
+        f32x4 acc[NI][NJ];
+        Product::template sums<true>({now.t.P, now.t.Q, 1, now.t.q0, now.t.p0, now.kt0, now.nk}, smem, acc);
+        Piece next;
+        const bool more = take(next);
+        barrier_lds();   // every wavefront has read the last step
+        // (the pointers are the lambda's own restricted ones so that the compiler does not wait for the next
+        // piece's loads before it reads the slab)
+        [&](uint8_t* __restrict buffers, float* __restrict mine) {
+            if (more) Product::begin({next.t.P, next.t.Q, 1, next.t.q0, next.t.p0, next.kt0, next.nk}, buffers);
+            if (now.split >= 0) {
+                f32x4* o = reinterpret_cast<f32x4*>(plan.partial) + (size_t)(now.split * plan.rest + now.tile - plan.whole) * NI * NJ * TH + tid;
 #pragma unroll
-        for (int j = 0; j < NJ; ++j)
+                for (int j = 0; j < NJ; ++j)
 #pragma unroll
-            for (int i = 0; i < NI; ++i) o[(j * NI + i) * TH] = acc[i][j];
-        return;
-    }
-#pragma unroll
-    for (int j = 0; j < NJ; ++j) {
-        f32x4 v[NI];
-#pragma unroll
-        for (int i = 0; i < NI; ++i) v[i] = acc[i][j];
-        finish<T, KIND, NI>(a, t, t.q0 + wq * Product::TQ + 16 * j, wp * Product::TP, v);
+                    for (int i = 0; i < NI; ++i) o[(j * NI + i) * TH] = acc[i][j];
+            } else {
+                finish<T, KIND, ACT, Product::TP, NI, NJ>(a, now.t, now.t.q0 + wq * Product::TQ, wp * Product::TP, acc, mine);
+            }
+        }(smem, slab);
+        if (!more) return;
+        now = next;
     }
 }
 
 // The split tiles' sums, added in order of k, and what is done with them: a workgroup per
 // tile and j (16 q of each wavefront)
-template <typename T, Kind KIND, int BQ, int BP, int WQ, int WP>
+template <typename T, Kind KIND, int ACT, int BQ, int BP, int WQ, int WP>
 __global__ __launch_bounds__(64 * WQ * WP) void linear_join_kernel(LinArgs a, Plan plan) {
     typedef LinTile<T, KIND, BQ, BP, WQ, WP> Product;
     constexpr int TH = Product::TH, NI = Product::NI, NJ = Product::NJ;
-    const int tid = threadIdx.x, wv = tid >> 6, wq = wv / WP, wp = wv % WP;
+    __shared__ __align__(16) float slab[WQ * WP][Slab<Product::TP>::BYTES / 4];
+    const int tid = threadIdx.x, wv = __builtin_amdgcn_readfirstlane(tid >> 6), wq = wv / WP, wp = wv % WP;
     const int r = blockIdx.x / NJ, j = blockIdx.x % NJ;
     const f32x4* from = reinterpret_cast<const f32x4*>(plan.partial) + ((size_t)r * NJ + j) * NI * TH + tid;
-    f32x4 v[NI];
+    f32x4 v[NI][1];
 #pragma unroll
-    for (int i = 0; i < NI; ++i) v[i] = from[i * TH];
+    for (int i = 0; i < NI; ++i) v[i][0] = from[i * TH];
 #pragma unroll 2
     for (int s = 1; s < plan.splits; ++s) {
         const f32x4* f = from + (size_t)s * plan.rest * NI * NJ * TH;
 #pragma unroll
-        for (int i = 0; i < NI; ++i) v[i] += f[i * TH];
+        for (int i = 0; i < NI; ++i) v[i][0] += f[i * TH];
     }
     const Tile t = locate<KIND, BQ, BP>(a, plan.whole + r, plan.nq, plan.np);
-    finish<T, KIND, NI>(a, t, t.q0 + wq * Product::TQ + 16 * j, wp * Product::TP, v);
+    finish<T, KIND, ACT, Product::TP, NI, 1>(a, t, t.q0 + wq * Product::TQ + 16 * j, wp * Product::TP, v, slab[wv]);
 }
 
 // ------------------------------------------------------------------ dz and its column sums
@@ -272,26 +355,21 @@ __global__ __launch_bounds__(256) void linear_dz_kernel(LinArgs a) {
     __shared__ float lds[4][DZ_COLS];
     const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
     const int first = blockIdx.x * DZ_ROWS, n0 = blockIdx.y * DZ_COLS + lane * 8, left = a.N - n0;
-    const int last = min(first + DZ_ROWS, a.offsets != nullptr ? offset_at(a, a.experts) : a.m);
+    const int last = min(first + DZ_ROWS, a.offsets != nullptr ? offset_of(a, a.experts) : a.m);
     int row = first;
     while (row < last) {
         const int e = a.offsets != nullptr ? expert_of(a, row) : 0;
         // (offsets that go back must not hold the loop up)
-        const int end = a.offsets != nullptr ? max(min(last, offset_at(a, e + 1)), row + 1) : last;
+        const int end = a.offsets != nullptr ? max(min(last, offset_of(a, e + 1)), row + 1) : last;
         float sum[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) sum[i] = 0.f;
         for (int r = row + wv; r < end && left > 0; r += 4) {
-            float d[8], lo[4], hi[4];
-            const uint16_t* dy = a.dy + r * a.lddy + n0;
-            load4<T>(dy, left, lo);
-            if (left > 4) load4<T>(dy + 4, left - 4, hi);
-            else hi[0] = hi[1] = hi[2] = hi[3] = 0.f;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) d[i] = lo[i], d[4 + i] = hi[i];
+            float d[8];
+            unpack8<T>(load8(a.dy + r * a.lddy + n0, left), d);
             if (a.act != MOE_ACT_NONE) {
-                const float* z = a.z + (size_t)r * z_ld(a.N) + n0;
-                const f32x4 z0 = *reinterpret_cast<const f32x4*>(z), z1 = left > 4 ? *reinterpret_cast<const f32x4*>(z + 4) : z0;
+                const float* z = a.z + (size_t)r * padded(a.N) + n0;
+                const f32x4 z0 = *reinterpret_cast<const f32x4*>(z), z1 = *reinterpret_cast<const f32x4*>(z + 4);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     float f, df;
@@ -302,8 +380,7 @@ __global__ __launch_bounds__(256) void linear_dz_kernel(LinArgs a) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) sum[i] += d[i];
             if (STORE)
-                *reinterpret_cast<uint4*>(a.dz_out + r * a.lddz + n0) =
-                    make_uint4(T::pack2(d[0], d[1]), T::pack2(d[2], d[3]), T::pack2(d[4], d[5]), T::pack2(d[6], d[7]));
+                *reinterpret_cast<uint4*>(a.dz_out + r * a.lddz + n0) = pack8<T>(d);
         }
         if (a.partial != nullptr) {
             *reinterpret_cast<f32x4*>(&lds[wv][lane * 8]) = (f32x4){sum[0], sum[1], sum[2], sum[3]};
@@ -324,7 +401,7 @@ template <typename T>
 __global__ __launch_bounds__(1024) void linear_bias_kernel(LinArgs a) {
     __shared__ float lds[16][64];
     const int c = threadIdx.x & 63, g = threadIdx.x >> 6, e = blockIdx.y, n = blockIdx.x * 64 + c;
-    const int r0 = a.offsets != nullptr ? offset_at(a, e) : 0, r1 = a.offsets != nullptr ? offset_at(a, e + 1) : a.m;
+    const int r0 = a.offsets != nullptr ? offset_of(a, e) : 0, r1 = a.offsets != nullptr ? offset_of(a, e + 1) : a.m;
     float s = 0.f;
     if (n < a.N && r1 > r0)
         for (int b = r0 / DZ_ROWS + g; b <= (r1 - 1) / DZ_ROWS; b += 16) s += a.partial[(size_t)(b + e) * a.N + n];
@@ -351,7 +428,7 @@ MOE_DEV __host__ int few_pass(int rows, int K) {
     return whole < fit ? whole : fit;
 }
 
-template <typename T>
+template <typename T, int ACT>
 __global__ __launch_bounds__(64 * FEW_WAVES) void linear_few_kernel(LinArgs a, int room) {
     constexpr int AHEAD = 5;
     extern __shared__ __align__(16) uint8_t smem[];   // x; then sums [wavefront][256]
@@ -407,12 +484,12 @@ __global__ __launch_bounds__(64 * FEW_WAVES) void linear_few_kernel(LinArgs a, i
     *reinterpret_cast<f32x4*>(&red[wv * 256 + lane * 4]) = acc;
     __syncthreads();
     if (tid >= 64) return;
-    f32x4 v[1] = {{0.f, 0.f, 0.f, 0.f}};
+    f32x4 v[1][1] = {{{0.f, 0.f, 0.f, 0.f}}};
 #pragma unroll
-    for (int i = 0; i < FEW_WAVES; ++i) v[0] += *reinterpret_cast<const f32x4*>(&red[i * 256 + lane * 4]);
+    for (int i = 0; i < FEW_WAVES; ++i) v[0][0] += *reinterpret_cast<const f32x4*>(&red[i * 256 + lane * 4]);
     Tile t;
     t.expert = s.expert, t.row0 = row0, t.p0 = n0, t.Q.rows = rows;
-    finish<T, FWD, 1>(a, t, 0, 0, v);
+    finish<T, FWD, ACT, 16, 1, 1>(a, t, 0, 0, v, red);   // (one wavefront, which has read what was there)
 }
 
 // ------------------------------------------------------------------ plans
@@ -485,22 +562,25 @@ Product plan_product(Kind kind, int m, int N, int K, int experts) {
     return best;
 }
 
-template <typename T, Kind KIND, int B, int WQ, int WP>
+template <typename T, Kind KIND, int ACT, int B, int WQ, int WP>
 hipError_t launch_tiles(const LinArgs& a, const Plan& plan, hipStream_t st) {
-    const int grid = (plan.whole + 7) / 8 * 8 + (plan.rest * plan.splits + 7) / 8 * 8;
-    if (grid == 0) return hipSuccess;
     typedef LinTile<T, KIND, B, B, WQ, WP> P;
-    const hipError_t e = launch_kernel(linear_kernel<T, KIND, B, B, WQ, WP>, dim3(grid), dim3(P::TH), P::LDS, st, a, plan);
+    constexpr int SLOTS = B == 256 ? N_CU : 2 * N_CU;
+    const int64_t work = plan.whole + (int64_t)plan.rest * plan.splits;
+    if (work == 0) return hipSuccess;
+    const int grid = (int)std::min<int64_t>(SLOTS, (work + 7) / 8 * 8);
+    const hipError_t e = launch_kernel(linear_kernel<T, KIND, ACT, B, B, WQ, WP>, dim3(grid), dim3(P::TH),
+                                       P::LDS + WQ * WP * Slab<P::TP>::BYTES, st, a, plan);
     if (e != hipSuccess || plan.rest == 0) return e;
-    return launch_kernel(linear_join_kernel<T, KIND, B, B, WQ, WP>, dim3(plan.rest * P::NJ), dim3(P::TH), 0, st, a, plan);
+    return launch_kernel(linear_join_kernel<T, KIND, ACT, B, B, WQ, WP>, dim3(plan.rest * P::NJ), dim3(P::TH), 0, st, a, plan);
 }
 
-template <typename T, Kind KIND>
+template <typename T, Kind KIND, int ACT>
 hipError_t launch_product(const LinArgs& a, float* partial, hipStream_t st) {
     Product p = plan_product(KIND, a.m, a.N, a.K, a.offsets != nullptr ? std::max(a.experts, 2) : 1);
     if (a.offsets != nullptr && a.experts == 1 && KIND == DW) p = plan_product(KIND, a.m, a.N, a.K, 1);
     p.plan.partial = partial;
-    return p.tile == 256 ? launch_tiles<T, KIND, 256, 2, 4>(a, p.plan, st) : launch_tiles<T, KIND, 128, 2, 2>(a, p.plan, st);
+    return p.tile == 256 ? launch_tiles<T, KIND, ACT, 256, 2, 4>(a, p.plan, st) : launch_tiles<T, KIND, ACT, 128, 2, 2>(a, p.plan, st);
 }
 
 constexpr int MAX_M = 1 << 24, MAX_N = 1 << 17, MAX_K = 1 << 16, MAX_EXPERTS = 1024;
@@ -520,9 +600,9 @@ bool rows_ok(const void* p, int64_t ld, int dim) {
 
 size_t forward_bytes(const moe_linear* f, int m) { return round_up(partial_bytes(FWD, m, f->rows, f->cols, f->experts), 256); }
 size_t saved_bytes_of(const moe_linear* f, int m) {
-    return f->act == MOE_ACT_NONE ? 0 : round_up((size_t)m * z_ld(f->rows) * 4, 256);
+    return f->act == MOE_ACT_NONE ? 0 : round_up((size_t)m * padded(f->rows) * 4, 256);
 }
-size_t dz_bytes(const moe_linear* f, int m) { return round_up((size_t)m * dz_ld(f->rows) * 2, 256); }
+size_t dz_bytes(const moe_linear* f, int m) { return round_up((size_t)m * padded(f->rows) * 2, 256); }
 size_t sums_bytes(const moe_linear* f, int m) {
     return f->bias == nullptr ? 0 : round_up((size_t)(cdiv(m, DZ_ROWS) + f->experts) * f->rows * 4, 256);
 }
@@ -540,13 +620,19 @@ LinArgs describe(const moe_linear* f, int m, const int32_t* offsets) {
     return a;
 }
 
-template <typename T>
-hipError_t forward(const LinArgs& a, float* partial, hipStream_t st) {
+template <typename T, int ACT>
+hipError_t forward_act(const LinArgs& a, float* partial, hipStream_t st) {
     const int each = cdiv(a.m, a.experts);   // rows of an expert, on average
-    if (each > FEW_ROWS) return launch_product<T, FWD>(a, partial, st);
+    if (each > FEW_ROWS) return launch_product<T, FWD, ACT>(a, partial, st);
     const int room = std::min(a.m, FEW_ROWS), items = a.offsets != nullptr ? a.m / room + std::min(a.experts, a.m) : cdiv(a.m, room);
     const size_t lds = std::max<size_t>((size_t)room * few_pass(room, a.K) * 2, sizeof(float) * FEW_WAVES * 256);
-    return launch_kernel(linear_few_kernel<T>, dim3(cdiv(a.N, 16), items), dim3(64 * FEW_WAVES), lds, st, a, room);
+    return launch_kernel(linear_few_kernel<T, ACT>, dim3(cdiv(a.N, 16), items), dim3(64 * FEW_WAVES), lds, st, a, room);
+}
+template <typename T>
+hipError_t forward(const LinArgs& a, float* partial, hipStream_t st) {
+    return a.act == MOE_ACT_NONE   ? forward_act<T, MOE_ACT_NONE>(a, partial, st)
+           : a.act == MOE_ACT_SILU ? forward_act<T, MOE_ACT_SILU>(a, partial, st)
+                                   : forward_act<T, MOE_ACT_GELU>(a, partial, st);
 }
 
 template <typename T>
@@ -564,8 +650,8 @@ hipError_t backward(LinArgs a, uint8_t* work, size_t work_dz, bool direct, hipSt
         d.partial = partial;
         e = launch_kernel(linear_bias_kernel<T>, dim3(cdiv(a.N, 64), a.experts), dim3(1024), 0, st, d);
     }
-    if (e == hipSuccess && a.dx != nullptr && a.m > 0) e = launch_product<T, DX>(a, partial, st);
-    if (e == hipSuccess && a.dw != nullptr) e = launch_product<T, DW>(a, partial, st);
+    if (e == hipSuccess && a.dx != nullptr && a.m > 0) e = launch_product<T, DX, MOE_ACT_NONE>(a, partial, st);
+    if (e == hipSuccess && a.dw != nullptr) e = launch_product<T, DW, MOE_ACT_NONE>(a, partial, st);
     return e;
 }
 
@@ -630,7 +716,7 @@ int moe_linear_backward(const moe_linear* f, const void* x, int64_t ldx, const i
         // with no activation dy is the operand itself, where its rows are whole chunks
         direct = f->act == MOE_ACT_NONE && f->rows % 8 == 0 && rows_ok(dy, lddy, f->rows);
         a.dz_out = reinterpret_cast<uint16_t*>(work);
-        a.dz = direct ? a.dy : a.dz_out, a.lddz = direct ? lddy : dz_ld(f->rows);
+        a.dz = direct ? a.dy : a.dz_out, a.lddz = direct ? lddy : padded(f->rows);
     }
     a.dw = reinterpret_cast<uint16_t*>(dw);
     a.dbias = reinterpret_cast<uint16_t*>(dbias);

@@ -73,68 +73,101 @@ MOE_DEV void interleave() {
 template <typename T, bool PR, bool QR, bool PAIRED, int BQ, int BP, int WQ, int WP>
 struct TileProduct {
     static constexpr int TH = 64 * WQ * WP, TQ = BQ / WQ, TP = BP / WP, NI = TP / 16, NJ = TQ / 16;
-    static constexpr int UP = BP * 8 / TH, UQ = BQ * 8 / TH, NW = TH / 64;   // 16-byte units per thread
-    static constexpr int P_BYTES = tile_bytes(BP, PR), STEP = P_BYTES + tile_bytes(BQ, QR);
+    // a tile of 64 k x rows has room for 128 or 256 rows
+    static constexpr int RP = PR && BP > 128 ? 256 : BP, RQ = BQ;
+    static constexpr int UP = RP * 8 / TH, UQ = RQ * 8 / TH, NW = TH / 64;   // 16-byte units per thread
+    static constexpr int P_BYTES = tile_bytes(RP, PR), STEP = P_BYTES + tile_bytes(RQ, QR);
     static constexpr int PSPAN = PAIRED ? BP / 2 : BP;
     static constexpr size_t LDS = 2 * STEP;
     static_assert(NW == 8 || NW == 4, "");
+    static_assert((!PR || RP == 128 || RP == 256) && (!QR || RQ == 128 || RQ == 256) && (!PAIRED || RP == BP), "");
 
-    // K steps kt0 .. kt0 + nk - 1 of the tile at (q0, p0); segs matrices one after another along k
-    static MOE_DEV void run(const Operand& P, const Operand& Q, int segs, int q0, int p0, int kt0, int nk, uint8_t* smem,
-                            f32x4 (&acc)[NI][NJ]) {
+    // A product's tile and its K steps kt0 .. kt0 + nk - 1; segs matrices one after another along k
+    struct Work {
+        const Operand &P, &Q;
+        int segs, q0, p0, kt0, nk;
+    };
+
+    // This thread's first unit of each tile: its byte offset from the tile's corner; unit u is
+    // unit_rows(u) rows further. A K-contiguous tile's units of a thread share their chunk of k.
+    struct Units {
+        uint32_t off_p, off_q, none_p;   // none_p: all ones where a lane has none of P's rows
+        int chunk;
+    };
+    static MOE_DEV Units units(const Work& w) {
         const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-        const int l16 = lane & 15, g = lane >> 4, wq = wv / WP, wp = wv % WP;
-
-
-        // This thread's first unit of each tile: its byte offset from the tile's corner; unit u is
-        // unit_rows(u) rows further. A K-contiguous tile's units of a thread share their chunk of k.
-        const int slot_p = PR ? lane / (BP / 8) : 0, slot_q = QR ? lane / (BQ / 8) : 0;
+        const int slot_p = PR ? lane / (RP / 8) : 0, slot_q = QR ? lane / (RQ / 8) : 0;
         const int row_k = wv * 8 + (lane >> 3), chunk = (lane & 7) ^ swz_k(row_k);
         const int first = PAIRED ? (row_k & 31) : row_k;
-        const uint32_t off_p = PR ? (uint32_t)(run_row_wave(BP, NW, wv, slot_p) * P.ld + lane % (BP / 8) * 8) * 2
-                                  : (uint32_t)(first * P.ld + chunk * 8) * 2;
-        const uint32_t off_q = QR ? (uint32_t)(run_row_wave(BQ, NW, wv, slot_q) * Q.ld + lane % (BQ / 8) * 8) * 2
-                                  : (uint32_t)(row_k * Q.ld + chunk * 8) * 2;
+        Units s;
+        s.chunk = chunk;
+        s.off_p = PR ? (uint32_t)(run_row_wave(RP, NW, wv, slot_p) * w.P.ld + lane % (RP / 8) * 8) * 2
+                     : (uint32_t)(first * w.P.ld + chunk * 8) * 2;
+        s.off_q = QR ? (uint32_t)(run_row_wave(RQ, NW, wv, slot_q) * w.Q.ld + lane % (RQ / 8) * 8) * 2
+                     : (uint32_t)(row_k * w.Q.ld + chunk * 8) * 2;
+        s.none_p = PR && RP > BP && lane % (RP / 8) * 8 >= BP ? PAST : 0u;
+        return s;
+    }
 
-        const int seg_steps = (P.k + BK - 1) / BK;
-        auto stage = [&](int kt, uint8_t* buf) {
-            const bool past = kt >= nk;
-            kt += kt0;
-            const int seg = segs == 2 && kt >= seg_steps ? 1 : 0;
-            const int k0 = (kt - seg * seg_steps) * BK;
-            auto side = [&](uint32_t off, const Operand& o, bool by_rows, int R, int at, int span, bool paired, int U, uint8_t* dst) {
-                const uint16_t* base = seg ? o.b : o.a;
-                const int left = min(o.rows - at, span), kleft = min(BK, o.k - k0);
-                const uint32_t beyond = chunk * 8 >= kleft ? PAST : 0u;   // a K tail's missing chunks
-                if (by_rows) {
-                    const auto buffer = buffer_rsrc(base + (size_t)k0 * o.ld + at, past ? 0u : (uint32_t)((kleft - 1) * o.ld + left) * 2);
+    // requests step kt's tiles (past the last: zeros)
+    static MOE_DEV void stage(const Work& w, const Units& s, int kt, uint8_t* buf) {
+        const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+        const int seg_steps = (w.P.k + BK - 1) / BK;
+        const bool past = kt >= w.nk;
+        kt += w.kt0;
+        const int seg = w.segs == 2 && kt >= seg_steps ? 1 : 0;
+        const int k0 = (kt - seg * seg_steps) * BK;
+        auto side = [&](uint32_t off, const Operand& o, bool by_rows, int R, int at, int span, bool paired, int U, uint32_t none, uint8_t* dst) {
+            const uint16_t* base = seg ? o.b : o.a;
+            const int left = min(o.rows - at, span), kleft = min(BK, o.k - k0);
+            const uint32_t beyond = s.chunk * 8 >= kleft ? PAST : 0u;   // a K tail's missing chunks
+            if (by_rows) {
+                const auto buffer = buffer_rsrc(base + (size_t)k0 * o.ld + at, past ? 0u : (uint32_t)((kleft - 1) * o.ld + left) * 2);
+                // (with both operands by rows the units' offsets would not fit into the registers beside the sums)
+                if (PR && QR) asm volatile("" : "+v"(off));
 #pragma unroll
-                    for (int u = 0; u < U; ++u)
-                        buffer_load_lds16(buffer, dst + (u * NW + wv) * PIECE, off + (uint32_t)(run_row_unit(R, NW, u) * o.ld * 2));
-                } else {
-                    const uint32_t bytes = past ? 0u : (uint32_t)((left - 1) * o.ld + kleft) * 2;
-                    const size_t corner = (size_t)at * o.ld + k0;
-                    // PAIRED: rows 32..63 of every 64 are the second matrix's: with eight wavefronts those
-                    // of wavefronts 4..7, with four those of every second unit
-                    const bool second = paired && NW == 8 && (wv & 4);
-                    const auto buffer = buffer_rsrc((second ? o.b : base) + corner, bytes);
-                    const auto other = paired && NW == 4 ? buffer_rsrc(o.b + corner, bytes) : buffer;
+                for (int u = 0; u < U; ++u)
+                    buffer_load_lds16(buffer, dst + (u * NW + wv) * PIECE, (off + (uint32_t)(run_row_unit(R, NW, u) * o.ld * 2)) | none);
+            } else {
+                const uint32_t bytes = past ? 0u : (uint32_t)((left - 1) * o.ld + kleft) * 2;
+                const size_t corner = (size_t)at * o.ld + k0;
+                // PAIRED: rows 32..63 of every 64 are the second matrix's: with eight wavefronts those
+                // of wavefronts 4..7, with four those of every second unit
+                const bool second = paired && NW == 8 && (wv & 4);
+                const auto buffer = buffer_rsrc((second ? o.b : base) + corner, bytes);
+                const auto other = paired && NW == 4 ? buffer_rsrc(o.b + corner, bytes) : buffer;
 #pragma unroll
-                    for (int u = 0; u < U; ++u) {
-                        const int rows = paired ? (u * NW * 8 >> 6) * 32 : u * NW * 8;
-                        const uint32_t v = (off + (uint32_t)(rows * o.ld * 2)) | beyond;
-                        uint8_t* to = dst + (u * NW + wv) * 1024;
-                        if (paired && NW == 4 && (u & 1)) buffer_load_lds16(other, to, v);
-                        else buffer_load_lds16(buffer, to, v);
-                    }
+                for (int u = 0; u < U; ++u) {
+                    const int rows = paired ? (u * NW * 8 >> 6) * 32 : u * NW * 8;
+                    const uint32_t v = (off + (uint32_t)(rows * o.ld * 2)) | beyond;
+                    uint8_t* to = dst + (u * NW + wv) * 1024;
+                    if (paired && NW == 4 && (u & 1)) buffer_load_lds16(other, to, v);
+                    else buffer_load_lds16(buffer, to, v);
                 }
-            };
-            side(off_p, P, PR, BP, p0, PSPAN, PAIRED, UP, buf);
-            side(off_q, Q, QR, BQ, q0, BQ, false, UQ, buf + P_BYTES);
+            }
         };
+        side(s.off_p, w.P, PR, RP, w.p0, PSPAN, PAIRED, UP, s.none_p, buf);
+        side(s.off_q, w.Q, QR, RQ, w.q0, BQ, false, UQ, 0u, buf + P_BYTES);
+    }
 
+    // requests the first two steps, into buffers that nobody reads any more
+    static MOE_DEV void begin(const Work& w, uint8_t* smem) {
+        if (w.nk <= 0) return;
+        const Units s = units(w);
+        stage(w, s, 0, smem);
+        stage(w, s, 1, smem + STEP);
+    }
+
+    // the sums, after begin; AFTER: other memory operations may have followed begin's. At the end this
+    // wavefront has read all that it will of the buffers.
+    template <bool AFTER>
+    static MOE_DEV void sums(const Work& w, uint8_t* smem, f32x4 (&acc)[NI][NJ]) {
+        const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+        const int l16 = lane & 15, g = lane >> 4, wq = wv / WP, wp = wv % WP;
+        const int nk = w.nk;
+        const Units s = units(w);
         // LDS byte offset of this lane's operand reads for half kk of a step; operand i lies 16 rows
-        // further, which is a constant in either layout
+        // further, which is a constant in either layout, as the second half is in one by rows
         auto read_base = [&](bool by_rows, int R, int base, int kk) {
             if (by_rows) {
                 const int run = (l16 >> 2) + 4 * (g & 1) + (R == 256 ? 8 * (g >> 1) : 0);
@@ -142,8 +175,8 @@ struct TileProduct {
             }
             return (base + l16) * (BK * 2) + (((g + 4 * kk) ^ swz_k(l16)) << 4);
         };
-        const int rdp0 = read_base(PR, BP, wp * TP, 0), rdp1 = PR ? rdp0 + BP / 16 * PIECE : read_base(PR, BP, wp * TP, 1);
-        const int rdq0 = read_base(QR, BQ, wq * TQ, 0), rdq1 = QR ? rdq0 + BQ / 16 * PIECE : read_base(QR, BQ, wq * TQ, 1);
+        const int rdp0 = read_base(PR, RP, wp * TP, 0), rdp1 = PR ? rdp0 + RP / 16 * PIECE : read_base(PR, RP, wp * TP, 1);
+        const int rdq0 = read_base(QR, RQ, wq * TQ, 0), rdq1 = QR ? rdq0 + RQ / 16 * PIECE : read_base(QR, RQ, wq * TQ, 1);
         auto fragment = [&](const uint8_t* p, bool by_rows, int R, int i) -> s16x8 {
             if (by_rows) {
                 const s16x4 lo = read_tr(p + i * 32), hi = read_tr(p + i * 32 + R * 2);   // k + 0..3, k + 4..7
@@ -165,9 +198,9 @@ struct TileProduct {
         auto read_half = [&](const uint8_t* buf, int kk, int to) {
             const uint8_t *bp = buf + (kk ? rdp1 : rdp0), *bq = buf + P_BYTES + (kk ? rdq1 : rdq0);
 #pragma unroll
-            for (int i = 0; i < NI; ++i) fp[to][i] = fragment(bp, PR, BP, i);
+            for (int i = 0; i < NI; ++i) fp[to][i] = fragment(bp, PR, RP, i);
 #pragma unroll
-            for (int j = 0; j < NJ; ++j) fq[to][j] = fragment(bq, QR, BQ, j);
+            for (int j = 0; j < NJ; ++j) fq[to][j] = fragment(bq, QR, RQ, j);
         };
         auto multiply = [&](int from) {
 #pragma unroll
@@ -185,7 +218,7 @@ struct TileProduct {
             interleave<READS, MFMAS, 0>();
             wait_vm_loads<0>();   // step kt + 1 has landed
             barrier_lds();        // for every wavefront, and every one has read the last of step kt
-            stage(kt + 2, b0);
+            stage(w, s, kt + 2, b0);
             read_half(b1, 0, 0);
             multiply(1);
             interleave<READS, MFMAS, UP + UQ>();
@@ -194,15 +227,13 @@ struct TileProduct {
             interleave<READS, MFMAS, 0>();
             wait_vm_loads<0>();
             barrier_lds();
-            stage(kt + 3, b1);    // (past the last step: zeros)
+            stage(w, s, kt + 3, b1);    // (past the last step: zeros)
             read_half(b0, 0, 0);
             multiply(1);
             interleave<READS, MFMAS, UP + UQ>();
         };
         if (nk > 0) {
-            stage(0, smem);
-            stage(1, smem + STEP);
-            wait_vm_loads<UP + UQ>();
+            wait_vm_loads<AFTER ? 0 : UP + UQ>();
             barrier_lds();
             read_half(smem, 0, 0);
             int kt = 0;
@@ -219,6 +250,11 @@ struct TileProduct {
                 multiply(1);
             }
         }
+    }
+
+    static MOE_DEV void run(const Work& w, uint8_t* smem, f32x4 (&acc)[NI][NJ]) {
+        begin(w, smem);
+        sums<false>(w, smem, acc);
     }
 };
 
