@@ -12,6 +12,8 @@
 //
 // dz is rounded to 16 bits, as an operand of the matrix cores, and nothing else before the results: the
 // gradients have sqrt(2) of the error that their own rounding gives them. z is kept in f32.
+#include <cmath>
+
 #include "block_rows.h"
 #include "block_tiles.h"
 
@@ -44,6 +46,19 @@ MOE_DEV float act_of(float v) {
         z = 2.f * 0.7978845608028654f * (c + 0.044715f * c * c * c);
     }
     return v * __builtin_amdgcn_rcpf(1.0f + __expf(-z));
+}
+
+// act'(v), NaN where v is
+MOE_DEV float act_slope(float v, int act) {
+    if (act == MOE_ACT_SILU) {
+        const float s = __builtin_amdgcn_rcpf(1.0f + __expf(-v));
+        return s * (1.f + v * (1.f - s));
+    }
+    const float c = clamp_up(v, 100.f), k = 2.f * 0.7978845608028654f;   // (fminf and fmaxf would make a number of a NaN)
+    const float z = k * (c + 0.044715f * c * c * c);
+    // (1 + tanh) / 2 and (1 - tanh) / 2, neither as a difference
+    const float s = __builtin_amdgcn_rcpf(1.f + __expf(-z)), q = __builtin_amdgcn_rcpf(1.f + __expf(z));
+    return s + c * s * q * k * (1.f + 0.134145f * c * c);
 }
 
 // 64 offsets at a time, one per lane; what lies outside 0..m or goes back does not count
@@ -132,16 +147,18 @@ struct Tile {
     int q0, p0;
     int expert, row0;   // q (DW: k) counts from this row
 };
-template <Kind KIND, int BQ, int BP>
-MOE_DEV Tile locate(const LinArgs& a, int tile, int nq, int np) {
+// order: of DW with offsets, the experts with the most rows first
+template <Kind KIND, bool GROUPED, int BQ, int BP>
+MOE_DEV Tile locate(const LinArgs& a, int tile, int nq, int np, const uint16_t* order) {
     Tile t;
     t.expert = 0, t.row0 = 0;
     int rows = a.m;
-    if (a.offsets != nullptr) {
+    if (GROUPED) {
         if (KIND == DW) {
             const int each = nq * np;
             t.expert = tile / each;
             tile -= t.expert * each;
+            t.expert = __builtin_amdgcn_readfirstlane(order[t.expert]);
             t.row0 = offset_of(a, t.expert);
             rows = max(offset_of(a, t.expert + 1) - t.row0, 0);
         } else {
@@ -181,10 +198,7 @@ struct Slab {
 template <typename T, Kind KIND, int ACT, int TP, int NI, int NJ>
 MOE_DEV void finish(const LinArgs& a, const Tile& t, int qw, int pw, const f32x4 (&v)[NI][NJ], float* slab) {
     typedef Slab<TP> S;
-    // (opaque, so that what follows from it is not kept in registers while the next piece is multiplied)
-    int lane = threadIdx.x & 63;
-    asm volatile("" : "+v"(lane));
-    const int l16 = lane & 15, g = lane >> 4;
+    const int lane = lane_here(), l16 = lane & 15, g = lane >> 4;
     const int r = lane / S::LPR, c = lane % S::LPR * 8;
     const int rows = KIND == DW ? a.N : t.Q.rows, p = t.p0 + pw + c, left = (KIND == FWD ? a.N : a.K) - p;
     if (qw >= rows) return;
@@ -235,8 +249,21 @@ MOE_DEV void finish(const LinArgs& a, const Tile& t, int qw, int pw, const f32x4
         }
 }
 
-// The work of one launch: the first `whole` tiles, each in one piece, and the `rest` (what does not fill the
-// CUs once more) in `splits` pieces along k. With an expert's rows per tile `whole` is only a bound.
+// order[i]: the expert with the i-th most rows (equal ones in their order). counts: room for E of them
+MOE_DEV void sort_experts(const LinArgs& a, int threads, int* counts, uint16_t* order) {
+    for (int e = threadIdx.x; e < a.experts; e += threads) counts[e] = max(offset_at(a, e + 1) - offset_at(a, e), 0);
+    __syncthreads();
+    for (int e = threadIdx.x; e < a.experts; e += threads) {
+        const int mine = counts[e];
+        int before = 0;
+        for (int i = 0; i < a.experts; ++i) before += counts[i] > mine || (counts[i] == mine && i < e) ? 1 : 0;
+        order[before] = (uint16_t)e;
+    }
+    __syncthreads();
+}
+
+// The work of one product: the first `whole` tiles, each in one piece, and the `rest` in `splits` pieces along k.
+// With offsets nothing is split, and of a product of the tokens' rows `whole` is only a bound.
 struct Plan {
     int nq, np;          // tiles along q and p
     int whole, rest, splits;
@@ -246,45 +273,112 @@ struct Plan {
 template <typename T, Kind KIND, int BQ, int BP, int WQ, int WP>
 using LinTile = TileProduct<T, p_by_rows(KIND), q_by_rows(KIND), false, BQ, BP, WQ, WP>;
 
-// A workgroup takes one piece after another. The loads of the next piece's first two steps are under way while it
-// finishes the one before, and its stores while it multiplies the next.
-template <typename T, Kind KIND, int ACT, int BQ, int BP, int WQ, int WP>
-__global__ __launch_bounds__(64 * WQ * WP) void linear_kernel(LinArgs a, Plan plan) {
-    extern __shared__ __align__(16) uint8_t smem[];
-    typedef LinTile<T, KIND, BQ, BP, WQ, WP> Product;
-    constexpr int TH = Product::TH, NI = Product::NI, NJ = Product::NJ;
-    const int tid = threadIdx.x, wv = __builtin_amdgcn_readfirstlane(tid >> 6), wq = wv / WP, wp = wv % WP;
-    float* const slab = reinterpret_cast<float*>(smem + Product::LDS + wv * Slab<Product::TP>::BYTES);
+struct Piece {
+    Tile t;
+    int tile, split, kt0, nk;   // split < 0: a whole tile
+};
+// Pieces that an XCD has of a product: an eighth of the whole tiles, side by side, and of the others
+struct Share {
+    int w0, whole, s0, pieces;
+};
+MOE_DEV Share share_of(const Plan& plan, int whole, int xcd) {
+    const int64_t pieces = (int64_t)plan.rest * plan.splits;
+    Share s;
+    s.w0 = (int)((int64_t)whole * xcd >> 3), s.whole = (int)((int64_t)whole * (xcd + 1) >> 3) - s.w0;
+    s.s0 = (int)(pieces * xcd >> 3), s.pieces = (int)(pieces * (xcd + 1) >> 3) - s.s0;
+    return s;
+}
+MOE_DEV void piece_at(const Plan& plan, const Share& s, int place, Piece& x) {
+    x.split = -1;
+    if (place < s.whole) {
+        x.tile = s.w0 + place;
+    } else {
+        const int item = s.s0 + place - s.whole;
+        x.split = item / plan.rest;
+        x.tile = plan.whole + item - x.split * plan.rest;
+    }
+}
+template <Kind KIND, bool GROUPED, int BQ, int BP>
+MOE_DEV void open_piece(const LinArgs& a, const Plan& plan, const uint16_t* order, Piece& x) {
+    x.t = locate<KIND, GROUPED, BQ, BP>(a, x.tile, plan.nq, plan.np, order);
+    const int steps = (x.t.P.k + BK - 1) / BK;
+    x.kt0 = GROUPED || x.split < 0 ? 0 : (int)((int64_t)x.split * steps / plan.splits);
+    x.nk = (GROUPED || x.split < 0 ? steps : (int)((int64_t)(x.split + 1) * steps / plan.splits)) - x.kt0;
+}
+template <int TH, int NI, int NJ>
+MOE_DEV void store_sums(const Plan& plan, const Piece& x, const f32x4 (&acc)[NI][NJ]) {
+    f32x4* o = reinterpret_cast<f32x4*>(plan.partial) + (size_t)(x.split * plan.rest + x.tile - plan.whole) * NI * NJ * TH + threadIdx.x;
+#pragma unroll
+    for (int j = 0; j < NJ; ++j)
+#pragma unroll
+        for (int i = 0; i < NI; ++i) o[(j * NI + i) * TH] = acc[i][j];
+}
 
-    // An eighth of the tiles, side by side, and of the pieces for each XCD, whose workgroups take them in turn
-    const int whole = a.offsets != nullptr && KIND != DW ? tiles_total(a, BQ) * plan.np : plan.whole;
-    const int pieces = plan.rest * plan.splits, xcd = blockIdx.x & 7, step = gridDim.x >> 3;
-    const int w0 = xcd * ((whole + 7) >> 3), w1 = min(w0 + ((whole + 7) >> 3), whole);
-    const int s0 = xcd * ((pieces + 7) >> 3), s1 = min(s0 + ((pieces + 7) >> 3), pieces);
-    struct Piece {
-        Tile t;
-        int tile, split, kt0, nk;   // split < 0: a whole tile
-    };
-    int at = blockIdx.x >> 3;
-    auto take = [&](Piece& x) -> bool {
-        const int n = max(w1 - w0, 0);
-        if (at < n) {
-            x.tile = w0 + at, x.split = -1;
-        } else {
-            const int item = s0 + at - n;
-            if (item >= s1) return false;
-            x.split = item / plan.rest;
-            x.tile = plan.whole + item - x.split * plan.rest;
+// Both kernels: a workgroup takes one piece after another. The loads of the next piece's first two steps are under
+// way while it finishes the one before. The pointers into LDS are a lambda's own restricted ones there, so that the
+// compiler does not wait for these loads before it reads the slab. GROUPED: with offsets.
+template <typename T, bool GROUPED, int ACT, int BQ, int BP, int WQ, int WP>
+__global__ __launch_bounds__(64 * WQ * WP) void linear_forward_kernel(LinArgs a, Plan plan) {
+    extern __shared__ __align__(16) uint8_t smem[];
+    typedef LinTile<T, FWD, BQ, BP, WQ, WP> Product;
+    constexpr int NI = Product::NI, NJ = Product::NJ;
+    const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wq = wv / WP, wp = wv % WP;
+    float* const slab = reinterpret_cast<float*>(smem + Product::LDS + wv * Slab<Product::TP>::BYTES);
+    const Share mine = share_of(plan, GROUPED ? tiles_total(a, BQ) * plan.np : plan.whole, blockIdx.x & 7);
+    int place = blockIdx.x >> 3;
+    if (place >= mine.whole + mine.pieces) return;
+    Piece now;
+    piece_at(plan, mine, place, now);
+    open_piece<FWD, GROUPED, BQ, BP>(a, plan, nullptr, now);
+    Product::begin({now.t.P, now.t.Q, 1, now.t.q0, now.t.p0, now.kt0, now.nk}, smem);
+    for (;;) {
+        f32x4 acc[NI][NJ];
+        Product::template sums<true>({now.t.P, now.t.Q, 1, now.t.q0, now.t.p0, now.kt0, now.nk}, smem, acc);
+        Piece next;
+        place += gridDim.x >> 3;
+        const bool more = place < mine.whole + mine.pieces;
+        if (more) {
+            piece_at(plan, mine, place, next);
+            open_piece<FWD, GROUPED, BQ, BP>(a, plan, nullptr, next);
         }
-        at += step;
-        x.t = locate<KIND, BQ, BP>(a, x.tile, plan.nq, plan.np);
-        const int steps = (x.t.P.k + BK - 1) / BK;
-        x.kt0 = x.split < 0 ? 0 : (int)((int64_t)x.split * steps / plan.splits);
-        x.nk = (x.split < 0 ? steps : (int)((int64_t)(x.split + 1) * steps / plan.splits)) - x.kt0;
-        return true;
+        barrier_lds();   // every wavefront has read the last step
+        [&](uint8_t* __restrict buffers, float* __restrict own) {
+            if (more) Product::begin({next.t.P, next.t.Q, 1, next.t.q0, next.t.p0, next.kt0, next.nk}, buffers);
+            if (!GROUPED && now.split >= 0) store_sums<Product::TH>(plan, now, acc);
+            else finish<T, FWD, ACT, Product::TP, NI, NJ>(a, now.t, now.t.q0 + wq * Product::TQ, wp * Product::TP, acc, own);
+        }(smem, slab);
+        if (!more) return;
+        now = next;
+    }
+}
+
+// What a workgroup has of one product's pieces in the backward pass. The XCD's pieces, `count` of this product
+// after `base` of another, go to its workgroups forth and back; run: with offsets, dW's tiles side by side on an XCD.
+template <typename T, Kind KIND, bool GROUPED, int B, int WQ, int WP>
+MOE_DEV void run_pieces(const LinArgs& a, const Plan& plan, const Share& mine, int base, int count, int run, int& turn,
+                        const uint16_t* order, uint8_t* smem, float* slab) {
+    typedef LinTile<T, KIND, B, B, WQ, WP> Product;
+    constexpr int NI = Product::NI, NJ = Product::NJ;
+    const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wq = wv / WP, wp = wv % WP;
+    auto take = [&](Piece& x) -> bool {
+        const int step = gridDim.x >> 3, at = blockIdx.x >> 3, xcd = blockIdx.x & 7;
+        for (;;) {
+            const int place = turn * step + (turn & 1 ? step - 1 - at : at) - base;
+            if (place >= count) return false;
+            ++turn;
+            if (GROUPED && KIND == DW) {
+                x.tile = (place / run * 8 + xcd) * run + place % run, x.split = -1;
+                if (x.tile >= plan.whole) continue;
+            } else {
+                piece_at(plan, mine, place, x);
+            }
+            open_piece<KIND, GROUPED, B, B>(a, plan, order, x);
+            return true;
+        }
     };
     Piece now;
     if (!take(now)) return;
+    barrier_lds();   // (what was in the buffers is read)
     Product::begin({now.t.P, now.t.Q, 1, now.t.q0, now.t.p0, now.kt0, now.nk}, smem);
     for (;;) {
         f32x4 acc[NI][NJ];
@@ -292,23 +386,39 @@ __global__ __launch_bounds__(64 * WQ * WP) void linear_kernel(LinArgs a, Plan pl
         Piece next;
         const bool more = take(next);
         barrier_lds();   // every wavefront has read the last step
-        // (the pointers are the lambda's own restricted ones so that the compiler does not wait for the next
-        // piece's loads before it reads the slab)
-        [&](uint8_t* __restrict buffers, float* __restrict mine) {
+        [&](uint8_t* __restrict buffers, float* __restrict own) {
             if (more) Product::begin({next.t.P, next.t.Q, 1, next.t.q0, next.t.p0, next.kt0, next.nk}, buffers);
-            if (now.split >= 0) {
-                f32x4* o = reinterpret_cast<f32x4*>(plan.partial) + (size_t)(now.split * plan.rest + now.tile - plan.whole) * NI * NJ * TH + tid;
-#pragma unroll
-                for (int j = 0; j < NJ; ++j)
-#pragma unroll
-                    for (int i = 0; i < NI; ++i) o[(j * NI + i) * TH] = acc[i][j];
-            } else {
-                finish<T, KIND, ACT, Product::TP, NI, NJ>(a, now.t, now.t.q0 + wq * Product::TQ, wp * Product::TP, acc, mine);
-            }
+            if (!GROUPED && now.split >= 0) store_sums<Product::TH>(plan, now, acc);
+            else finish<T, KIND, MOE_ACT_NONE, Product::TP, NI, NJ>(a, now.t, now.t.q0 + wq * Product::TQ, wp * Product::TP, acc, own);
         }(smem, slab);
         if (!more) return;
         now = next;
     }
+}
+
+// dx and dW in one launch, so that the longer pieces of the one (W_FIRST: dW's) are filled up with the other's: neither
+// fills the CUs evenly by itself. With offsets dW's tiles have as many steps as their expert has rows: each XCD has an
+// eighth of each expert's, those with the most rows first (experts of 8 to 2000 rows, 506 on average: no workgroup has
+// more than a quarter above the mean, where an eighth of the experts for each XCD left one with twice the mean).
+template <typename T, bool GROUPED, bool W_FIRST, int B, int WQ, int WP>
+__global__ __launch_bounds__(64 * WQ * WP) void linear_backward_kernel(LinArgs a, Plan px, Plan pw) {
+    extern __shared__ __align__(16) uint8_t smem[];
+    typedef LinTile<T, DX, B, B, WQ, WP> ProductX;
+    typedef LinTile<T, DW, B, B, WQ, WP> ProductW;
+    constexpr size_t LDS = ProductX::LDS > ProductW::LDS ? ProductX::LDS : ProductW::LDS;
+    constexpr int SLAB = Slab<ProductX::TP>::BYTES;
+    const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), xcd = blockIdx.x & 7;
+    float* const slab = reinterpret_cast<float*>(smem + LDS + wv * SLAB);
+    uint16_t* const order = reinterpret_cast<uint16_t*>(smem + LDS + WQ * WP * SLAB);
+    if (GROUPED && pw.whole > 0) sort_experts(a, ProductX::TH, reinterpret_cast<int*>(smem), order);
+    const Share sx = share_of(px, GROUPED && px.whole > 0 ? tiles_total(a, B) * px.np : px.whole, xcd);
+    const Share sw = share_of(pw, pw.whole, xcd);
+    const int run = max((pw.nq * pw.np + 7) >> 3, 1);
+    const int nx = sx.whole + sx.pieces, nw = GROUPED ? (pw.whole + 8 * run - 1) / (8 * run) * run : sw.whole + sw.pieces;
+    int turn = 0;
+    if (W_FIRST) run_pieces<T, DW, GROUPED, B, WQ, WP>(a, pw, sw, 0, nw, run, turn, order, smem, slab);
+    run_pieces<T, DX, GROUPED, B, WQ, WP>(a, px, sx, W_FIRST ? nw : 0, nx, run, turn, order, smem, slab);
+    if (!W_FIRST) run_pieces<T, DW, GROUPED, B, WQ, WP>(a, pw, sw, nx, nw, run, turn, order, smem, slab);
 }
 
 // The split tiles' sums, added in order of k, and what is done with them: a workgroup per
@@ -330,16 +440,21 @@ __global__ __launch_bounds__(64 * WQ * WP) void linear_join_kernel(LinArgs a, Pl
 #pragma unroll
         for (int i = 0; i < NI; ++i) v[i][0] += f[i * TH];
     }
-    const Tile t = locate<KIND, BQ, BP>(a, plan.whole + r, plan.nq, plan.np);
+    const Tile t = locate<KIND, false, BQ, BP>(a, plan.whole + r, plan.nq, plan.np, nullptr);
     finish<T, KIND, ACT, Product::TP, NI, 1>(a, t, t.q0 + wq * Product::TQ + 16 * j, wp * Product::TP, v, slab[wv]);
 }
 
 // ------------------------------------------------------------------ dz and its column sums
 
-// A workgroup owns DZ_ROWS rows and 512 columns, eight per lane, a row per wavefront at a time. The rows may be
+// A workgroup owns a chunk of rows and 512 columns, eight per lane, a row per wavefront at a time. The rows may be
 // several experts': where one ends the sums of its columns go to the row (chunk + expert) of `partial`, a number of
 // its own for every expert in every chunk.
-constexpr int DZ_ROWS = 64, DZ_COLS = 512;
+constexpr int DZ_COLS = 512;
+// rows of a chunk: 16, or as many more as leave at least 512 chunks, up to 64 (1013 x 4101: 28.7 us with 64, 8
+// with 16)
+MOE_DEV __host__ int dz_rows(int m) { return m >= 512 * 64 ? 64 : m >= 512 * 32 ? 32 : 16; }
+// at most as many chunks have m rows or fewer
+int dz_chunks(int m) { return std::max({(m + 63) / 64, std::min((m + 15) / 16, 1024), std::min((m + 31) / 32, 1024)}); }
 
 // the number of experts whose rows end at `row` or before: the expert of that row
 MOE_DEV int expert_of(const LinArgs& a, int row) {
@@ -354,8 +469,9 @@ template <typename T, bool STORE>
 __global__ __launch_bounds__(256) void linear_dz_kernel(LinArgs a) {
     __shared__ float lds[4][DZ_COLS];
     const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
-    const int first = blockIdx.x * DZ_ROWS, n0 = blockIdx.y * DZ_COLS + lane * 8, left = a.N - n0;
-    const int last = min(first + DZ_ROWS, a.offsets != nullptr ? offset_of(a, a.experts) : a.m);
+    constexpr int U = 4;   // rows that a wavefront requests at a time
+    const int chunk = dz_rows(a.m), first = blockIdx.x * chunk, n0 = blockIdx.y * DZ_COLS + lane * 8, left = a.N - n0;
+    const int last = min(first + chunk, a.offsets != nullptr ? offset_of(a, a.experts) : a.m);
     int row = first;
     while (row < last) {
         const int e = a.offsets != nullptr ? expert_of(a, row) : 0;
@@ -364,23 +480,33 @@ __global__ __launch_bounds__(256) void linear_dz_kernel(LinArgs a) {
         float sum[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) sum[i] = 0.f;
-        for (int r = row + wv; r < end && left > 0; r += 4) {
-            float d[8];
-            unpack8<T>(load8(a.dy + r * a.lddy + n0, left), d);
-            if (a.act != MOE_ACT_NONE) {
-                const float* z = a.z + (size_t)r * padded(a.N) + n0;
-                const f32x4 z0 = *reinterpret_cast<const f32x4*>(z), z1 = *reinterpret_cast<const f32x4*>(z + 4);
+        for (int r0 = row + wv; r0 < end && left > 0; r0 += 4 * U) {
+            uint4 dy[U];
+            f32x4 z[U][2];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    float f, df;
-                    act_both(i < 4 ? z0[i] : z1[i - 4], a.act, f, df);
-                    d[i] = i < left ? d[i] * df : 0.f;
+            for (int u = 0; u < U; ++u) {
+                const int r = min(r0 + 4 * u, end - 1);
+                dy[u] = load8(a.dy + r * a.lddy + n0, left);
+                if (a.act != MOE_ACT_NONE) {
+                    const float* from = a.z + (size_t)r * padded(a.N) + n0;
+                    z[u][0] = *reinterpret_cast<const f32x4*>(from), z[u][1] = *reinterpret_cast<const f32x4*>(from + 4);
                 }
             }
 #pragma unroll
-            for (int i = 0; i < 8; ++i) sum[i] += d[i];
-            if (STORE)
-                *reinterpret_cast<uint4*>(a.dz_out + r * a.lddz + n0) = pack8<T>(d);
+            for (int u = 0; u < U; ++u) {
+                const int r = r0 + 4 * u;
+                float d[8];
+                unpack8<T>(dy[u], d);
+                if (a.act != MOE_ACT_NONE) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) d[i] = i < left ? d[i] * act_slope(z[u][i >> 2][i & 3], a.act) : 0.f;
+                }
+                if (r < end) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) sum[i] += d[i];
+                    if (STORE) *reinterpret_cast<uint4*>(a.dz_out + r * a.lddz + n0) = pack8<T>(d);
+                }
+            }
         }
         if (a.partial != nullptr) {
             *reinterpret_cast<f32x4*>(&lds[wv][lane * 8]) = (f32x4){sum[0], sum[1], sum[2], sum[3]};
@@ -403,8 +529,10 @@ __global__ __launch_bounds__(1024) void linear_bias_kernel(LinArgs a) {
     const int c = threadIdx.x & 63, g = threadIdx.x >> 6, e = blockIdx.y, n = blockIdx.x * 64 + c;
     const int r0 = a.offsets != nullptr ? offset_of(a, e) : 0, r1 = a.offsets != nullptr ? offset_of(a, e + 1) : a.m;
     float s = 0.f;
+    const int chunk = dz_rows(a.m);
     if (n < a.N && r1 > r0)
-        for (int b = r0 / DZ_ROWS + g; b <= (r1 - 1) / DZ_ROWS; b += 16) s += a.partial[(size_t)(b + e) * a.N + n];
+#pragma unroll 8
+        for (int b = r0 / chunk + g; b <= (r1 - 1) / chunk; b += 16) s += a.partial[(size_t)(b + e) * a.N + n];
     lds[g][c] = s;
     __syncthreads();
     if (g == 0 && n < a.N) {
@@ -497,90 +625,172 @@ __global__ __launch_bounds__(64 * FEW_WAVES) void linear_few_kernel(LinArgs a, i
 int cdiv(int a, int b) { return (a + b - 1) / b; }
 
 constexpr int N_CU = 256, MAX_SPLITS = 16;
-struct Product {
-    Plan plan;
-    int tile;         // 256 or 128
+
+// The tiles that there are: BQ x BP, of how many the CUs hold at a time (LDS), and what a K step of so many at once
+// takes, in us (forward; dx and dW, whose operands are transposed on their way from LDS), and the beginning and the
+// end of one. Few rows only where they are the tokens'.
+struct Shape {
+    int bq, bp, slots;
+    double step, back, ends;
 };
+constexpr Shape SHAPES[] = {{256, 256, N_CU, 1.5, 1.7, 8}, {128, 128, 2 * N_CU, 1.0, 1.1, 6}, {64, 128, 2 * N_CU, 0.65, 0, 5}, {32, 128, 3 * N_CU, 0.65, 0, 5}};
+constexpr int N_SHAPES = 4, BACK_SHAPES = 2;
+
 struct Extent {
-    int nq, np, tiles, steps, slots;
+    int nq, np, tiles, steps;
+    double likely;   // tiles that there will be
 };
-// tiles of B x B along q and p, all of them (with a matrix per expert: at most), K steps of one, and how many the
-// CUs hold at a time
-Extent extent(Kind kind, int m, int N, int K, int experts, int B) {
+// tiles along q and p, all of them (with offsets: at most), K steps of one
+Extent extent(Kind kind, int m, int N, int K, int experts, bool grouped, const Shape& s) {
     Extent e;
-    e.steps = cdiv(kind == FWD ? K : kind == DX ? N : m, BK);
-    e.nq = cdiv(kind == DW ? N : m, B), e.np = cdiv(kind == FWD ? N : K, B);
-    e.tiles = kind == DW ? experts * e.nq * e.np : experts == 1 ? e.nq * e.np : (m / B + std::min(experts, m)) * e.np;
-    e.slots = B == 256 ? N_CU : 2 * N_CU;
+    e.steps = cdiv(kind == FWD ? K : kind == DX ? N : grouped ? cdiv(m, experts) : m, BK);
+    e.nq = cdiv(kind == DW ? N : m, s.bq), e.np = cdiv(kind == FWD ? N : K, s.bp);
+    e.tiles = kind == DW ? experts * e.nq * e.np : grouped ? (m / s.bq + std::min(experts, m)) * e.np : e.nq * e.np;
+    e.likely = grouped && kind != DW ? std::min((double)e.tiles, (m / (double)s.bq + 0.5 * std::min(experts, m)) * e.np) : e.tiles;
     return e;
 }
-// Bytes that hold the split tiles' sums of any plan for m rows or fewer
+// Bytes that hold the split tiles' sums of any plan for m rows or fewer: the pieces are at most the
+// slots, and at most the tiles times the splits
 size_t partial_bytes(Kind kind, int m, int N, int K, int experts) {
     if (experts > 1) return 0;
     size_t most = 0;
-    for (int B : {256, 128}) {
-        const Extent e = extent(kind, m, N, K, 1, B);
+    for (int i = 0; i < (kind == FWD ? N_SHAPES : BACK_SHAPES); ++i) {
+        const Shape& s = SHAPES[i];
+        const Extent e = extent(kind, m, N, K, 1, false, s);
         const int splits = std::min(MAX_SPLITS, e.steps / 2);
-        if (splits >= 2) most = std::max(most, (size_t)std::min<int64_t>(e.slots, (int64_t)e.tiles * splits) * B * B * sizeof(float));
+        if (splits >= 2) most = std::max(most, (size_t)std::min<int64_t>(s.slots, (int64_t)e.tiles * splits) * s.bq * s.bp * sizeof(float));
     }
-    return most;
+    return round_up(most, 256);
 }
+// what the sums of n pieces cost: they pass through memory twice, at 5 TB/s, and their join is a launch
+double join_cost(const Shape& s, int pieces) { return 6 + 2.0 * s.bq * s.bp * 4 / 5e6 * pieces; }
 
-// How a product is cut up: 256 x 256 or 128 x 128 tiles, and by how much the tiles past the last full
-// round of the CUs are split along k. Costs in units of one K step of a 256 x 256 tile on a CU
-// (about 1.65 us): a 128 x 128 tile's step takes 0.33 of it (a quarter of the products, at three quarters
-// of the rate); the split tiles' sums pass through memory twice (0.06 a 256 x 256 tile and split, and 4 for
-// the second launch). With a matrix per expert nothing is split.
-Product plan_product(Kind kind, int m, int N, int K, int experts) {
-    Product best{};
+// How a forward pass is cut up: which tiles, and by how much those past the last full round of the CUs are split along
+// k. With offsets nothing is split.
+Plan plan_forward(int m, int N, int K, int experts, bool grouped, int* shape) {
+    Plan best{};
     double best_cost = 1e300;
-    for (int B : {256, 128}) {
-        const Extent e = extent(kind, m, N, K, experts, B);
-        Product p{};
-        p.tile = B;
-        p.plan.nq = e.nq, p.plan.np = e.np;
-        const double step = B == 256 ? 1 : 0.66, share = B == 256 ? 0.06 : 0.015;   // (two workgroups share a CU)
-        p.plan.whole = e.tiles, p.plan.splits = 1;
-        double cost;
-        if (experts > 1) {
-            const int steps = kind == DW ? cdiv(cdiv(m, experts), BK) : e.steps;
-            cost = cdiv(e.tiles, e.slots) * (double)steps * step;
-        } else {
-            const int rounds = e.tiles / e.slots, rest = e.tiles % e.slots;
-            cost = rounds * (double)e.steps * step;
-            if (rest > 0) {
-                double tail = e.steps * step;
-                for (int s = 2; s <= MAX_SPLITS && s * 2 <= e.steps && rest * s <= e.slots; ++s) {
-                    const double t = cdiv(e.steps, s) * step + 4 + share * rest * s;
-                    if (t < tail) tail = t, p.plan.whole = e.tiles - rest, p.plan.rest = rest, p.plan.splits = s;
-                }
-                cost += tail;
+    for (int i = 0; i < N_SHAPES; ++i) {
+        const Shape& s = SHAPES[i];
+        const Extent e = extent(FWD, m, N, K, experts, grouped, s);
+        Plan p{e.nq, e.np, e.tiles, 0, 1, nullptr};
+        const double tile = e.steps * s.step + s.ends;
+        double cost = std::max(1.0, std::ceil(e.likely / s.slots)) * tile;
+        const int rest = e.tiles % s.slots;
+        if (!grouped && rest > 0) {
+            const double full = e.tiles / s.slots * tile;
+            for (int n = 2; n <= MAX_SPLITS && n * 2 <= e.steps && rest * n <= s.slots; ++n) {
+                const double c = full + cdiv(e.steps, n) * s.step + s.ends + join_cost(s, rest * n);
+                if (c < cost) cost = c, p.whole = e.tiles - rest, p.rest = rest, p.splits = n;
             }
         }
-        if (cost < best_cost) best_cost = cost, best = p;
+        if (cost < best_cost) best_cost = cost, best = p, *shape = i;
     }
     return best;
 }
 
-template <typename T, Kind KIND, int ACT, int B, int WQ, int WP>
-hipError_t launch_tiles(const LinArgs& a, const Plan& plan, hipStream_t st) {
-    typedef LinTile<T, KIND, B, B, WQ, WP> P;
-    constexpr int SLOTS = B == 256 ? N_CU : 2 * N_CU;
-    const int64_t work = plan.whole + (int64_t)plan.rest * plan.splits;
-    if (work == 0) return hipSuccess;
-    const int grid = (int)std::min<int64_t>(SLOTS, (work + 7) / 8 * 8);
-    const hipError_t e = launch_kernel(linear_kernel<T, KIND, ACT, B, B, WQ, WP>, dim3(grid), dim3(P::TH),
-                                       P::LDS + WQ * WP * Slab<P::TP>::BYTES, st, a, plan);
-    if (e != hipSuccess || plan.rest == 0) return e;
-    return launch_kernel(linear_join_kernel<T, KIND, ACT, B, B, WQ, WP>, dim3(plan.rest * P::NJ), dim3(P::TH), 0, st, a, plan);
+// How dx and dW (where wanted) are: one kind of tiles for both, and in how many pieces along k those of either. With
+// both, what they take together, and two fifths of the shorter piece for its end; with one, whole rounds.
+struct BackPlan {
+    Plan x, w;
+    int shape;
+    bool w_first;
+};
+BackPlan plan_backward(int m, int N, int K, int experts, bool grouped, bool want_x, bool want_w) {
+    BackPlan best{};
+    double best_cost = 1e300;
+    for (int i = 0; i < BACK_SHAPES; ++i) {
+        const Shape& s = SHAPES[i];
+        Extent e[2];
+        Plan p[2]{};
+        for (int k = 0; k < 2; ++k) {
+            e[k] = extent(k == 0 ? DX : DW, m, N, K, experts, grouped, s);
+            if (k == 0 ? want_x : want_w) p[k] = {e[k].nq, e[k].np, e[k].tiles, 0, 1, nullptr};
+            else e[k].tiles = 0, e[k].likely = 0;
+        }
+        auto splits_of = [&](int k, int n) { return n == 1 || (!grouped && e[k].tiles > 0 && n * 2 <= e[k].steps && (int64_t)e[k].tiles * n <= s.slots); };
+        for (int nx = 1; nx <= MAX_SPLITS; ++nx) {
+            if (!splits_of(0, nx)) continue;
+            for (int nw = 1; nw <= MAX_SPLITS; ++nw) {
+                if (!splits_of(1, nw)) continue;
+                const int n[2] = {nx, nw};
+                double piece[2], total = 0, joins = 0;
+                for (int k = 0; k < 2; ++k) {
+                    piece[k] = cdiv(e[k].steps, n[k]) * s.back + s.ends;
+                    total += e[k].likely * n[k] * piece[k] / s.slots;
+                    if (n[k] > 1) joins += join_cost(s, e[k].tiles * n[k]);
+                }
+                double cost;
+                if (want_x && want_w) {
+                    cost = std::max({total + 0.4 * std::min(piece[0], piece[1]), piece[0], piece[1]});
+                } else {
+                    const int k = want_x ? 0 : 1;
+                    cost = std::max(1.0, std::ceil(e[k].likely * n[k] / s.slots)) * piece[k];
+                }
+                cost += joins;
+                if (cost >= best_cost) continue;
+                best_cost = cost;
+                best.shape = i, best.w_first = piece[1] >= piece[0];
+                best.x = p[0], best.w = p[1];
+                for (int k = 0; k < 2; ++k)
+                    if (n[k] > 1) {
+                        Plan& q = k == 0 ? best.x : best.w;
+                        q.rest = q.whole, q.whole = 0, q.splits = n[k];
+                    }
+            }
+        }
+    }
+    return best;
 }
 
-template <typename T, Kind KIND, int ACT>
-hipError_t launch_product(const LinArgs& a, float* partial, hipStream_t st) {
-    Product p = plan_product(KIND, a.m, a.N, a.K, a.offsets != nullptr ? std::max(a.experts, 2) : 1);
-    if (a.offsets != nullptr && a.experts == 1 && KIND == DW) p = plan_product(KIND, a.m, a.N, a.K, 1);
-    p.plan.partial = partial;
-    return p.tile == 256 ? launch_tiles<T, KIND, ACT, 256, 2, 4>(a, p.plan, st) : launch_tiles<T, KIND, ACT, 128, 2, 2>(a, p.plan, st);
+template <typename T, Kind KIND, int ACT, int I, int WQ, int WP>
+hipError_t launch_join(const LinArgs& a, const Plan& plan, hipStream_t st) {
+    constexpr Shape S = SHAPES[I];
+    typedef LinTile<T, KIND, S.bq, S.bp, WQ, WP> P;
+    if (plan.rest == 0) return hipSuccess;
+    return launch_kernel(linear_join_kernel<T, KIND, ACT, S.bq, S.bp, WQ, WP>, dim3(plan.rest * P::NJ), dim3(P::TH), 0, st, a, plan);
+}
+int grid_of(int64_t pieces, int slots) { return (int)std::min<int64_t>(slots, (pieces + 7) / 8 * 8); }
+int64_t pieces_of(const Plan& p) { return p.whole + (int64_t)p.rest * p.splits; }
+
+template <typename T, int ACT, int I, int WQ, int WP>
+hipError_t launch_forward_tiles(const LinArgs& a, const Plan& plan, hipStream_t st) {
+    constexpr Shape S = SHAPES[I];
+    typedef LinTile<T, FWD, S.bq, S.bp, WQ, WP> P;
+    auto* const k = a.offsets != nullptr ? linear_forward_kernel<T, true, ACT, S.bq, S.bp, WQ, WP> : linear_forward_kernel<T, false, ACT, S.bq, S.bp, WQ, WP>;
+    const hipError_t e = launch_kernel(k, dim3(grid_of(pieces_of(plan), S.slots)), dim3(P::TH), P::LDS + WQ * WP * Slab<P::TP>::BYTES, st, a, plan);
+    return e != hipSuccess ? e : launch_join<T, FWD, ACT, I, WQ, WP>(a, plan, st);
+}
+template <typename T, int ACT>
+hipError_t launch_forward(const LinArgs& a, float* partial, hipStream_t st) {
+    int shape = 0;
+    Plan p = plan_forward(a.m, a.N, a.K, a.experts, a.offsets != nullptr, &shape);
+    p.partial = partial;
+    switch (shape) {
+        case 0: return launch_forward_tiles<T, ACT, 0, 2, 4>(a, p, st);
+        case 1: return launch_forward_tiles<T, ACT, 1, 2, 2>(a, p, st);
+        case 2: return launch_forward_tiles<T, ACT, 2, 1, 4>(a, p, st);
+        default: return launch_forward_tiles<T, ACT, 3, 1, 4>(a, p, st);
+    }
+}
+
+template <typename T, int I, int WQ, int WP>
+hipError_t launch_backward_tiles(const LinArgs& a, const BackPlan& b, hipStream_t st) {
+    constexpr Shape S = SHAPES[I];
+    typedef LinTile<T, DX, S.bq, S.bp, WQ, WP> X;
+    typedef LinTile<T, DW, S.bq, S.bp, WQ, WP> W;
+    const size_t lds = std::max(X::LDS, W::LDS) + WQ * WP * Slab<X::TP>::BYTES + (a.offsets != nullptr ? (size_t)a.experts * 2 : 0);
+    auto* const k = a.offsets != nullptr ? linear_backward_kernel<T, true, true, S.bq, WQ, WP>
+                    : b.w_first ? linear_backward_kernel<T, false, true, S.bq, WQ, WP> : linear_backward_kernel<T, false, false, S.bq, WQ, WP>;
+    hipError_t e = launch_kernel(k, dim3(grid_of(pieces_of(b.x) + pieces_of(b.w), S.slots)), dim3(X::TH), lds, st, a, b.x, b.w);
+    if (e == hipSuccess) e = launch_join<T, DX, MOE_ACT_NONE, I, WQ, WP>(a, b.x, st);
+    return e != hipSuccess ? e : launch_join<T, DW, MOE_ACT_NONE, I, WQ, WP>(a, b.w, st);
+}
+template <typename T>
+hipError_t launch_backward(const LinArgs& a, float* partial_x, float* partial_w, hipStream_t st) {
+    BackPlan b = plan_backward(a.m, a.N, a.K, a.experts, a.offsets != nullptr, a.dx != nullptr && a.m > 0, a.dw != nullptr);
+    b.x.partial = partial_x, b.w.partial = partial_w;
+    return b.shape == 0 ? launch_backward_tiles<T, 0, 2, 4>(a, b, st) : launch_backward_tiles<T, 1, 2, 2>(a, b, st);
 }
 
 constexpr int MAX_M = 1 << 24, MAX_N = 1 << 17, MAX_K = 1 << 16, MAX_EXPERTS = 1024;
@@ -598,18 +808,17 @@ bool rows_ok(const void* p, int64_t ld, int dim) {
     return p != nullptr && aligned_to(p, 16) && ld >= dim && ld % 8 == 0 && ld <= (1 << 22);
 }
 
-size_t forward_bytes(const moe_linear* f, int m) { return round_up(partial_bytes(FWD, m, f->rows, f->cols, f->experts), 256); }
+size_t forward_bytes(const moe_linear* f, int m) { return partial_bytes(FWD, m, f->rows, f->cols, f->experts); }
 size_t saved_bytes_of(const moe_linear* f, int m) {
     return f->act == MOE_ACT_NONE ? 0 : round_up((size_t)m * padded(f->rows) * 4, 256);
 }
 size_t dz_bytes(const moe_linear* f, int m) { return round_up((size_t)m * padded(f->rows) * 2, 256); }
 size_t sums_bytes(const moe_linear* f, int m) {
-    return f->bias == nullptr ? 0 : round_up((size_t)(cdiv(m, DZ_ROWS) + f->experts) * f->rows * 4, 256);
+    return f->bias == nullptr ? 0 : round_up((size_t)(dz_chunks(m) + f->experts) * f->rows * 4, 256);
 }
-size_t product_bytes(const moe_linear* f, int m) {
-    return round_up(std::max(partial_bytes(DX, m, f->rows, f->cols, f->experts), partial_bytes(DW, m, f->rows, f->cols, f->experts)), 256);
-}
-size_t backward_bytes(const moe_linear* f, int m) { return dz_bytes(f, m) + std::max(sums_bytes(f, m), product_bytes(f, m)); }
+size_t dx_bytes(const moe_linear* f, int m) { return partial_bytes(DX, m, f->rows, f->cols, f->experts); }
+size_t dw_bytes(const moe_linear* f, int m) { return partial_bytes(DW, m, f->rows, f->cols, f->experts); }
+size_t backward_bytes(const moe_linear* f, int m) { return dz_bytes(f, m) + std::max(sums_bytes(f, m), dx_bytes(f, m) + dw_bytes(f, m)); }
 
 LinArgs describe(const moe_linear* f, int m, const int32_t* offsets) {
     LinArgs a{};
@@ -623,7 +832,7 @@ LinArgs describe(const moe_linear* f, int m, const int32_t* offsets) {
 template <typename T, int ACT>
 hipError_t forward_act(const LinArgs& a, float* partial, hipStream_t st) {
     const int each = cdiv(a.m, a.experts);   // rows of an expert, on average
-    if (each > FEW_ROWS) return launch_product<T, FWD, ACT>(a, partial, st);
+    if (each > FEW_ROWS) return launch_forward<T, ACT>(a, partial, st);
     const int room = std::min(a.m, FEW_ROWS), items = a.offsets != nullptr ? a.m / room + std::min(a.experts, a.m) : cdiv(a.m, room);
     const size_t lds = std::max<size_t>((size_t)room * few_pass(room, a.K) * 2, sizeof(float) * FEW_WAVES * 256);
     return launch_kernel(linear_few_kernel<T, ACT>, dim3(cdiv(a.N, 16), items), dim3(64 * FEW_WAVES), lds, st, a, room);
@@ -636,13 +845,13 @@ hipError_t forward(const LinArgs& a, float* partial, hipStream_t st) {
 }
 
 template <typename T>
-hipError_t backward(LinArgs a, uint8_t* work, size_t work_dz, bool direct, hipStream_t st) {
+hipError_t backward(LinArgs a, uint8_t* work, size_t work_dz, size_t work_dx, bool direct, hipStream_t st) {
     hipError_t e = hipSuccess;
     float* const partial = reinterpret_cast<float*>(work + work_dz);
     if (a.m > 0 && (!direct || a.dbias != nullptr)) {
         LinArgs d = a;
         if (a.dbias != nullptr) d.partial = partial;
-        e = launch_kernel(direct ? linear_dz_kernel<T, false> : linear_dz_kernel<T, true>, dim3(cdiv(a.m, DZ_ROWS), cdiv(a.N, DZ_COLS)),
+        e = launch_kernel(direct ? linear_dz_kernel<T, false> : linear_dz_kernel<T, true>, dim3(cdiv(a.m, dz_rows(a.m)), cdiv(a.N, DZ_COLS)),
                           dim3(256), 0, st, d);
     }
     if (e == hipSuccess && a.dbias != nullptr) {
@@ -650,8 +859,8 @@ hipError_t backward(LinArgs a, uint8_t* work, size_t work_dz, bool direct, hipSt
         d.partial = partial;
         e = launch_kernel(linear_bias_kernel<T>, dim3(cdiv(a.N, 64), a.experts), dim3(1024), 0, st, d);
     }
-    if (e == hipSuccess && a.dx != nullptr && a.m > 0) e = launch_product<T, DX, MOE_ACT_NONE>(a, partial, st);
-    if (e == hipSuccess && a.dw != nullptr) e = launch_product<T, DW, MOE_ACT_NONE>(a, partial, st);
+    if (e == hipSuccess && ((a.dx != nullptr && a.m > 0) || a.dw != nullptr))
+        e = launch_backward<T>(a, partial, reinterpret_cast<float*>(work + work_dz + work_dx), st);
     return e;
 }
 
@@ -722,8 +931,8 @@ int moe_linear_backward(const moe_linear* f, const void* x, int64_t ldx, const i
     a.dbias = reinterpret_cast<uint16_t*>(dbias);
     uint8_t* const w = reinterpret_cast<uint8_t*>(work);
     const hipStream_t st = (hipStream_t)stream;
-    const size_t work_dz = m > 0 ? dz_bytes(f, m) : 0;
-    return status_of(f->dtype == MOE_BF16 ? backward<Bf16>(a, w, work_dz, direct, st) : backward<F16>(a, w, work_dz, direct, st));
+    const size_t work_dz = m > 0 ? dz_bytes(f, m) : 0, work_dx = m > 0 ? dx_bytes(f, m) : 0;
+    return status_of(f->dtype == MOE_BF16 ? backward<Bf16>(a, w, work_dz, work_dx, direct, st) : backward<F16>(a, w, work_dz, work_dx, direct, st));
 }
 
 }  // extern "C"

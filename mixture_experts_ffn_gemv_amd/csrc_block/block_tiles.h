@@ -67,20 +67,26 @@ MOE_DEV void interleave() {
     }
 }
 
+// The lane, opaque to the compiler: what follows from it is worked out where it is used, and not kept in registers
+// over another tile's products
+MOE_DEV int lane_here() {
+    int lane = threadIdx.x & 63;
+    asm volatile("" : "+v"(lane));
+    return lane;
+}
+
 // A BQ x BP tile of the output by WQ x WP wavefronts: acc[i][j] of a lane holds p = 16 i + 4 (lane / 16) +
 // 0..3 and q = 16 j + lane % 16 of its wavefront's part. PR, QR: p or q (not k) is the operand's
 // consecutive index. PAIRED: of every 64 p, the first 32 are P's first matrix, the others the second.
 template <typename T, bool PR, bool QR, bool PAIRED, int BQ, int BP, int WQ, int WP>
 struct TileProduct {
     static constexpr int TH = 64 * WQ * WP, TQ = BQ / WQ, TP = BP / WP, NI = TP / 16, NJ = TQ / 16;
-    // a tile of 64 k x rows has room for 128 or 256 rows
-    static constexpr int RP = PR && BP > 128 ? 256 : BP, RQ = BQ;
-    static constexpr int UP = RP * 8 / TH, UQ = RQ * 8 / TH, NW = TH / 64;   // 16-byte units per thread
-    static constexpr int P_BYTES = tile_bytes(RP, PR), STEP = P_BYTES + tile_bytes(RQ, QR);
+    static constexpr int UP = BP * 8 / TH, UQ = BQ * 8 / TH, NW = TH / 64;   // 16-byte units per thread
+    static constexpr int P_BYTES = tile_bytes(BP, PR), STEP = P_BYTES + tile_bytes(BQ, QR);
     static constexpr int PSPAN = PAIRED ? BP / 2 : BP;
     static constexpr size_t LDS = 2 * STEP;
     static_assert(NW == 8 || NW == 4, "");
-    static_assert((!PR || RP == 128 || RP == 256) && (!QR || RQ == 128 || RQ == 256) && (!PAIRED || RP == BP), "");
+    static_assert((!PR || BP == 128 || BP == 256) && (!QR || BQ == 128 || BQ == 256), "");
 
     // A product's tile and its K steps kt0 .. kt0 + nk - 1; segs matrices one after another along k
     struct Work {
@@ -91,21 +97,20 @@ struct TileProduct {
     // This thread's first unit of each tile: its byte offset from the tile's corner; unit u is
     // unit_rows(u) rows further. A K-contiguous tile's units of a thread share their chunk of k.
     struct Units {
-        uint32_t off_p, off_q, none_p;   // none_p: all ones where a lane has none of P's rows
+        uint32_t off_p, off_q;
         int chunk;
     };
     static MOE_DEV Units units(const Work& w) {
-        const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-        const int slot_p = PR ? lane / (RP / 8) : 0, slot_q = QR ? lane / (RQ / 8) : 0;
+        const int lane = lane_here(), wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+        const int slot_p = PR ? lane / (BP / 8) : 0, slot_q = QR ? lane / (BQ / 8) : 0;
         const int row_k = wv * 8 + (lane >> 3), chunk = (lane & 7) ^ swz_k(row_k);
         const int first = PAIRED ? (row_k & 31) : row_k;
         Units s;
         s.chunk = chunk;
-        s.off_p = PR ? (uint32_t)(run_row_wave(RP, NW, wv, slot_p) * w.P.ld + lane % (RP / 8) * 8) * 2
+        s.off_p = PR ? (uint32_t)(run_row_wave(BP, NW, wv, slot_p) * w.P.ld + lane % (BP / 8) * 8) * 2
                      : (uint32_t)(first * w.P.ld + chunk * 8) * 2;
-        s.off_q = QR ? (uint32_t)(run_row_wave(RQ, NW, wv, slot_q) * w.Q.ld + lane % (RQ / 8) * 8) * 2
+        s.off_q = QR ? (uint32_t)(run_row_wave(BQ, NW, wv, slot_q) * w.Q.ld + lane % (BQ / 8) * 8) * 2
                      : (uint32_t)(row_k * w.Q.ld + chunk * 8) * 2;
-        s.none_p = PR && RP > BP && lane % (RP / 8) * 8 >= BP ? PAST : 0u;
         return s;
     }
 
@@ -117,7 +122,7 @@ struct TileProduct {
         kt += w.kt0;
         const int seg = w.segs == 2 && kt >= seg_steps ? 1 : 0;
         const int k0 = (kt - seg * seg_steps) * BK;
-        auto side = [&](uint32_t off, const Operand& o, bool by_rows, int R, int at, int span, bool paired, int U, uint32_t none, uint8_t* dst) {
+        auto side = [&](uint32_t off, const Operand& o, bool by_rows, int R, int at, int span, bool paired, int U, uint8_t* dst) {
             const uint16_t* base = seg ? o.b : o.a;
             const int left = min(o.rows - at, span), kleft = min(BK, o.k - k0);
             const uint32_t beyond = s.chunk * 8 >= kleft ? PAST : 0u;   // a K tail's missing chunks
@@ -127,7 +132,7 @@ struct TileProduct {
                 if (PR && QR) asm volatile("" : "+v"(off));
 #pragma unroll
                 for (int u = 0; u < U; ++u)
-                    buffer_load_lds16(buffer, dst + (u * NW + wv) * PIECE, (off + (uint32_t)(run_row_unit(R, NW, u) * o.ld * 2)) | none);
+                    buffer_load_lds16(buffer, dst + (u * NW + wv) * PIECE, off + (uint32_t)(run_row_unit(R, NW, u) * o.ld * 2));
             } else {
                 const uint32_t bytes = past ? 0u : (uint32_t)((left - 1) * o.ld + kleft) * 2;
                 const size_t corner = (size_t)at * o.ld + k0;
@@ -146,8 +151,8 @@ struct TileProduct {
                 }
             }
         };
-        side(s.off_p, w.P, PR, RP, w.p0, PSPAN, PAIRED, UP, s.none_p, buf);
-        side(s.off_q, w.Q, QR, RQ, w.q0, BQ, false, UQ, 0u, buf + P_BYTES);
+        side(s.off_p, w.P, PR, BP, w.p0, PSPAN, PAIRED, UP, buf);
+        side(s.off_q, w.Q, QR, BQ, w.q0, BQ, false, UQ, buf + P_BYTES);
     }
 
     // requests the first two steps, into buffers that nobody reads any more
@@ -162,7 +167,7 @@ struct TileProduct {
     // wavefront has read all that it will of the buffers.
     template <bool AFTER>
     static MOE_DEV void sums(const Work& w, uint8_t* smem, f32x4 (&acc)[NI][NJ]) {
-        const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+        const int lane = lane_here(), wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
         const int l16 = lane & 15, g = lane >> 4, wq = wv / WP, wp = wv % WP;
         const int nk = w.nk;
         const Units s = units(w);
@@ -175,8 +180,8 @@ struct TileProduct {
             }
             return (base + l16) * (BK * 2) + (((g + 4 * kk) ^ swz_k(l16)) << 4);
         };
-        const int rdp0 = read_base(PR, RP, wp * TP, 0), rdp1 = PR ? rdp0 + RP / 16 * PIECE : read_base(PR, RP, wp * TP, 1);
-        const int rdq0 = read_base(QR, RQ, wq * TQ, 0), rdq1 = QR ? rdq0 + RQ / 16 * PIECE : read_base(QR, RQ, wq * TQ, 1);
+        const int rdp0 = read_base(PR, BP, wp * TP, 0), rdp1 = PR ? rdp0 + BP / 16 * PIECE : read_base(PR, BP, wp * TP, 1);
+        const int rdq0 = read_base(QR, BQ, wq * TQ, 0), rdq1 = QR ? rdq0 + BQ / 16 * PIECE : read_base(QR, BQ, wq * TQ, 1);
         auto fragment = [&](const uint8_t* p, bool by_rows, int R, int i) -> s16x8 {
             if (by_rows) {
                 const s16x4 lo = read_tr(p + i * 32), hi = read_tr(p + i * 32 + R * 2);   // k + 0..3, k + 4..7
@@ -198,9 +203,9 @@ struct TileProduct {
         auto read_half = [&](const uint8_t* buf, int kk, int to) {
             const uint8_t *bp = buf + (kk ? rdp1 : rdp0), *bq = buf + P_BYTES + (kk ? rdq1 : rdq0);
 #pragma unroll
-            for (int i = 0; i < NI; ++i) fp[to][i] = fragment(bp, PR, RP, i);
+            for (int i = 0; i < NI; ++i) fp[to][i] = fragment(bp, PR, BP, i);
 #pragma unroll
-            for (int j = 0; j < NJ; ++j) fq[to][j] = fragment(bq, QR, RQ, j);
+            for (int j = 0; j < NJ; ++j) fq[to][j] = fragment(bq, QR, BQ, j);
         };
         auto multiply = [&](int from) {
 #pragma unroll
