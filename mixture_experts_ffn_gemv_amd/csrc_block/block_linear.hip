@@ -788,9 +788,17 @@ hipError_t launch_backward_tiles(const LinArgs& a, const BackPlan& b, hipStream_
 }
 template <typename T>
 hipError_t launch_backward(const LinArgs& a, float* partial_x, float* partial_w, hipStream_t st) {
-    BackPlan b = plan_backward(a.m, a.N, a.K, a.experts, a.offsets != nullptr, a.dx != nullptr && a.m > 0, a.dw != nullptr);
-    b.x.partial = partial_x, b.w.partial = partial_w;
-    return b.shape == 0 ? launch_backward_tiles<T, 0, 2, 4>(a, b, st) : launch_backward_tiles<T, 1, 2, 2>(a, b, st);
+    const bool grouped = a.offsets != nullptr, want_x = a.dx != nullptr && a.m > 0, want_w = a.dw != nullptr;
+    auto launch = [&](bool x, bool w) {
+        BackPlan b = plan_backward(a.m, a.N, a.K, a.experts, grouped, x, w);
+        b.x.partial = partial_x, b.w.partial = partial_w;
+        return b.shape == 0 ? launch_backward_tiles<T, 0, 2, 4>(a, b, st) : launch_backward_tiles<T, 1, 2, 2>(a, b, st);
+    };
+    if (!grouped || !want_x || !want_w) return launch(want_x, want_w);
+    // with offsets each by itself: tiles of dx that run side by side share an expert's weights in their XCD's L2, and
+    // pieces of dW between them part them (16184 rows of 32 experts, 2048 x 1408: 142 and 155 us, together 309)
+    const hipError_t e = launch(true, false);
+    return e != hipSuccess ? e : launch(false, true);
 }
 
 constexpr int MAX_M = 1 << 24, MAX_N = 1 << 17, MAX_K = 1 << 16, MAX_EXPERTS = 1024;
