@@ -583,13 +583,24 @@ def moe_w4_gated(w_gate, w_up, x, h, act="silu", limit=0.0, stream=None):
                                      _stream(stream)), me)
 
 
-def _matrix(t, rows, dim, dtype, where):
-    """A device matrix whose type and width the call takes from it -> (rows, dim, dtype); rows, dim: as given, or any."""
-    if t is None or t.dim() != 2 or (rows is not None and t.shape[0] != rows) or (dim is not None and t.shape[1] != dim):
+def _any_rows(t, dtype, where):
+    """A device matrix of that type with consecutive values in each row -> (pointer, row stride, rows, values of a row)."""
+    shape = t.shape
+    if t.dtype is not dtype or len(shape) != 2 or not t.is_cuda:
         raise MoeError(MOE_EINVAL, where)
-    if dtype is not None and t.dtype is not dtype:
+    m, dim = shape
+    ld, one = t.stride()
+    if one != 1 and dim != 1:
         raise MoeError(MOE_EINVAL, where)
-    return t.shape[0], t.shape[1], t.dtype
+    return t.data_ptr(), ld if m > 1 else dim, m, dim   # (one row: its stride leads nowhere)
+
+
+def _picks(t, where):
+    """A contiguous int32 device matrix [m, topk] -> (pointer, m, topk)."""
+    shape = t.shape
+    if t.dtype is not torch.int32 or len(shape) != 2 or not t.is_cuda or not t.is_contiguous():
+        raise MoeError(MOE_EINVAL, where)
+    return t.data_ptr(), shape[0], shape[1]
 
 
 def moe_sort_workspace(m, topk, n_experts):
@@ -603,56 +614,54 @@ def moe_sort(idx, n_experts, row_of, pick_of, offsets, work, stream=None):
     """The order by expert of the picks idx int32 [m, topk]: row_of [m, topk], pick_of [m * topk] (or None) and
     offsets [n_experts + 1], all int32."""
     me = "moe_sort"
-    m, topk, _ = _matrix(idx, None, None, torch.int32, me)
+    picks, m, topk = _picks(idx, me)
     return _check(lib().moe_sort(
-        _whole(idx, (m, topk), torch.int32, me), m, topk, n_experts, _whole(row_of, (m, topk), torch.int32, me),
-        _whole(pick_of, (m * topk,), torch.int32, me), _whole(offsets, (n_experts + 1,), torch.int32, me), *_bytes(work, me),
-        _stream(stream)), me)
+        picks, m, topk, n_experts, _whole(row_of, (m, topk), torch.int32, me), _whole(pick_of, (m * topk,), torch.int32, me),
+        _whole(offsets, (n_experts + 1,), torch.int32, me), *_bytes(work, me), _stream(stream)), me)
+
+
+def _moved(tokens, sorted_rows, row_of, where):
+    """Token rows [m, dim], sorted rows [rows, dim] and row_of [m, topk] of one call -> their pointers and sizes."""
+    at, m, topk = _picks(row_of, where)
+    dt = tokens.dtype
+    if dt not in _DTYPES:
+        raise MoeError(MOE_EINVAL, where)
+    t, ldt, n, dim = _any_rows(tokens, dt, where)
+    s, lds, rows, width = _any_rows(sorted_rows, dt, where)
+    if n != m or width != dim:
+        raise MoeError(MOE_EINVAL, where)
+    return _DTYPES[dt], dim, t, ldt, s, lds, rows, at, m, topk
 
 
 def moe_dispatch_forward(x, row_of, xs, stream=None):
     """xs[row_of[t, j]] = x[t]: x [m, dim], row_of [m, topk], xs [rows, dim]."""
     me = "moe_dispatch_forward"
-    m, topk, _ = _matrix(row_of, None, None, torch.int32, me)
-    _, dim, dt = _matrix(x, m, None, None, me)
-    rows = _matrix(xs, None, dim, dt, me)[0]
-    return _check(lib().moe_dispatch_forward(_dtype(dt, me), dim, *_rows(x, m, dim, dt, me), _whole(row_of, (m, topk), torch.int32, me),
-                                             m, topk, *_rows(xs, rows, dim, dt, me), rows, _stream(stream)), me)
+    dt, dim, x_, ldx, xs_, ldxs, rows, at, m, topk = _moved(x, xs, row_of, me)
+    return _check(lib().moe_dispatch_forward(dt, dim, x_, ldx, at, m, topk, xs_, ldxs, rows, _stream(stream)), me)
 
 
 def moe_dispatch_backward(dxs, row_of, dx, stream=None):
     """dx[t] = sum over j of dxs[row_of[t, j]]."""
     me = "moe_dispatch_backward"
-    m, topk, _ = _matrix(row_of, None, None, torch.int32, me)
-    _, dim, dt = _matrix(dx, m, None, None, me)
-    rows = _matrix(dxs, None, dim, dt, me)[0]
-    return _check(lib().moe_dispatch_backward(_dtype(dt, me), dim, *_rows(dxs, rows, dim, dt, me), rows,
-                                              _whole(row_of, (m, topk), torch.int32, me), m, topk, *_rows(dx, m, dim, dt, me),
-                                              _stream(stream)), me)
+    dt, dim, dx_, lddx, dxs_, lddxs, rows, at, m, topk = _moved(dx, dxs, row_of, me)
+    return _check(lib().moe_dispatch_backward(dt, dim, dxs_, lddxs, rows, at, m, topk, dx_, lddx, _stream(stream)), me)
 
 
 def moe_combine_forward(e, weights, row_of, y, stream=None):
     """y[t] = sum over j of weights[t, j] e[row_of[t, j]]: e [rows, dim], weights f32 [m, topk], y [m, dim]."""
     me = "moe_combine_forward"
-    m, topk, _ = _matrix(row_of, None, None, torch.int32, me)
-    _, dim, dt = _matrix(y, m, None, None, me)
-    rows = _matrix(e, None, dim, dt, me)[0]
-    return _check(lib().moe_combine_forward(_dtype(dt, me), dim, *_rows(e, rows, dim, dt, me), rows,
-                                            _whole(weights, (m, topk), torch.float32, me),
-                                            _whole(row_of, (m, topk), torch.int32, me), m, topk, *_rows(y, m, dim, dt, me),
+    dt, dim, y_, ldy, e_, lde, rows, at, m, topk = _moved(y, e, row_of, me)
+    return _check(lib().moe_combine_forward(dt, dim, e_, lde, rows, _whole(weights, (m, topk), torch.float32, me), at, m, topk, y_, ldy,
                                             _stream(stream)), me)
 
 
 def moe_combine_backward(dy, e, weights, row_of, de=None, dweights=None, stream=None):
     """Gradients of moe_combine_forward into the tensors that are given."""
     me = "moe_combine_backward"
-    m, topk, _ = _matrix(row_of, None, None, torch.int32, me)
-    _, dim, dt = _matrix(dy, m, None, None, me)
-    rows = _matrix(e, None, dim, dt, me)[0]
+    dt, dim, dy_, lddy, e_, lde, rows, at, m, topk = _moved(dy, e, row_of, me)
     return _check(lib().moe_combine_backward(
-        _dtype(dt, me), dim, *_rows(dy, m, dim, dt, me), *_rows(e, rows, dim, dt, me), rows,
-        _whole(weights, (m, topk), torch.float32, me), _whole(row_of, (m, topk), torch.int32, me), m, topk,
-        *_rows(de, rows, dim, dt, me), _whole(dweights, (m, topk), torch.float32, me), _stream(stream)), me)
+        dt, dim, dy_, lddy, e_, lde, rows, _whole(weights, (m, topk), torch.float32, me), at, m, topk, *_rows(de, rows, dim, dy.dtype, me),
+        _whole(dweights, (m, topk), torch.float32, me), _stream(stream)), me)
 
 
 _LINEAR_ACTS = {**_ACTS, "none": MOE_ACT_NONE, None: MOE_ACT_NONE}

@@ -42,53 +42,43 @@ MOE_DEV uint4 philox(uint32_t c, uint32_t row, uint64_t use, uint64_t seed) {
 }
 
 // A thread takes eight columns of a row at a time, `N` chunks of 16 bytes
-template <typename T, Tail TAIL, bool RESIDUAL>
+template <typename T, Tail TAIL, bool RESIDUAL, bool ONCE>
 __global__ __launch_bounds__(256) void dropout_kernel(DropArgs a) {
-    constexpr int V = Raw<T>::V, N = 8 / V, U = 2;
+    constexpr int V = Raw<T>::V, N = 8 / V;
     const uint64_t seed = a.rng[0], use = a.rng[1];
-    Place p[U];
-    p[0] = first_place(a.walk);
-    for (; p[0].row < a.m; p[0] = p[U - 1].next(a.walk)) {
-        Raw<T> x[U][N], r[U][N];
-        int col[U][N], skip[U][N];
+    for (Place p = first_place(a.walk); p.row < a.m; p = p.next(a.walk)) {
+        Raw<T> x[N], r[N];
+        int col[N], skip[N];
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            if (u > 0) p[u] = p[u - 1].next(a.walk);
-            const int64_t row = min(p[u].row, (int64_t)a.m - 1);
+        for (int n = 0; n < N; ++n) {
+            place_chunk<TAIL>(p.chunk * N + n, V, a.dim, col[n], skip[n]);
+            x[n].template load_of<TAIL, ONCE>(a.x, p.row * a.ldx, col[n], a.dim);
+            if (RESIDUAL) r[n].template load_of<TAIL, ONCE>(a.residual, p.row * a.ldr, col[n], a.dim);
+        }
+        const uint4 bits = philox((uint32_t)p.chunk, (uint32_t)p.row, use, seed);
+        const uint32_t w[4] = {bits.x, bits.y, bits.z, bits.w};
+        bool keep[8];
 #pragma unroll
-            for (int n = 0; n < N; ++n) {
-                place_chunk<TAIL>(p[u].chunk * N + n, V, a.dim, col[u][n], skip[u][n]);
-                x[u][n].template load<TAIL>(a.x, row * a.ldx, col[u][n], a.dim);
-                if (RESIDUAL) r[u][n].template load<TAIL>(a.residual, row * a.ldr, col[u][n], a.dim);
-            }
+        for (int i = 0; i < 4; ++i) keep[2 * i] = (w[i] & 0xFFFF) >= a.threshold, keep[2 * i + 1] = (w[i] >> 16) >= a.threshold;
+        uint32_t mask = 0;
+        if (TAIL != WHOLE) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) mask |= (keep[i] ? 1u : 0u) << i;
         }
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const uint4 bits = philox((uint32_t)p[u].chunk, (uint32_t)p[u].row, use, seed);
-            const uint32_t w[4] = {bits.x, bits.y, bits.z, bits.w};
-            bool keep[8];
+        for (int n = 0; n < N; ++n) {
+            float v[V], res[V];
+            x[n].template get<WHOLE>(v, 0);
+            if (RESIDUAL) r[n].template get<WHOLE>(res, 0);
+            // (a chunk that begins before its columns: theirs are its last)
+            const uint32_t mine = (mask >> (n * V)) << skip[n];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) keep[2 * i] = (w[i] & 0xFFFF) >= a.threshold, keep[2 * i + 1] = (w[i] >> 16) >= a.threshold;
-            uint32_t mask = 0;
-            if (TAIL != WHOLE) {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) mask |= (keep[i] ? 1u : 0u) << i;
+            for (int i = 0; i < V; ++i) {
+                const bool k = TAIL == WHOLE ? keep[n * V + i] : (mine >> i & 1) != 0;
+                const float d = k ? v[i] * a.scale : 0.f;   // (what is dropped may be infinite or NaN)
+                v[i] = RESIDUAL ? res[i] + d : d;
             }
-#pragma unroll
-            for (int n = 0; n < N; ++n) {
-                float v[V], res[V];
-                x[u][n].template get<WHOLE>(v, 0);
-                if (RESIDUAL) r[u][n].template get<WHOLE>(res, 0);
-                // (a chunk that begins before its columns: theirs are its last)
-                const uint32_t mine = (mask >> (n * V)) << skip[u][n];
-#pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    const bool k = TAIL == WHOLE ? keep[n * V + i] : (mine >> i & 1) != 0;
-                    const float d = k ? v[i] * a.scale : 0.f;   // (what is dropped may be infinite or NaN)
-                    v[i] = RESIDUAL ? res[i] + d : d;
-                }
-                if (p[u].row < a.m) store_chunk<T, TAIL>(a.y, p[u].row * a.ldy, col[u][n], a.dim, skip[u][n], a.past_l2, v);
-            }
+            store_chunk<T, TAIL>(a.y, p.row * a.ldy, col[n], a.dim, skip[n], a.past_l2, v);
         }
     }
 }
@@ -99,15 +89,20 @@ int check_dropout(const moe_dropout* f) {
     return f->p >= 0.0 && f->p <= 1.0 ? MOE_OK : MOE_EINVAL;
 }
 
-template <typename T, bool RESIDUAL>
-hipError_t launch_dropout(DropArgs a, hipStream_t st) {
+template <typename T, bool RESIDUAL, bool ONCE>
+hipError_t launch_dropout_of(DropArgs a, hipStream_t st) {
     const int per_row = (a.dim + 7) / 8;
-    const int64_t blocks = std::min<int64_t>(((int64_t)per_row * a.m + 255) / 256, 256 * 8);   // as many as are resident
+    const int64_t blocks = walk_blocks((int64_t)per_row * a.m, ONCE);
     a.walk = walk(per_row, blocks * 256);
     const Tail tail = tail_of(a.dim, Raw<T>::V);
-    auto* const k = tail == SHORT ? dropout_kernel<T, SHORT, RESIDUAL>
-                    : tail == WHOLE ? dropout_kernel<T, WHOLE, RESIDUAL> : dropout_kernel<T, SHIFTED, RESIDUAL>;
+    auto* const k = tail == SHORT ? dropout_kernel<T, SHORT, RESIDUAL, false>
+                    : tail == WHOLE ? dropout_kernel<T, WHOLE, RESIDUAL, ONCE> : dropout_kernel<T, SHIFTED, RESIDUAL, ONCE>;
     return launch_kernel(k, dim3((unsigned)blocks), dim3(256), 0, st, a);
+}
+template <typename T, bool RESIDUAL>
+hipError_t launch_dropout(const DropArgs& a, hipStream_t st) {
+    return past_caches((size_t)a.m * a.dim * sizeof(typename T::bits) * (RESIDUAL ? 3 : 2)) ? launch_dropout_of<T, RESIDUAL, true>(a, st)
+                                                                                          : launch_dropout_of<T, RESIDUAL, false>(a, st);
 }
 
 int dropout(const moe_dropout* f, const uint64_t* rng, const void* x, int64_t ldx, const void* residual, int64_t ldr, int32_t m,

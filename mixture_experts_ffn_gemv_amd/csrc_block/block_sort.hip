@@ -188,7 +188,7 @@ __global__ __launch_bounds__(256) void dispatch_kernel(MoveArgs a) {
 }
 
 // out[t] = sum over j of w[t, j] e[row_of[t, j]] (WEIGHTED; else w = 1), `J` rows requested at a time
-template <typename T, Tail TAIL, bool WEIGHTED, int J>
+template <typename T, Tail TAIL, bool WEIGHTED, bool ONCE, int J>
 __global__ __launch_bounds__(256) void combine_kernel(MoveArgs a) {
     constexpr int V = Raw<T>::V;
     for (Place p = first_place(a.walk); p.row < a.m; p = p.next(a.walk)) {
@@ -207,7 +207,7 @@ __global__ __launch_bounds__(256) void combine_kernel(MoveArgs a) {
                 const int row = j0 + j < a.topk ? row_at(a, p.row, j0 + j) : -1;
                 there[j] = row >= 0;
                 w[j] = WEIGHTED && there[j] ? a.weights[p.row * a.topk + j0 + j] : 1.f;
-                e[j].template load<TAIL>(a.e, max(row, 0) * a.lde, col, a.dim);
+                e[j].template load_of<TAIL, ONCE>(a.e, max(row, 0) * a.lde, col, a.dim);
             }
 #pragma unroll
             for (int j = 0; j < J; ++j) {
@@ -296,9 +296,9 @@ int check_move(int32_t dtype, int32_t dim, int32_t m, int32_t topk, int32_t rows
 bool past_l2(int64_t rows, int dim, size_t size) { return (size_t)rows * dim * size > (32u << 20); }
 
 template <typename K>
-hipError_t launch_walk(K* k, MoveArgs a, int v, hipStream_t st) {
+hipError_t launch_walk(K* k, MoveArgs a, int v, bool past, hipStream_t st) {
     const int per_row = (a.dim + v - 1) / v;
-    const int64_t blocks = std::min<int64_t>(((int64_t)per_row * a.m + 255) / 256, 256 * 8);
+    const int64_t blocks = walk_blocks((int64_t)per_row * a.m, past);
     a.walk = walk(per_row, blocks * 256);
     return launch_kernel(k, dim3((unsigned)blocks), dim3(256), 0, st, a);
 }
@@ -308,28 +308,29 @@ hipError_t launch_dispatch(const MoveArgs& a, hipStream_t st) {
     constexpr int V = Raw<T>::V;
     const Tail tail = tail_of(a.dim, V);
     return launch_walk(tail == SHORT ? dispatch_kernel<T, SHORT> : tail == WHOLE ? dispatch_kernel<T, WHOLE> : dispatch_kernel<T, SHIFTED>,
-                       a, V, st);
+                       a, V, a.past_l2, st);
 }
 
-template <typename T, bool WEIGHTED, int J>
+template <typename T, bool WEIGHTED, bool ONCE, int J>
 hipError_t launch_combine_j(const MoveArgs& a, hipStream_t st) {
     constexpr int V = Raw<T>::V;
     const Tail tail = tail_of(a.dim, V);
-    return launch_walk(tail == SHORT ? combine_kernel<T, SHORT, WEIGHTED, J>
-                       : tail == WHOLE ? combine_kernel<T, WHOLE, WEIGHTED, J> : combine_kernel<T, SHIFTED, WEIGHTED, J>, a, V, st);
+    return launch_walk(tail == SHORT ? combine_kernel<T, SHORT, WEIGHTED, false, J>
+                       : tail == WHOLE ? combine_kernel<T, WHOLE, WEIGHTED, ONCE, J> : combine_kernel<T, SHIFTED, WEIGHTED, ONCE, J>, a, V, ONCE, st);
 }
-template <typename T, bool WEIGHTED>
+template <typename T, bool WEIGHTED, bool ONCE>
 hipError_t launch_combine_t(const MoveArgs& a, hipStream_t st) {
-    if (a.topk == 1) return launch_combine_j<T, WEIGHTED, 1>(a, st);
-    if (a.topk == 2) return launch_combine_j<T, WEIGHTED, 2>(a, st);
-    if (a.topk <= 4) return launch_combine_j<T, WEIGHTED, 4>(a, st);
-    if (a.topk <= 6) return launch_combine_j<T, WEIGHTED, 6>(a, st);
-    return launch_combine_j<T, WEIGHTED, 8>(a, st);
+    if (a.topk == 1) return launch_combine_j<T, WEIGHTED, ONCE, 1>(a, st);
+    if (a.topk == 2) return launch_combine_j<T, WEIGHTED, ONCE, 2>(a, st);
+    if (a.topk <= 4) return launch_combine_j<T, WEIGHTED, ONCE, 4>(a, st);
+    if (a.topk <= 6) return launch_combine_j<T, WEIGHTED, ONCE, 6>(a, st);
+    return launch_combine_j<T, WEIGHTED, ONCE, 8>(a, st);
 }
-template <bool WEIGHTED>
-hipError_t launch_combine_of(int dtype, const MoveArgs& a, hipStream_t st) {
-    return dtype == MOE_BF16 ? launch_combine_t<Bf16, WEIGHTED>(a, st)
-           : dtype == MOE_F16 ? launch_combine_t<F16, WEIGHTED>(a, st) : launch_combine_t<F32, WEIGHTED>(a, st);
+template <typename T>
+hipError_t launch_combine_of(const MoveArgs& a, hipStream_t st) {
+    const bool once = past_caches((std::min((size_t)a.m * a.topk, (size_t)a.rows) + a.m) * a.dim * sizeof(typename T::bits));
+    if (a.weights != nullptr) return once ? launch_combine_t<T, true, true>(a, st) : launch_combine_t<T, true, false>(a, st);
+    return once ? launch_combine_t<T, false, true>(a, st) : launch_combine_t<T, false, false>(a, st);
 }
 
 template <typename T, int J>
@@ -339,7 +340,7 @@ hipError_t launch_backward_j(const MoveArgs& a, hipStream_t st) {
     const int chunks = (a.dim + V - 1) / V;
     int tpr = 1;
     while (tpr < 64 && tpr < chunks) tpr *= 2;
-    const bool wide = chunks > 128 && a.m < 8192;
+    const bool wide = chunks > 128;   // (8192 x 5120 bf16, six picks: 219 us, a wavefront per token 223)
     const int per = wide ? 1 : 256 / tpr;
     auto pick = [&](auto* narrow, auto* whole) { return wide ? whole : narrow; };
     auto* const k = tail == SHORT ? combine_backward_kernel<T, SHORT, false, J>
@@ -368,7 +369,7 @@ int sum_rows(int32_t dtype, int32_t dim, const void* e, int64_t lde, int32_t row
     a.e = rows > 0 ? e : out, a.lde = rows > 0 ? lde : 0, a.out = out, a.ldo = ldo, a.weights = weights, a.row_of = row_of;
     a.dim = dim, a.m = m, a.topk = topk, a.rows = rows, a.past_l2 = past_l2(m, dim, size);
     const hipStream_t st = (hipStream_t)stream;
-    return status_of(weights != nullptr ? launch_combine_of<true>(dtype, a, st) : launch_combine_of<false>(dtype, a, st));
+    return status_of(dtype == MOE_BF16 ? launch_combine_of<Bf16>(a, st) : dtype == MOE_F16 ? launch_combine_of<F16>(a, st) : launch_combine_of<F32>(a, st));
 }
 
 }  // namespace
