@@ -76,29 +76,41 @@ struct Slice {
 MOE_DEV int tiles_total(const LinArgs& a, int rows) {
     const int lane = threadIdx.x & 63;
     int n = 0;
+#pragma unroll 4
     for (int e = lane; e < a.experts; e += 64) n += (max(offset_at(a, e + 1) - offset_at(a, e), 0) + rows - 1) / rows;
     n = wave_inclusive_scan(n);
     return __builtin_amdgcn_readlane(n, 63);
 }
-MOE_DEV Slice find_slice(const LinArgs& a, int rows, int np, int tile) {
+// false: there are not so many
+MOE_DEV bool find_slice(const LinArgs& a, int rows, int np, int tile, Slice& s) {
     const int lane = threadIdx.x & 63;
-    Slice s{0, 0, 0, 0};
-    int before = 0;   // tiles of the experts before these 64
-    for (int e0 = 0; e0 < a.experts; e0 += 64) {
-        const int lo = offset_at(a, e0 + lane), cnt = e0 + lane < a.experts ? max(offset_at(a, e0 + lane + 1) - lo, 0) : 0;
-        const int n = (cnt + rows - 1) / rows * np, upto = before + wave_inclusive_scan(n);
-        const uint64_t past = __ballot(upto > tile);
-        if (past != 0) {
-            const int l = __builtin_ctzll(past);
-            s.expert = e0 + l;
-            s.row0 = __builtin_amdgcn_readlane(lo, l);
-            s.rows = __builtin_amdgcn_readlane(cnt, l);
-            s.tile = tile - (__builtin_amdgcn_readlane(upto, l) - __builtin_amdgcn_readlane(n, l));
-            break;
+    constexpr int U = 4;   // 256 experts' offsets are requested at a time
+    s = {0, 0, 0, 0};
+    int before = 0;   // tiles of the experts before these
+    for (int e0 = 0; e0 < a.experts; e0 += 64 * U) {
+        int lo[U], cnt[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int e = e0 + 64 * u + lane;
+            lo[u] = offset_at(a, e);
+            cnt[u] = e < a.experts ? max(offset_at(a, e + 1) - lo[u], 0) : 0;
         }
-        before = __builtin_amdgcn_readlane(upto, 63);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int n = (cnt[u] + rows - 1) / rows * np, upto = before + wave_inclusive_scan(n);
+            const uint64_t past = __ballot(upto > tile);
+            if (past != 0) {
+                const int l = __builtin_ctzll(past);
+                s.expert = e0 + 64 * u + l;
+                s.row0 = __builtin_amdgcn_readlane(lo[u], l);
+                s.rows = __builtin_amdgcn_readlane(cnt[u], l);
+                s.tile = tile - (__builtin_amdgcn_readlane(upto, l) - __builtin_amdgcn_readlane(n, l));
+                return true;
+            }
+            before = __builtin_amdgcn_readlane(upto, 63);
+        }
     }
-    return s;
+    return false;
 }
 
 // eight consecutive 16-bit values of a row, of which `left` > 0 are there; no alignment but a value's
@@ -162,7 +174,8 @@ MOE_DEV Tile locate(const LinArgs& a, int tile, int nq, int np, const uint16_t* 
             t.row0 = offset_of(a, t.expert);
             rows = max(offset_of(a, t.expert + 1) - t.row0, 0);
         } else {
-            const Slice s = find_slice(a, BQ, np, tile);
+            Slice s;
+            find_slice(a, BQ, np, tile, s);
             t.expert = s.expert, t.row0 = s.row0, rows = s.rows, tile = s.tile;
             nq = (rows + BQ - 1) / BQ;
         }
@@ -195,6 +208,23 @@ struct Slab {
     static constexpr int LPR = TP / 8, ROWS = 64 / LPR >= 16 ? 16 : 8, STRIDE = TP + 4;   // lanes per row
     static constexpr int BYTES = ROWS * STRIDE * 4;
 };
+// eight values (KIND FWD: sums, with the bias and the residual as they lie) on their way to memory
+template <typename T, int ACT>
+MOE_DEV void put_forward(const LinArgs& a, int64_t row, int p, int left, float (&o)[8], const uint4& bias, const uint4& residual) {
+    float b[8], res[8];
+    unpack8<T>(bias, b);
+    unpack8<T>(residual, res);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) o[i] += b[i];
+    if (ACT != MOE_ACT_NONE && a.z != nullptr) {
+        float* z = a.z + row * padded(a.N) + p;
+        *reinterpret_cast<f32x4*>(z) = (f32x4){o[0], o[1], o[2], o[3]};
+        *reinterpret_cast<f32x4*>(z + 4) = (f32x4){o[4], o[5], o[6], o[7]};
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) o[i] = act_of<ACT>(o[i]) + res[i];
+    store8(a.y + row * a.ldy + p, left, pack8<T>(o));
+}
 template <typename T, Kind KIND, int ACT, int TP, int NI, int NJ>
 MOE_DEV void finish(const LinArgs& a, const Tile& t, int qw, int pw, const f32x4 (&v)[NI][NJ], float* slab) {
     typedef Slab<TP> S;
@@ -203,13 +233,10 @@ MOE_DEV void finish(const LinArgs& a, const Tile& t, int qw, int pw, const f32x4
     const int rows = KIND == DW ? a.N : t.Q.rows, p = t.p0 + pw + c, left = (KIND == FWD ? a.N : a.K) - p;
     if (qw >= rows) return;
     const bool mine = lane < S::ROWS * S::LPR && left > 0;
-    float b[8];
-    if (KIND == FWD) {
-        const uint4 q = a.bias != nullptr && mine ? load8(a.bias + (size_t)t.expert * a.N + p, left) : make_uint4(0, 0, 0, 0);
-        unpack8<T>(q, b);
-    }
-    auto residual = [&](int q) { return a.residual != nullptr && mine && q < rows ? load8(a.residual + (t.row0 + q) * a.ldr + p, left) : make_uint4(0, 0, 0, 0); };
-    uint4 next = KIND == FWD ? residual(qw + r) : make_uint4(0, 0, 0, 0);
+    const uint4 none = make_uint4(0, 0, 0, 0);
+    const uint4 bias = KIND == FWD && a.bias != nullptr && mine ? load8(a.bias + (size_t)t.expert * a.N + p, left) : none;
+    auto residual = [&](int q) { return a.residual != nullptr && mine && q < rows ? load8(a.residual + (t.row0 + q) * a.ldr + p, left) : none; };
+    uint4 next = KIND == FWD ? residual(qw + r) : none;
 #pragma unroll
     for (int j = 0; j < NJ; ++j)
 #pragma unroll
@@ -228,20 +255,7 @@ MOE_DEV void finish(const LinArgs& a, const Tile& t, int qw, int pw, const f32x4
             if constexpr (KIND == FWD) {
                 const uint4 here = next;
                 next = residual(q + S::ROWS);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) o[i] += b[i];
-                if (mine && q < rows) {
-                    if (ACT != MOE_ACT_NONE && a.z != nullptr) {
-                        float* z = a.z + row * padded(a.N) + p;
-                        *reinterpret_cast<f32x4*>(z) = (f32x4){o[0], o[1], o[2], o[3]};
-                        *reinterpret_cast<f32x4*>(z + 4) = (f32x4){o[4], o[5], o[6], o[7]};
-                    }
-                    float res[8];
-                    unpack8<T>(here, res);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) o[i] = act_of<ACT>(o[i]) + res[i];
-                    store8(a.y + row * a.ldy + p, left, pack8<T>(o));
-                }
+                if (mine && q < rows) put_forward<T, ACT>(a, row, p, left, o, bias, here);
             } else if (mine && q < rows) {   // (K is a multiple of 8)
                 uint16_t* const to = KIND == DX ? a.dx + row * a.lddx : a.dw + ((size_t)t.expert * a.N + q) * a.K;
                 *reinterpret_cast<uint4*>(to + p) = pack8<T>(o);
@@ -564,8 +578,7 @@ __global__ __launch_bounds__(64 * FEW_WAVES) void linear_few_kernel(LinArgs a, i
     const int n0 = blockIdx.x * 16, pass_k = few_pass(room, a.K), row_bytes = pass_k * 2, runs = row_bytes / 1024;
     Slice s{0, 0, a.m, 0};
     if (a.offsets != nullptr) {
-        if ((int)blockIdx.y >= tiles_total(a, room)) return;
-        s = find_slice(a, room, 1, blockIdx.y);
+        if (!find_slice(a, room, 1, blockIdx.y, s)) return;
     } else {
         s.tile = blockIdx.y;
     }
@@ -575,6 +588,12 @@ __global__ __launch_bounds__(64 * FEW_WAVES) void linear_few_kernel(LinArgs a, i
     const auto X = buffer_rsrc(a.x + row0 * a.ldx, (uint32_t)((rows - 1) * a.ldx + a.K) * 2);
     const int xt = min(l16, rows - 1);   // (a token that does not exist reads another's; its sums are not used)
     f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+    // the first wavefront finishes: eight values of row lane / 2 a lane. What it adds is requested before the weights
+    const int er = lane >> 1, ep = n0 + (lane & 1) * 8, left = a.N - ep;
+    const bool ends = wv == 0 && er < rows && left > 0;
+    uint4 bias = make_uint4(0, 0, 0, 0), residual = bias;
+    if (ends && a.bias != nullptr) bias = load8(a.bias + (size_t)s.expert * a.N + ep, left);
+    if (ends && a.residual != nullptr) residual = load8(a.residual + (row0 + er) * a.ldr + ep, left);
     for (int k0 = 0; k0 < a.K; k0 += pass_k) {
         const int chunks = (min(pass_k, a.K - k0) + 31) / 32;
         const int c0 = wv * chunks / FEW_WAVES, c1 = (wv + 1) * chunks / FEW_WAVES;
@@ -611,13 +630,18 @@ __global__ __launch_bounds__(64 * FEW_WAVES) void linear_few_kernel(LinArgs a, i
     float* red = reinterpret_cast<float*>(smem);
     *reinterpret_cast<f32x4*>(&red[wv * 256 + lane * 4]) = acc;
     __syncthreads();
-    if (tid >= 64) return;
-    f32x4 v[1][1] = {{{0.f, 0.f, 0.f, 0.f}}};
+    if (!ends) return;
+    // weight row 4 g + r of token l16 lies at 64 g + 4 l16 + r of a wavefront's sums
+    float o[8];
 #pragma unroll
-    for (int i = 0; i < FEW_WAVES; ++i) v[0][0] += *reinterpret_cast<const f32x4*>(&red[i * 256 + lane * 4]);
-    Tile t;
-    t.expert = s.expert, t.row0 = row0, t.p0 = n0, t.Q.rows = rows;
-    finish<T, FWD, ACT, 16, 1, 1>(a, t, 0, 0, v, red);   // (one wavefront, which has read what was there)
+    for (int h = 0; h < 2; ++h) {
+        f32x4 v = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < FEW_WAVES; ++i) v += *reinterpret_cast<const f32x4*>(&red[i * 256 + (2 * (lane & 1) + h) * 64 + er * 4]);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) o[4 * h + r] = v[r];
+    }
+    put_forward<T, ACT>(a, row0 + er, ep, left, o, bias, residual);
 }
 
 // ------------------------------------------------------------------ plans
@@ -841,7 +865,9 @@ template <typename T, int ACT>
 hipError_t forward_act(const LinArgs& a, float* partial, hipStream_t st) {
     const int each = cdiv(a.m, a.experts);   // rows of an expert, on average
     if (each > FEW_ROWS) return launch_forward<T, ACT>(a, partial, st);
-    const int room = std::min(a.m, FEW_ROWS), items = a.offsets != nullptr ? a.m / room + std::min(a.experts, a.m) : cdiv(a.m, room);
+    // LDS room for as many rows, or with offsets twice the average (more of one expert read its weights again, from the
+    // L2): a token's six experts of 384 31.9 us with room for all six rows, 29.2 with room for two
+    const int room = std::min(a.m, a.offsets != nullptr ? std::min(2 * each, FEW_ROWS) : FEW_ROWS), items = a.offsets != nullptr ? a.m / room + std::min(a.experts, a.m) : cdiv(a.m, room);
     const size_t lds = std::max<size_t>((size_t)room * few_pass(room, a.K) * 2, sizeof(float) * FEW_WAVES * 256);
     return launch_kernel(linear_few_kernel<T, ACT>, dim3(cdiv(a.N, 16), items), dim3(64 * FEW_WAVES), lds, st, a, room);
 }
