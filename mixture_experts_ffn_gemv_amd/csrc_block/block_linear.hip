@@ -560,8 +560,10 @@ __global__ __launch_bounds__(1024) void linear_bias_kernel(LinArgs a) {
 // ------------------------------------------------------------------ few rows
 
 // Up to 16 rows of each matrix: FWD with the weights read straight into registers, since nothing would be
-// read twice. A workgroup owns 16 weight rows, each of its eight wavefronts a part of k, and their sums are
-// joined through LDS in wavefront order. x comes into LDS whole, or as much of k at a time as fits.
+// read twice. A wavefront multiplies 16 weight rows at a time. Either the eight of a workgroup have the same ones, each a
+// part of k, and their sums are joined through LDS in wavefront order; or (OWN) each has its own and all of k, where
+// there are enough of them to fill the CUs: with short k the parts would be a load or two each. x comes into LDS whole, or
+// as much of k at a time as fits.
 constexpr int FEW_WAVES = 8, FEW_ROWS = 16;
 constexpr int FEW_LDS = 64 << 10;
 // values of k that a pass takes, a multiple of 512: whole runs of 1024 bytes
@@ -570,12 +572,12 @@ MOE_DEV __host__ int few_pass(int rows, int K) {
     return whole < fit ? whole : fit;
 }
 
-template <typename T, int ACT>
+template <typename T, int ACT, bool OWN>
 __global__ __launch_bounds__(64 * FEW_WAVES) void linear_few_kernel(LinArgs a, int room) {
     constexpr int AHEAD = 5;
     extern __shared__ __align__(16) uint8_t smem[];   // x; then sums [wavefront][256]
     const int tid = threadIdx.x, lane = tid & 63, wv = __builtin_amdgcn_readfirstlane(tid >> 6), l16 = lane & 15, g = lane >> 4;
-    const int n0 = blockIdx.x * 16, pass_k = few_pass(room, a.K), row_bytes = pass_k * 2, runs = row_bytes / 1024;
+    const int n0 = (OWN ? blockIdx.x * FEW_WAVES + wv : blockIdx.x) * 16, pass_k = few_pass(room, a.K), row_bytes = pass_k * 2, runs = row_bytes / 1024;
     Slice s{0, 0, a.m, 0};
     if (a.offsets != nullptr) {
         if (!find_slice(a, room, 1, blockIdx.y, s)) return;
@@ -588,15 +590,16 @@ __global__ __launch_bounds__(64 * FEW_WAVES) void linear_few_kernel(LinArgs a, i
     const auto X = buffer_rsrc(a.x + row0 * a.ldx, (uint32_t)((rows - 1) * a.ldx + a.K) * 2);
     const int xt = min(l16, rows - 1);   // (a token that does not exist reads another's; its sums are not used)
     f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-    // the first wavefront finishes: eight values of row lane / 2 a lane. What it adds is requested before the weights
+    // the first wavefront (OWN: each) finishes: eight values of row lane / 2 a lane. What it adds is requested before
+    // the weights
     const int er = lane >> 1, ep = n0 + (lane & 1) * 8, left = a.N - ep;
-    const bool ends = wv == 0 && er < rows && left > 0;
+    const bool ends = (OWN || wv == 0) && er < rows && left > 0;
     uint4 bias = make_uint4(0, 0, 0, 0), residual = bias;
     if (ends && a.bias != nullptr) bias = load8(a.bias + (size_t)s.expert * a.N + ep, left);
     if (ends && a.residual != nullptr) residual = load8(a.residual + (row0 + er) * a.ldr + ep, left);
     for (int k0 = 0; k0 < a.K; k0 += pass_k) {
         const int chunks = (min(pass_k, a.K - k0) + 31) / 32;
-        const int c0 = wv * chunks / FEW_WAVES, c1 = (wv + 1) * chunks / FEW_WAVES;
+        const int c0 = OWN ? 0 : wv * chunks / FEW_WAVES, c1 = OWN ? chunks : (wv + 1) * chunks / FEW_WAVES;
         for (int r = wv; r < rows * runs; r += FEW_WAVES) {
             // 16-byte chunk c of a row lies at c ^ (row & 15)
             const int row = r / runs, k = k0 + (r - row * runs) * 512 + (lane ^ (row & 15)) * 8;
@@ -637,7 +640,7 @@ __global__ __launch_bounds__(64 * FEW_WAVES) void linear_few_kernel(LinArgs a, i
     for (int h = 0; h < 2; ++h) {
         f32x4 v = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int i = 0; i < FEW_WAVES; ++i) v += *reinterpret_cast<const f32x4*>(&red[i * 256 + (2 * (lane & 1) + h) * 64 + er * 4]);
+        for (int i = OWN ? wv : 0; i < (OWN ? wv + 1 : FEW_WAVES); ++i) v += *reinterpret_cast<const f32x4*>(&red[i * 256 + (2 * (lane & 1) + h) * 64 + er * 4]);
 #pragma unroll
         for (int r = 0; r < 4; ++r) o[4 * h + r] = v[r];
     }
@@ -861,6 +864,11 @@ LinArgs describe(const moe_linear* f, int m, const int32_t* offsets) {
     return a;
 }
 
+// Whether each wavefront has weight rows of its own, of `blocks` of 16 in all. With parts of k and with rows of its own:
+// 122 experts of 432 x 1813 (K x N) with 105 rows 80 and 29 us, 64 of 1024 x 2048 with one row each 69 and 45, 32 of
+// 4096 x 2048 101 and 101; one row of 1024 x 32768 13.6 and 13.6, of 512 x 8192 5.6 and 7.1.
+bool few_own(int K, int64_t blocks) { return K <= 2048 && blocks >= 2048; }
+
 template <typename T, int ACT>
 hipError_t forward_act(const LinArgs& a, float* partial, hipStream_t st) {
     const int each = cdiv(a.m, a.experts);   // rows of an expert, on average
@@ -869,7 +877,10 @@ hipError_t forward_act(const LinArgs& a, float* partial, hipStream_t st) {
     // L2): a token's six experts of 384 31.9 us with room for all six rows, 29.2 with room for two
     const int room = std::min(a.m, a.offsets != nullptr ? std::min(2 * each, FEW_ROWS) : FEW_ROWS), items = a.offsets != nullptr ? a.m / room + std::min(a.experts, a.m) : cdiv(a.m, room);
     const size_t lds = std::max<size_t>((size_t)room * few_pass(room, a.K) * 2, sizeof(float) * FEW_WAVES * 256);
-    return launch_kernel(linear_few_kernel<T, ACT>, dim3(cdiv(a.N, 16), items), dim3(64 * FEW_WAVES), lds, st, a, room);
+    const int blocks = cdiv(a.N, 16);
+    const bool own = few_own(a.K, (int64_t)blocks * std::min(items, std::max(a.m, 1)));
+    return launch_kernel(own ? linear_few_kernel<T, ACT, true> : linear_few_kernel<T, ACT, false>, dim3(own ? cdiv(blocks, FEW_WAVES) : blocks, items),
+                         dim3(64 * FEW_WAVES), lds, st, a, room);
 }
 template <typename T>
 hipError_t forward(const LinArgs& a, float* partial, hipStream_t st) {

@@ -224,7 +224,7 @@ def linear_run(c, act, bias=True, residual=True, offsets=None, extra=0, step=Tru
 LINEAR = [(1, 8, 1, BF16, "none"), (1, 256, 264, F16, "silu"), (2, 64, 37, BF16, "gelu"), (3, 4104, 40, F16, "none"), (15, 72, 130, BF16, "silu"),
           (16, 2312, 19, F16, "gelu"), (16, 520, 4099, BF16, "none"), (17, 264, 72, F16, "silu"), (23, 1032, 257, BF16, "gelu"),
           (33, 136, 264, F16, "none"), (64, 256, 771, BF16, "silu"), (65, 776, 256, F16, "gelu"), (127, 72, 201, BF16, "none"),
-          (130, 1024, 520, BF16, "silu"), (257, 392, 646, F16, "gelu"), (300, 264, 264, BF16, "none"), (40, 4104, 72, BF16, "silu")]
+          (130, 1024, 520, BF16, "silu"), (257, 392, 646, F16, "gelu"), (300, 264, 264, BF16, "none"), (40, 4104, 72, BF16, "silu"), (3, 72, 33001, F16, "gelu"), (12, 520, 40000, BF16, "none")]
 
 
 @pytest.mark.parametrize("m,k,n,dtype,act", LINEAR)
@@ -309,6 +309,8 @@ EXPERTS = [  # rows of each expert (and rows behind the last), K, N
     ([130, 0, 127, 1, 300], 11, 264, 200, BF16, "gelu"),
     ([700, 1, 0, 300], 0, 72, 264, BF16, "none"),
     ([5] * 70 + [0] * 30 + [70], 0, 40, 24, F16, "silu"),    # more experts than a wavefront's lanes
+    ([1, 0, 2] * 30, 4, 72, 1401, BF16, "gelu"),             # a wavefront's own weight rows, past the last of them
+    ([3] + [1] * 60, 0, 520, 712, F16, "none"),
 ]
 
 
