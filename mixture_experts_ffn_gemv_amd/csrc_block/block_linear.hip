@@ -470,12 +470,27 @@ MOE_DEV __host__ int dz_rows(int m) { return m >= 512 * 64 ? 64 : m >= 512 * 32 
 // at most as many chunks have m rows or fewer
 int dz_chunks(int m) { return std::max({(m + 63) / 64, std::min((m + 15) / 16, 1024), std::min((m + 31) / 32, 1024)}); }
 
-// the number of experts whose rows end at `row` or before: the expert of that row
-MOE_DEV int expert_of(const LinArgs& a, int row) {
+// The experts of rising rows: the ends of 64 experts at a time wait in the lanes
+struct ExpertWalk {
+    int base, end;   // the lane's: where expert base + lane ends
+};
+MOE_DEV ExpertWalk walk_experts(const LinArgs& a, int row) {
     const int lane = threadIdx.x & 63;
-    int n = 0;
+    int n = 0;   // experts that end at `row` or before
+#pragma unroll 4
     for (int e0 = 0; e0 < a.experts; e0 += 64) n += __popcll(__ballot(e0 + lane < a.experts && offset_at(a, e0 + lane + 1) <= row));
-    return n;
+    return {n, offset_at(a, n + lane + 1)};
+}
+// the expert of `row` and where it ends (experts that are not there end with the last)
+MOE_DEV int expert_of(const LinArgs& a, ExpertWalk& w, int row, int& end) {
+    uint64_t past;
+    while ((past = __ballot(w.end > row)) == 0 && w.base + 64 < a.experts) {
+        w.base += 64;
+        w.end = offset_at(a, w.base + (threadIdx.x & 63) + 1);
+    }
+    const int l = past != 0 ? __builtin_ctzll(past) : 0;
+    end = __builtin_amdgcn_readlane(w.end, l);
+    return min(w.base + l, a.experts - 1);
 }
 
 // STORE: dz is wanted (else it is dy itself, and only the sums are)
@@ -486,11 +501,16 @@ __global__ __launch_bounds__(256) void linear_dz_kernel(LinArgs a) {
     constexpr int U = 4;   // rows that a wavefront requests at a time
     const int chunk = dz_rows(a.m), first = blockIdx.x * chunk, n0 = blockIdx.y * DZ_COLS + lane * 8, left = a.N - n0;
     const int last = min(first + chunk, a.offsets != nullptr ? offset_of(a, a.experts) : a.m);
+    const bool parts = a.offsets != nullptr && a.partial != nullptr;   // each expert's sums are wanted
+    ExpertWalk walk{0, 0};
+    if (parts && first < last) walk = walk_experts(a, first);
     int row = first;
     while (row < last) {
-        const int e = a.offsets != nullptr ? expert_of(a, row) : 0;
-        // (offsets that go back must not hold the loop up)
-        const int end = a.offsets != nullptr ? max(min(last, offset_of(a, e + 1)), row + 1) : last;
+        int e = 0, end = last;
+        if (parts) {
+            e = expert_of(a, walk, row, end);
+            end = max(min(last, end), row + 1);   // (offsets that go back must not hold the loop up)
+        }
         float sum[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) sum[i] = 0.f;
