@@ -527,6 +527,21 @@ def test_a_block_of_them_on_another_stream():
         assert torch.equal(a[k], b[k]), k
 
 
+def test_two_blocks_of_them_at_once():
+    # each with its own buffers, workspaces and stream
+    a, b, c, d = (chain_tensors(300, 2, 6, 136, 264, F16, seed=s) for s in (4, 5, 4, 5))
+    chain_step(a)
+    chain_step(b)
+    torch.cuda.synchronize()
+    streams = torch.cuda.Stream(), torch.cuda.Stream()
+    for _ in range(3):
+        for t, s in zip((c, d), streams):
+            chain_step(t, stream=s)
+    torch.cuda.synchronize()
+    for k in OUTPUTS:
+        assert torch.equal(a[k], c[k]) and torch.equal(b[k], d[k]), k
+
+
 def test_with_the_routing_of_the_layer():
     # the picks and weights that moe_route writes are what moe_sort and moe_combine_forward take
     shape, m = S.TINY, 50
