@@ -194,15 +194,12 @@ MOE_DEV Tile locate(const LinArgs& a, int tile, int nq, int np, const uint16_t* 
     return t;
 }
 
-// What a wavefront does with its sums of 16 NJ q (from qw) and TP p (from pw): v[i][j] of a lane is p = 16 i +
-// 4 g + 0..3 of q = 16 j + l16. They pass through the wavefront's own piece of LDS, SLAB bytes, a few rows at
-// a time, so that a lane has eight values of one row, and its neighbours the ones beside them: memory is
-// read and written in whole lines (four values a lane wrote quarters of them).
 // what other lanes of the wavefront wrote to LDS before is read after, and the other way round
 MOE_DEV void wave_fence() {
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     __builtin_amdgcn_wave_barrier();
 }
+// A wavefront's own piece of LDS, through which its sums pass on their way out: a few rows of TP values at a time
 template <int TP>
 struct Slab {
     static constexpr int LPR = TP / 8, ROWS = 64 / LPR >= 16 ? 16 : 8, STRIDE = TP + 4;   // lanes per row
@@ -225,6 +222,10 @@ MOE_DEV void put_forward(const LinArgs& a, int64_t row, int p, int left, float (
     for (int i = 0; i < 8; ++i) o[i] = act_of<ACT>(o[i]) + res[i];
     store8(a.y + row * a.ldy + p, left, pack8<T>(o));
 }
+// What a wavefront does with its sums of 16 NJ q (from qw) and TP p (from pw): v[i][j] of a lane is p = 16 i +
+// 4 g + 0..3 of q = 16 j + l16. They pass through the wavefront's own piece of LDS, a few rows at a time, so
+// that a lane has eight values of one row, and its neighbours the ones beside them: memory is read and written in
+// whole lines (four values a lane wrote quarters of them).
 template <typename T, Kind KIND, int ACT, int TP, int NI, int NJ>
 MOE_DEV void finish(const LinArgs& a, const Tile& t, int qw, int pw, const f32x4 (&v)[NI][NJ], float* slab) {
     typedef Slab<TP> S;
@@ -464,7 +465,7 @@ __global__ __launch_bounds__(64 * WQ * WP) void linear_join_kernel(LinArgs a, Pl
 // several experts': where one ends the sums of its columns go to the row (chunk + expert) of `partial`, a number of
 // its own for every expert in every chunk.
 constexpr int DZ_COLS = 512;
-// rows of a chunk: 16, or as many more as leave at least 512 chunks, up to 64 (1013 x 4101: 28.7 us with 64, 8
+// rows of a chunk: 16, or as many more as leave at least 512 chunks, up to 64 (1013 x 4101: 28.7 us with 64, 11.8
 // with 16)
 MOE_DEV __host__ int dz_rows(int m) { return m >= 512 * 64 ? 64 : m >= 512 * 32 ? 32 : 16; }
 // at most as many chunks have m rows or fewer
@@ -477,7 +478,6 @@ struct ExpertWalk {
 MOE_DEV ExpertWalk walk_experts(const LinArgs& a, int row) {
     const int lane = threadIdx.x & 63;
     int n = 0;   // experts that end at `row` or before
-#pragma unroll 4
     for (int e0 = 0; e0 < a.experts; e0 += 64) n += __popcll(__ballot(e0 + lane < a.experts && offset_at(a, e0 + lane + 1) <= row));
     return {n, offset_at(a, n + lane + 1)};
 }
