@@ -83,6 +83,13 @@ def test_sort_is_the_stable_order(m, topk, n_experts, bad):
         assert torch.equal(got, want)
 
 
+@pytest.mark.parametrize("n", [24 * 1024, 24 * 1024 + 1])
+def test_sort_of_as_many_picks_as_one_launch_takes_and_one_more(n):
+    idx = picks(n, 1, 1024, n, bad=0.03)
+    for got, want in zip(sort_run(idx, 1024), ref.sort(idx, 1024)):
+        assert torch.equal(got, want)
+
+
 def test_sort_without_picks_and_on_another_stream():
     idx = picks(3000, 6, 100, 5)
     want = ref.sort(idx, 100)

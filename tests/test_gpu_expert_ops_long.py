@@ -103,3 +103,17 @@ def test_experts_of_many_tiles_against_float64(n_experts, rows, k, n, dtype, act
             want = ref.linear(c["x"][a:b], c["w"][e], c["bias"][e] if bias else None, c["residual"][a:b], act, dy=c["dy"][a:b])
             for name, t in got.items():
                 check(t[a:b] if name in ("y", "dx") else t[e], want[name], f"{name} of expert {e}")
+
+
+def test_gradients_of_more_workgroups_than_a_grid_holds_along_one_axis():
+    # (a workgroup a token: 2^24 of 256 threads; tokens without rows but for the last)
+    m, dim = 1 << 24, 1032
+    dy = torch.empty(m, dim, dtype=BF16, device=DEV)
+    dy[-1] = 2
+    e = torch.full((1, dim), 3.0, dtype=BF16, device=DEV)
+    row_of = torch.full((m, 1), -1, dtype=torch.int32, device=DEV)
+    row_of[-1] = 0
+    weights, dweights, de = torch.full((m, 1), 0.5, device=DEV), torch.full((m, 1), NAN, device=DEV), torch.full_like(e, NAN)
+    moe.moe_combine_backward(dy, e, weights, row_of, de, dweights)
+    torch.cuda.synchronize()
+    assert not dweights[:-1].any() and dweights[-1].item() == 6.0 * dim and (de == 1).all()
