@@ -580,24 +580,19 @@ __global__ __launch_bounds__(1024) void linear_bias_kernel(LinArgs a) {
 // ------------------------------------------------------------------ few rows
 
 // Up to 16 rows of each matrix: FWD with the weights read straight into registers, since nothing would be
-// read twice. A wavefront multiplies 16 weight rows at a time. Either the eight of a workgroup have the same ones, each a
-// part of k, and their sums are joined through LDS in wavefront order; or (OWN) each has its own and all of k, where
-// there are enough of them to fill the CUs: with short k the parts would be a load or two each. x comes into LDS whole, or
-// as much of k at a time as fits.
+// read twice. A workgroup multiplies 16 weight rows at a time, each wavefront a part of k, and their sums are joined through
+// LDS in wavefront order. x comes into LDS whole.
 constexpr int FEW_WAVES = 8, FEW_ROWS = 16;
 constexpr int FEW_LDS = 64 << 10;
-// values of k that a pass takes, a multiple of 512: whole runs of 1024 bytes
-MOE_DEV __host__ int few_pass(int rows, int K) {
-    const int whole = (K + 511) / 512 * 512, fit = FEW_LDS / (rows * 1024) * 512;
-    return whole < fit ? whole : fit;
-}
+// values of k of a row in LDS, whole runs of 1024 bytes
+MOE_DEV __host__ int few_row(int K) { return (K + 511) / 512 * 512; }
 
-template <typename T, int ACT, bool OWN>
+template <typename T, int ACT>
 __global__ __launch_bounds__(64 * FEW_WAVES) void linear_few_kernel(LinArgs a, int room) {
     constexpr int AHEAD = 5;
     extern __shared__ __align__(16) uint8_t smem[];   // x; then sums [wavefront][256]
     const int tid = threadIdx.x, lane = tid & 63, wv = __builtin_amdgcn_readfirstlane(tid >> 6), l16 = lane & 15, g = lane >> 4;
-    const int n0 = (OWN ? blockIdx.x * FEW_WAVES + wv : blockIdx.x) * 16, pass_k = few_pass(room, a.K), row_bytes = pass_k * 2, runs = row_bytes / 1024;
+    const int n0 = blockIdx.x * 16, row_bytes = few_row(a.K) * 2, runs = row_bytes / 1024;
     Slice s{0, 0, a.m, 0};
     if (a.offsets != nullptr) {
         if (!find_slice(a, room, 1, blockIdx.y, s)) return;
@@ -610,46 +605,42 @@ __global__ __launch_bounds__(64 * FEW_WAVES) void linear_few_kernel(LinArgs a, i
     const auto X = buffer_rsrc(a.x + row0 * a.ldx, (uint32_t)((rows - 1) * a.ldx + a.K) * 2);
     const int xt = min(l16, rows - 1);   // (a token that does not exist reads another's; its sums are not used)
     f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-    // the first wavefront (OWN: each) finishes: eight values of row lane / 2 a lane. What it adds is requested before
-    // the weights
+    // the first wavefront finishes: eight values of row lane / 2 a lane. What it adds is requested before the weights
     const int er = lane >> 1, ep = n0 + (lane & 1) * 8, left = a.N - ep;
-    const bool ends = (OWN || wv == 0) && er < rows && left > 0;
+    const bool ends = wv == 0 && er < rows && left > 0;
     uint4 bias = make_uint4(0, 0, 0, 0), residual = bias;
     if (ends && a.bias != nullptr) bias = load8(a.bias + (size_t)s.expert * a.N + ep, left);
     if (ends && a.residual != nullptr) residual = load8(a.residual + (row0 + er) * a.ldr + ep, left);
-    for (int k0 = 0; k0 < a.K; k0 += pass_k) {
-        const int chunks = (min(pass_k, a.K - k0) + 31) / 32;
-        const int c0 = OWN ? 0 : wv * chunks / FEW_WAVES, c1 = OWN ? chunks : (wv + 1) * chunks / FEW_WAVES;
-        for (int r = wv; r < rows * runs; r += FEW_WAVES) {
-            // 16-byte chunk c of a row lies at c ^ (row & 15)
-            const int row = r / runs, k = k0 + (r - row * runs) * 512 + (lane ^ (row & 15)) * 8;
-            buffer_load_lds16(X, smem + r * 1024, k < a.K ? (uint32_t)(row * a.ldx + k) * 2 : PAST);
-        }
-        uint4 wq[AHEAD];
-        auto request = [&](int i, int c) { wq[i] = *reinterpret_cast<const uint4*>(w + min(k0 + 32 * min(c, chunks - 1) + 8 * g, a.K - 8)); };
-#pragma unroll
-        for (int i = 0; i < AHEAD; ++i) request(i, c0 + i);
-        wait_vm_loads<AHEAD>();   // this wavefront's part of x has landed
-        barrier_lds();
-        auto multiply = [&](int i, int c) {
-            // a weight that stands in for one past K is not one (x is zero there)
-            const uint32_t on = k0 + 32 * c + 8 * g < a.K ? ~0u : 0u;
-            const u32x4 wm = {wq[i].x & on, wq[i].y & on, wq[i].z & on, wq[i].w & on};
-            const int cx = c * 4 + g;
-            acc = T::mfma(__builtin_bit_cast(s16x8, wm), *reinterpret_cast<const s16x8*>(smem + xt * row_bytes + ((cx ^ (xt & 15)) << 4)), acc);
-        };
-        int c = c0;
-        for (; c + AHEAD < c1; c += AHEAD)
-#pragma unroll
-            for (int i = 0; i < AHEAD; ++i) {
-                multiply(i, c + i);
-                request(i, c + AHEAD + i);
-            }
-#pragma unroll
-        for (int i = 0; i < AHEAD; ++i)
-            if (c + i < c1) multiply(i, c + i);   // (a chunk of another's part is left out)
-        __syncthreads();   // x is read; the next part, or the sums, take its place
+    const int chunks = (a.K + 31) / 32, c0 = wv * chunks / FEW_WAVES, c1 = (wv + 1) * chunks / FEW_WAVES;
+    for (int r = wv; r < rows * runs; r += FEW_WAVES) {
+        // 16-byte chunk c of a row lies at c ^ (row & 15)
+        const int row = r / runs, k = (r - row * runs) * 512 + (lane ^ (row & 15)) * 8;
+        buffer_load_lds16(X, smem + r * 1024, k < a.K ? (uint32_t)(row * a.ldx + k) * 2 : PAST);
     }
+    uint4 wq[AHEAD];
+    auto request = [&](int i, int c) { wq[i] = *reinterpret_cast<const uint4*>(w + min(32 * min(c, chunks - 1) + 8 * g, a.K - 8)); };
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) request(i, c0 + i);
+    wait_vm_loads<AHEAD>();   // this wavefront's part of x has landed
+    barrier_lds();
+    auto multiply = [&](int i, int c) {
+        // a weight that stands in for one past K is not one (x is zero there)
+        const uint32_t on = 32 * c + 8 * g < a.K ? ~0u : 0u;
+        const u32x4 wm = {wq[i].x & on, wq[i].y & on, wq[i].z & on, wq[i].w & on};
+        const int cx = c * 4 + g;
+        acc = T::mfma(__builtin_bit_cast(s16x8, wm), *reinterpret_cast<const s16x8*>(smem + xt * row_bytes + ((cx ^ (xt & 15)) << 4)), acc);
+    };
+    int c = c0;
+    for (; c + AHEAD < c1; c += AHEAD)
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) {
+            multiply(i, c + i);
+            request(i, c + AHEAD + i);
+        }
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i)
+        if (c + i < c1) multiply(i, c + i);   // (a chunk of another's part is left out)
+    __syncthreads();   // x is read; the sums take its place
     float* red = reinterpret_cast<float*>(smem);
     *reinterpret_cast<f32x4*>(&red[wv * 256 + lane * 4]) = acc;
     __syncthreads();
@@ -660,7 +651,7 @@ __global__ __launch_bounds__(64 * FEW_WAVES) void linear_few_kernel(LinArgs a, i
     for (int h = 0; h < 2; ++h) {
         f32x4 v = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int i = OWN ? wv : 0; i < (OWN ? wv + 1 : FEW_WAVES); ++i) v += *reinterpret_cast<const f32x4*>(&red[i * 256 + (2 * (lane & 1) + h) * 64 + er * 4]);
+        for (int i = 0; i < FEW_WAVES; ++i) v += *reinterpret_cast<const f32x4*>(&red[i * 256 + (2 * (lane & 1) + h) * 64 + er * 4]);
 #pragma unroll
         for (int r = 0; r < 4; ++r) o[4 * h + r] = v[r];
     }
@@ -884,23 +875,36 @@ LinArgs describe(const moe_linear* f, int m, const int32_t* offsets) {
     return a;
 }
 
-// Whether each wavefront has weight rows of its own, of `blocks` of 16 in all. With parts of k and with rows of its own:
-// 122 experts of 432 x 1813 (K x N) with 105 rows 80 and 29 us, 64 of 1024 x 2048 with one row each 69 and 45, 32 of
-// 4096 x 2048 101 and 101; one row of 1024 x 32768 13.6 and 13.6, of 512 x 8192 5.6 and 7.1.
-bool few_own(int K, int64_t blocks) { return K <= 2048 && blocks >= 2048; }
+// Whether m rows take the kernel for few rows; `room`: rows of x that a workgroup of it has LDS for, all of them or with
+// offsets twice the average (more of one expert read its weights again, from the L2). x has to fit whole, and with offsets
+// it is for so few experts that tiles of 32 rows leave CUs idle; with short k, of which each wavefront has but a load or two,
+// for fewer. That kernel and those tiles, weights from memory, K x N:
+//   4096 x 4096          1 row 9.9 and 15.7 us, 8 rows 10.4 and 15.5, 16 rows (not whole) 15.2 and 15.5
+//   8192 x 1024          1 row 11.2 and 14.5 us, 16 rows (not whole) 19.1 and 14.4
+//   2048 x 65536         1 row 55.6 and 64.4 us, 16 rows 63.9 and 64.9
+//   384 of 2304 x 5120   2 rows 18.1 and 33.1 us, 4 rows 27.8 and 34.8, 6 rows 39.7 and 37.2, 12 rows 71.5 and 52.3
+//   384 of 2304 x 1280   6 rows 13.9 and 33.0 us, 16 rows 28.2 and 34.7, 96 rows 136 and 99, 1536 rows 597 and 373
+//   384 of 256 x 2048    2 rows 7.5 and 7.4 us, 6 rows 12.1 and 7.6
+//   64 of 1024 x 2048    6 rows 8.4 and 15.9 us, 24 rows 23.6 and 19.8
+//   122 of 432 x 1813    6 rows 6.9 and 10.4 us, 16 rows 15.0 and 11.2
+//   8 of 4096 x 4096     6 rows 42.0 and 58.2 us, 16 rows 55.3 and 63.4
+bool few_rows(const LinArgs& a, int& room) {
+    const int each = cdiv(a.m, a.experts);   // rows of an expert, on average
+    if (each > FEW_ROWS) return false;
+    room = std::min(a.m, a.offsets != nullptr ? std::min(2 * each, FEW_ROWS) : FEW_ROWS);
+    if (room * few_row(a.K) * 2 > FEW_LDS) return false;
+    if (a.offsets == nullptr) return true;
+    const double picked = a.experts * (1 - std::pow(1 - 1.0 / a.experts, a.m));   // experts with a row, where every row picks one of all
+    return picked * cdiv(a.N, 128) < std::min(a.K / 4, a.K < 4096 ? 200 : N_CU);
+}
 
 template <typename T, int ACT>
 hipError_t forward_act(const LinArgs& a, float* partial, hipStream_t st) {
-    const int each = cdiv(a.m, a.experts);   // rows of an expert, on average
-    if (each > FEW_ROWS) return launch_forward<T, ACT>(a, partial, st);
-    // LDS room for as many rows, or with offsets twice the average (more of one expert read its weights again, from the
-    // L2): a token's six experts of 384 31.9 us with room for all six rows, 29.2 with room for two
-    const int room = std::min(a.m, a.offsets != nullptr ? std::min(2 * each, FEW_ROWS) : FEW_ROWS), items = a.offsets != nullptr ? a.m / room + std::min(a.experts, a.m) : cdiv(a.m, room);
-    const size_t lds = std::max<size_t>((size_t)room * few_pass(room, a.K) * 2, sizeof(float) * FEW_WAVES * 256);
-    const int blocks = cdiv(a.N, 16);
-    const bool own = few_own(a.K, (int64_t)blocks * std::min(items, std::max(a.m, 1)));
-    return launch_kernel(own ? linear_few_kernel<T, ACT, true> : linear_few_kernel<T, ACT, false>, dim3(own ? cdiv(blocks, FEW_WAVES) : blocks, items),
-                         dim3(64 * FEW_WAVES), lds, st, a, room);
+    int room = 0;
+    if (!few_rows(a, room)) return launch_forward<T, ACT>(a, partial, st);
+    const int items = a.offsets != nullptr ? a.m / room + std::min(a.experts, a.m) : 1;
+    const size_t lds = std::max<size_t>((size_t)room * few_row(a.K) * 2, sizeof(float) * FEW_WAVES * 256);
+    return launch_kernel(linear_few_kernel<T, ACT>, dim3(cdiv(a.N, 16), items), dim3(64 * FEW_WAVES), lds, st, a, room);
 }
 template <typename T>
 hipError_t forward(const LinArgs& a, float* partial, hipStream_t st) {
