@@ -7,6 +7,9 @@
 // rows a call holds before it. The 128 bits serve eight values of 16: one generator call for each 16 bytes
 // of 16-bit values. 32 bits per value would cost twice the multiplications, which are most of the
 // instructions here; with 16 a probability is a multiple of 2^-16, and the scale that of the multiple.
+//
+// Memory bounds it: 8192 x 5120 bf16 43 us with a residual (252 MB, 5.9 TB/s) and 34 without (168 MB, 5.0 TB/s); 1003 x
+// 1111 f32 is a launch, 4 to 5 us.
 #include "block_rows.h"
 
 namespace moe {

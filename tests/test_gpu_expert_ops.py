@@ -83,7 +83,7 @@ def test_sort_is_the_stable_order(m, topk, n_experts, bad):
         assert torch.equal(got, want)
 
 
-@pytest.mark.parametrize("n", [24 * 1024, 24 * 1024 + 1])
+@pytest.mark.parametrize("n", [24 * 1024, 24 * 1024 + 1, 48 * 1024 - 5, 48 * 1024, 48 * 1024 + 1, 60000])
 def test_sort_of_as_many_picks_as_one_launch_takes_and_one_more(n):
     idx = picks(n, 1, 1024, n, bad=0.03)
     for got, want in zip(sort_run(idx, 1024), ref.sort(idx, 1024)):
