@@ -583,6 +583,21 @@ def moe_w4_gated(w_gate, w_up, x, h, act="silu", limit=0.0, stream=None):
                                      _stream(stream)), me)
 
 
+_several = None   # whether there are devices that a tensor could be on but the current one
+
+
+def _stream_of(stream, where, *tensors):
+    """The stream of a call on these tensors (None among them: not given). Their device has to be the current one."""
+    global _several
+    if _several is None:
+        _several = torch.cuda.device_count() > 1
+    if _several:
+        here = torch.cuda.current_device()
+        if any(t is not None and t.get_device() != here for t in tensors):
+            raise MoeError(MOE_EINVAL, where)
+    return _stream(stream)
+
+
 def _any_rows(t, dtype, where):
     """A device matrix of that type with consecutive values in each row -> (pointer, row stride, rows, values of a row)."""
     shape = t.shape
@@ -617,7 +632,8 @@ def moe_sort(idx, n_experts, row_of, pick_of, offsets, work, stream=None):
     picks, m, topk = _picks(idx, me)
     return _check(lib().moe_sort(
         picks, m, topk, n_experts, _whole(row_of, (m, topk), torch.int32, me), _whole(pick_of, (m * topk,), torch.int32, me),
-        _whole(offsets, (n_experts + 1,), torch.int32, me), *_bytes(work, me), _stream(stream)), me)
+        _whole(offsets, (n_experts + 1,), torch.int32, me), *_bytes(work, me),
+        _stream_of(stream, me, idx, row_of, pick_of, offsets, work)), me)
 
 
 def _moved(tokens, sorted_rows, row_of, where):
@@ -637,14 +653,16 @@ def moe_dispatch_forward(x, row_of, xs, stream=None):
     """xs[row_of[t, j]] = x[t]: x [m, dim], row_of [m, topk], xs [rows, dim]."""
     me = "moe_dispatch_forward"
     dt, dim, x_, ldx, xs_, ldxs, rows, at, m, topk = _moved(x, xs, row_of, me)
-    return _check(lib().moe_dispatch_forward(dt, dim, x_, ldx, at, m, topk, xs_, ldxs, rows, _stream(stream)), me)
+    return _check(lib().moe_dispatch_forward(dt, dim, x_, ldx, at, m, topk, xs_, ldxs, rows,
+                                             _stream_of(stream, me, x, row_of, xs)), me)
 
 
 def moe_dispatch_backward(dxs, row_of, dx, stream=None):
     """dx[t] = sum over j of dxs[row_of[t, j]]."""
     me = "moe_dispatch_backward"
     dt, dim, dx_, lddx, dxs_, lddxs, rows, at, m, topk = _moved(dx, dxs, row_of, me)
-    return _check(lib().moe_dispatch_backward(dt, dim, dxs_, lddxs, rows, at, m, topk, dx_, lddx, _stream(stream)), me)
+    return _check(lib().moe_dispatch_backward(dt, dim, dxs_, lddxs, rows, at, m, topk, dx_, lddx,
+                                              _stream_of(stream, me, dxs, row_of, dx)), me)
 
 
 def moe_combine_forward(e, weights, row_of, y, stream=None):
@@ -652,7 +670,7 @@ def moe_combine_forward(e, weights, row_of, y, stream=None):
     me = "moe_combine_forward"
     dt, dim, y_, ldy, e_, lde, rows, at, m, topk = _moved(y, e, row_of, me)
     return _check(lib().moe_combine_forward(dt, dim, e_, lde, rows, _whole(weights, (m, topk), torch.float32, me), at, m, topk, y_, ldy,
-                                            _stream(stream)), me)
+                                            _stream_of(stream, me, e, weights, row_of, y)), me)
 
 
 def moe_combine_backward(dy, e, weights, row_of, de=None, dweights=None, stream=None):
@@ -661,7 +679,7 @@ def moe_combine_backward(dy, e, weights, row_of, de=None, dweights=None, stream=
     dt, dim, dy_, lddy, e_, lde, rows, at, m, topk = _moved(dy, e, row_of, me)
     return _check(lib().moe_combine_backward(
         dt, dim, dy_, lddy, e_, lde, rows, _whole(weights, (m, topk), torch.float32, me), at, m, topk, *_rows(de, rows, dim, dy.dtype, me),
-        _whole(dweights, (m, topk), torch.float32, me), _stream(stream)), me)
+        _whole(dweights, (m, topk), torch.float32, me), _stream_of(stream, me, dy, e, weights, row_of, de, dweights)), me)
 
 
 _LINEAR_ACTS = {**_ACTS, "none": MOE_ACT_NONE, None: MOE_ACT_NONE}
@@ -697,7 +715,7 @@ def moe_linear_forward(f, x, y, work, offsets=None, residual=None, saved=None, s
     return _check(lib().moe_linear_forward(
         ctypes.byref(f), *_rows(x, m, f.cols, dt, me), _whole(offsets, (f.experts + 1,), torch.int32, me), m,
         *_rows(residual, m, f.rows, dt, me), *_rows(y, m, f.rows, dt, me), *_bytes(saved, me), *_bytes(work, me),
-        _stream(stream)), me)
+        _stream_of(stream, me, *f.tensors, x, y, work, offsets, residual, saved)), me)
 
 
 def moe_linear_backward(f, x, dy, saved, work, offsets=None, dx=None, dw=None, dbias=None, stream=None):
@@ -707,7 +725,8 @@ def moe_linear_backward(f, x, dy, saved, work, offsets=None, dx=None, dw=None, d
     return _check(lib().moe_linear_backward(
         ctypes.byref(f), *_rows(x, m, f.cols, dt, me), _whole(offsets, (f.experts + 1,), torch.int32, me), m,
         *_rows(dy, m, f.rows, dt, me), *_bytes(saved, me), *_rows(dx, m, f.cols, dt, me), _whole(dw, w.shape, dt, me),
-        _whole(dbias, w.shape[:-1], dt, me), *_bytes(work, me), _stream(stream)), me)
+        _whole(dbias, w.shape[:-1], dt, me), *_bytes(work, me),
+        _stream_of(stream, me, *f.tensors, x, dy, saved, work, offsets, dx, dw, dbias)), me)
 
 
 def make_dropout(dim, dtype, p):
@@ -722,11 +741,11 @@ def moe_dropout_forward(f, rng, x, y, residual=None, stream=None):
     me, m, dt = "moe_dropout_forward", x.shape[0], f.torch_dtype
     return _check(lib().moe_dropout_forward(
         ctypes.byref(f), _whole(rng, (2,), torch.int64, me), *_rows(x, m, f.dim, dt, me), *_rows(residual, m, f.dim, dt, me), m,
-        *_rows(y, m, f.dim, dt, me), _stream(stream)), me)
+        *_rows(y, m, f.dim, dt, me), _stream_of(stream, me, rng, x, y, residual)), me)
 
 
 def moe_dropout_backward(f, rng, dy, dx, stream=None):
     """dx = keep dy / (1 - p) with the mask of the forward call."""
     me, m, dt = "moe_dropout_backward", dy.shape[0], f.torch_dtype
     return _check(lib().moe_dropout_backward(ctypes.byref(f), _whole(rng, (2,), torch.int64, me), *_rows(dy, m, f.dim, dt, me), m,
-                                             *_rows(dx, m, f.dim, dt, me), _stream(stream)), me)
+                                             *_rows(dx, m, f.dim, dt, me), _stream_of(stream, me, rng, dy, dx)), me)

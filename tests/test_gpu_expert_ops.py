@@ -571,3 +571,29 @@ def test_with_the_routing_of_the_layer():
     v = total * x.double().cpu()
     base.check(y, *ref.stored(v, (shape.topk + 1) * ref.F32 * v.abs(), BF16), "y")
     moe.moe_destroy(ctx)
+
+
+def test_tensors_of_another_device_are_refused(monkeypatch):
+    # (as it looks where these tensors' device is not the current one)
+    t = dict(x=torch.zeros(3, 64, dtype=BF16, device=DEV), row_of=torch.zeros(3, 1, dtype=torch.int32, device=DEV), w=torch.zeros(3, 1, device=DEV),
+             offsets=torch.zeros(2, dtype=torch.int32, device=DEV), rng=torch.zeros(2, dtype=torch.int64, device=DEV),
+             work=torch.empty(1 << 22, dtype=torch.uint8, device=DEV))
+    x, row_of, w = t["x"], t["row_of"], t["w"]
+    y = torch.full_like(x, 7)
+    f, drop = moe.make_linear(torch.zeros(64, 64, dtype=BF16, device=DEV)), moe.make_dropout(64, BF16, 0.5)
+    calls = [lambda: moe.moe_sort(row_of, 1, row_of, None, t["offsets"], None), lambda: moe.moe_dispatch_forward(x, row_of, y),
+             lambda: moe.moe_dispatch_backward(x, row_of, y), lambda: moe.moe_combine_forward(x, w, row_of, y),
+             lambda: moe.moe_combine_backward(x, x, w, row_of, y, w), lambda: moe.moe_linear_forward(f, x, y, t["work"]),
+             lambda: moe.moe_linear_backward(f, x, x, None, t["work"], dx=y), lambda: moe.moe_dropout_forward(drop, t["rng"], x, y),
+             lambda: moe.moe_dropout_backward(drop, t["rng"], x, y)]
+    monkeypatch.setattr(moe, "_several", True)
+    here = torch.cuda.current_device()
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: here + 1)
+    for call in calls:
+        with pytest.raises(moe.MoeError):
+            call()
+    monkeypatch.undo()
+    monkeypatch.setattr(moe, "_several", True)
+    assert (y == 7).all() and not row_of.any()
+    moe.moe_linear_forward(f, x, y, t["work"])
+    assert not y.any()
