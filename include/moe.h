@@ -570,8 +570,8 @@ int moe_linear_forward(const moe_linear* f, const void* x, int64_t ldx, const in
  * dz over an expert's rows. (The residual's is dy itself.) x, offsets, m, the weights and saved are those of the
  * forward call. dx [m, K] (row stride lddx as ldx), dw [experts, N, K] (16-byte aligned) and dbias [experts, N] are
  * written, not added to; each may be NULL and is then not computed. An expert without rows gets zeros. dz is
- * rounded to the value type, as an operand of the products (in f16, past 65504 it is infinite); dbias is summed
- * in f32 before that. m = 0 writes zeros to dw and dbias. No output may overlap an input. Errors as
+ * rounded to the value type, as an operand of the products (in f16, past 65504 it is infinite), but not where m is
+ * 8 or less and offsets NULL; dbias is summed in f32 before that. m = 0 writes zeros to dw and dbias. No output may overlap an input. Errors as
  * moe_linear_forward. */
 int moe_linear_backward(const moe_linear* f, const void* x, int64_t ldx, const int32_t* offsets, int32_t m,
                         const void* dy, int64_t lddy, const void* saved, size_t saved_bytes, void* dx, int64_t lddx,

@@ -11,7 +11,8 @@
 // wavefront adds up 64 at a time. A workgroup without a tile ends at once.
 //
 // dz is rounded to 16 bits, as an operand of the matrix cores, and nothing else before the results: the
-// gradients have sqrt(2) of the error that their own rounding gives them. z is kept in f32.
+// gradients have sqrt(2) of the error that their own rounding gives them. (Of eight rows or fewer of one matrix it is not:
+// their backward pass is a kernel of its own.) z is kept in f32.
 //
 // What bounds it: with few rows the weights' bytes (one row of 2304 x 5120 bf16: 8.0 us a call, 23.6 MB; six experts of
 // 5120 x 2304, one row each: 29 us, 4.9 TB/s; 64 experts of 2048 x 1408 f16, 47 rows each: 86 to 92 us, 390 MB); with many
@@ -665,6 +666,117 @@ __global__ __launch_bounds__(64 * FEW_WAVES) void linear_few_kernel(LinArgs a, i
     put_forward<T, ACT>(a, row0 + er, ep, left, o, bias, residual);
 }
 
+// Up to eight rows of one matrix, backward, in one pass over the weights: with so few rows the products are bound by reading W and
+// writing dW, dz can stay in f32 (a lane multiplies it itself), and nothing but dx's sums needs a second launch. A
+// workgroup has 512 columns of k, eight a lane, and `rows` weight rows, every fourth a wavefront; dz of 64 of them at a
+// time waits in LDS. Silu, all three gradients, weights from memory (K x N), and with dz, its sums and tiles instead: one row
+// of 5120 x 2304 18.3 us and 31.0 (47 MB), eight 23.0 and 31.3; of 4096 x 16384 70 and 121, eight 75 and 121 (268 MB); of 952 x
+// 364 10.6 and 13.3; eight of 8192 x 512 16.1 and 16.6. Sixteen rows of x and dx would not fit the registers.
+constexpr int FEW_BACK = 8, FEW_BACK_COLS = 512, FEW_BACK_ROWS = 64;
+
+template <typename T, int M>
+__global__ __launch_bounds__(256) void linear_few_backward_kernel(LinArgs a, int rows) {
+    __shared__ __align__(16) float dzs[FEW_BACK_ROWS][M];
+    __shared__ __align__(16) float red[4][FEW_BACK_COLS];
+    constexpr int U = 4;   // weight rows that a wavefront requests at a time
+    const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
+    const int k = blockIdx.x * FEW_BACK_COLS + lane * 8, first = blockIdx.y * rows, last = min(first + rows, a.N);
+    const bool live = k < a.K;
+    const int at = live ? k : 0;   // (a lane past K reads the first columns and writes none)
+    float x[M][8], dx[M][8];
+#pragma unroll
+    for (int t = 0; t < M; ++t) {
+        uint4 q = make_uint4(0, 0, 0, 0);   // (a row that does not exist: its dz is zero too)
+        if (t < a.m && a.dw != nullptr) q = *reinterpret_cast<const uint4*>(a.x + t * a.ldx + at);
+        unpack8<T>(q, x[t]);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) dx[t][i] = 0.f;
+    }
+    for (int n0 = first; n0 < last; n0 += FEW_BACK_ROWS) {
+        const int here = min(last - n0, FEW_BACK_ROWS);
+        for (int i = tid; i < FEW_BACK_ROWS * M; i += 256) {
+            const int t = i / FEW_BACK_ROWS, r = i % FEW_BACK_ROWS, n = n0 + r;
+            float d = 0.f;
+            if (t < a.m && r < here) {
+                d = T::load(a.dy[t * a.lddy + n]);
+                if (a.act != MOE_ACT_NONE) d *= act_slope(a.z[(size_t)t * padded(a.N) + n], a.act);
+            }
+            dzs[r][t] = d;
+        }
+        __syncthreads();
+        if (a.dbias != nullptr && blockIdx.x == 0 && tid < here) {
+            float s = 0.f;
+#pragma unroll
+            for (int t = 0; t < M; ++t) s += dzs[tid][t];
+            a.dbias[n0 + tid] = T::store(s);
+        }
+        if (a.dx != nullptr || a.dw != nullptr)
+            for (int r0 = wv; r0 < here; r0 += 4 * U) {
+                uint4 w[U];
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    w[u] = make_uint4(0, 0, 0, 0);
+                    if (a.dx != nullptr) w[u] = *reinterpret_cast<const uint4*>(a.w + (size_t)(n0 + min(r0 + 4 * u, here - 1)) * a.K + at);
+                }
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const int r = r0 + 4 * u;
+                    if (r >= here) break;
+                    float v[8], o[8], dz[M];
+                    unpack8<T>(w[u], v);
+#pragma unroll
+                    for (int t = 0; t < M; ++t) dz[t] = dzs[r][t];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) o[i] = 0.f;
+#pragma unroll
+                    for (int t = 0; t < M; ++t)
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) o[i] += dz[t] * x[t][i], dx[t][i] += dz[t] * v[i];
+                    if (a.dw != nullptr && live) *reinterpret_cast<uint4*>(a.dw + (size_t)(n0 + r) * a.K + k) = pack8<T>(o);
+                }
+            }
+        __syncthreads();   // dz is read
+    }
+    if (a.dx == nullptr) return;
+    // the wavefronts' sums in their order, a row at a time
+#pragma unroll
+    for (int t = 0; t < M; ++t) {
+        if (t < a.m) {
+            *reinterpret_cast<f32x4*>(&red[wv][lane * 8]) = (f32x4){dx[t][0], dx[t][1], dx[t][2], dx[t][3]};
+            *reinterpret_cast<f32x4*>(&red[wv][lane * 8 + 4]) = (f32x4){dx[t][4], dx[t][5], dx[t][6], dx[t][7]};
+            __syncthreads();
+            for (int c = tid; c < FEW_BACK_COLS; c += 256) {
+                const int col = blockIdx.x * FEW_BACK_COLS + c;
+                const float s = (red[0][c] + red[1][c]) + (red[2][c] + red[3][c]);
+                if (col < a.K) {
+                    if (gridDim.y == 1) a.dx[t * a.lddx + col] = T::store(s);
+                    else a.partial[((size_t)blockIdx.y * a.m + t) * a.K + col] = s;
+                }
+            }
+            __syncthreads();
+        }
+    }
+}
+
+// dx: the sums of `pieces` parts of the weight rows in a fixed order, 256 columns of a row by 16 wavefronts
+template <typename T>
+__global__ __launch_bounds__(1024) void linear_few_join_kernel(LinArgs a, int pieces) {
+    __shared__ __align__(16) f32x4 lds[16][64];
+    const int lane = threadIdx.x & 63, g = threadIdx.x >> 6, k = blockIdx.x * 256 + lane * 4, t = blockIdx.y;
+    f32x4 s = {0.f, 0.f, 0.f, 0.f};
+    if (k < a.K)
+#pragma unroll 8
+        for (int i = g; i < pieces; i += 16) s += *reinterpret_cast<const f32x4*>(a.partial + ((size_t)i * a.m + t) * a.K + k);
+    lds[g][lane] = s;
+    __syncthreads();
+    if (g == 0 && k < a.K) {
+        s = lds[0][lane];
+#pragma unroll
+        for (int i = 1; i < 16; ++i) s += lds[i][lane];
+        *reinterpret_cast<uint2*>(a.dx + t * a.lddx + k) = make_uint2(T::pack2(s[0], s[1]), T::pack2(s[2], s[3]));
+    }
+}
+
 // ------------------------------------------------------------------ plans
 
 int cdiv(int a, int b) { return (a + b - 1) / b; }
@@ -874,7 +986,19 @@ size_t sums_bytes(const moe_linear* f, int m) {
 }
 size_t dx_bytes(const moe_linear* f, int m) { return partial_bytes(DX, m, f->rows, f->cols, f->experts); }
 size_t dw_bytes(const moe_linear* f, int m) { return partial_bytes(DW, m, f->rows, f->cols, f->experts); }
-size_t backward_bytes(const moe_linear* f, int m) { return dz_bytes(f, m) + std::max(sums_bytes(f, m), dx_bytes(f, m) + dw_bytes(f, m)); }
+// weight rows of a workgroup: as many as make about two workgroups a CU, but 512 parts of the rows at most, and 16 rows at least
+int few_back_rows(int N, int K) {
+    const int parts = std::min(cdiv(2 * N_CU, cdiv(K, FEW_BACK_COLS)), 512);
+    return std::max(16, cdiv(cdiv(N, parts), 4) * 4);
+}
+
+// dx's sums of few rows
+size_t few_back_bytes(const moe_linear* f, int m) {
+    return f->experts > 1 ? 0 : round_up((size_t)cdiv(f->rows, few_back_rows(f->rows, f->cols)) * std::min(m, FEW_BACK) * f->cols * 4, 256);
+}
+size_t backward_bytes(const moe_linear* f, int m) {
+    return std::max(dz_bytes(f, m) + std::max(sums_bytes(f, m), dx_bytes(f, m) + dw_bytes(f, m)), few_back_bytes(f, m));
+}
 
 LinArgs describe(const moe_linear* f, int m, const int32_t* offsets) {
     LinArgs a{};
@@ -923,8 +1047,24 @@ hipError_t forward(const LinArgs& a, float* partial, hipStream_t st) {
                                    : forward_act<T, MOE_ACT_GELU>(a, partial, st);
 }
 
+template <typename T, int M>
+hipError_t few_backward_of(const LinArgs& a, hipStream_t st) {
+    const int rows = few_back_rows(a.N, a.K), parts = cdiv(a.N, rows);
+    const bool columns = a.dx != nullptr || a.dw != nullptr;
+    const hipError_t e = launch_kernel(linear_few_backward_kernel<T, M>, dim3(columns ? cdiv(a.K, FEW_BACK_COLS) : 1, parts), dim3(256), 0, st, a, rows);
+    if (e != hipSuccess || a.dx == nullptr || parts == 1) return e;
+    return launch_kernel(linear_few_join_kernel<T>, dim3(cdiv(a.K, 256), a.m), dim3(1024), 0, st, a, parts);
+}
+template <typename T>
+hipError_t few_backward(LinArgs a, float* partial, hipStream_t st) {
+    if (a.dx == nullptr && a.dw == nullptr && a.dbias == nullptr) return hipSuccess;
+    a.partial = partial;
+    return a.m == 1 ? few_backward_of<T, 1>(a, st) : a.m == 2 ? few_backward_of<T, 2>(a, st) : a.m <= 4 ? few_backward_of<T, 4>(a, st) : few_backward_of<T, 8>(a, st);
+}
+
 template <typename T>
 hipError_t backward(LinArgs a, uint8_t* work, size_t work_dz, size_t work_dx, bool direct, hipStream_t st) {
+    if (a.m > 0 && a.m <= FEW_BACK && a.offsets == nullptr) return few_backward<T>(a, reinterpret_cast<float*>(work), st);
     hipError_t e = hipSuccess;
     float* const partial = reinterpret_cast<float*>(work + work_dz);
     if (a.m > 0 && (!direct || a.dbias != nullptr)) {

@@ -246,6 +246,37 @@ def test_linear_against_float64(m, k, n, dtype, act):
         assert untouched(got[name]), name
 
 
+FEW = [(1, 952, 364, BF16, "silu"), (5, 1544, 4101, F16, "gelu"), (8, 520, 70, BF16, "none"), (7, 8, 3, F16, "silu"), (6, 5128, 1030, BF16, "gelu"),
+       (2, 8, 33001, F16, "silu"), (8, 512, 64, BF16, "gelu"), (4, 1032, 16, F16, "none"), (3, 520, 17, BF16, "silu"), (9, 520, 70, BF16, "silu")]
+
+
+@pytest.mark.parametrize("m,k,n,dtype,act", FEW)
+def test_gradients_of_few_rows_against_float64(m, k, n, dtype, act):
+    c = linear_case(m, k, n, dtype, seed=k + n)
+    want = ref.linear(c["x"], c["w"], c["bias"], c["residual"], act, dy=c["dy"])
+    got = linear_run(c, act, extra=5 * (m % 2))
+    for name, t in got.items():
+        check(t, *want[name], name)
+    assert untouched(got["dx"])
+    for only in ("dx", "dw", "dbias"):   # each by itself: the same bits
+        alone = linear_run(c, act, extra=5 * (m % 2), want=(only,))
+        assert torch.equal(alone[only], got[only]), only
+
+
+def test_few_rows_round_their_gradients_once():
+    # dW of one row is dz x: off by half a step of bf16 (2^-8), and by what z and the slope are off in f32. 64 terms of z are off by
+    # 64 2^-24 sum |x w| < 2e-4, and the slope, whose derivative is at most 1/2, by half of that: less than 2^-12
+    c = linear_case(1, 64, 4096, BF16, seed=11)
+    got = linear_run(c, "silu", residual=False)["dw"].cpu().double()
+    x, w, dy = (c[name].double() for name in ("x", "w", "dy"))
+    assert (x.abs() @ w.abs().T).max() < 50
+    z = x @ w.T + c["bias"].double()
+    s = torch.sigmoid(z)
+    slope = s * (1 + z * (1 - s))
+    value, most = (dy * slope).T * x, dy.T.abs() * x.abs() * 2.0 ** -12
+    assert ((got - value).abs() <= value.abs() * 2.0 ** -8 + most * 1.01).all()
+
+
 def test_linear_large_tiles_against_float64():
     # enough output tiles for the largest tiles in every product, none of them whole
     m, k, n = 2100, 4360, 2309
