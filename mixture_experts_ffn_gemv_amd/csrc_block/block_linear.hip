@@ -419,29 +419,44 @@ MOE_DEV void run_pieces(const LinArgs& a, const Plan& plan, const Share& mine, i
     }
 }
 
-// dx and dW in one launch, so that the longer pieces of the one (W_FIRST: dW's) are filled up with the other's: neither
-// fills the CUs evenly by itself. With offsets dW's tiles have as many steps as their expert has rows: each XCD has an
-// eighth of each expert's, those with the most rows first (experts of 8 to 2000 rows, 506 on average: no workgroup has
-// more than a quarter above the mean, where an eighth of the experts for each XCD left one with twice the mean).
-template <typename T, bool GROUPED, bool W_FIRST, int B, int WQ, int WP>
+// dx and dW of one matrix in one launch, so that the longer pieces of the one (W_FIRST: dW's) are filled up with the other's:
+// neither fills the CUs evenly by itself.
+template <typename T, bool W_FIRST, int B, int WQ, int WP>
 __global__ __launch_bounds__(64 * WQ * WP) void linear_backward_kernel(LinArgs a, Plan px, Plan pw) {
     extern __shared__ __align__(16) uint8_t smem[];
     typedef LinTile<T, DX, B, B, WQ, WP> ProductX;
     typedef LinTile<T, DW, B, B, WQ, WP> ProductW;
     constexpr size_t LDS = ProductX::LDS > ProductW::LDS ? ProductX::LDS : ProductW::LDS;
-    constexpr int SLAB = Slab<ProductX::TP>::BYTES;
     const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), xcd = blockIdx.x & 7;
-    float* const slab = reinterpret_cast<float*>(smem + LDS + wv * SLAB);
-    uint16_t* const order = reinterpret_cast<uint16_t*>(smem + LDS + WQ * WP * SLAB);
-    if (GROUPED && pw.whole > 0) sort_experts(a, ProductX::TH, reinterpret_cast<int*>(smem), order);
-    const Share sx = share_of(px, GROUPED && px.whole > 0 ? tiles_total(a, B) * px.np : px.whole, xcd);
-    const Share sw = share_of(pw, pw.whole, xcd);
-    const int run = max((pw.nq * pw.np + 7) >> 3, 1);
-    const int nx = sx.whole + sx.pieces, nw = GROUPED ? (pw.whole + 8 * run - 1) / (8 * run) * run : sw.whole + sw.pieces;
+    float* const slab = reinterpret_cast<float*>(smem + LDS + wv * Slab<ProductX::TP>::BYTES);
+    const Share sx = share_of(px, px.whole, xcd), sw = share_of(pw, pw.whole, xcd);
+    const int nx = sx.whole + sx.pieces, nw = sw.whole + sw.pieces;
     int turn = 0;
-    if (W_FIRST) run_pieces<T, DW, GROUPED, B, WQ, WP>(a, pw, sw, 0, nw, run, turn, order, smem, slab);
-    run_pieces<T, DX, GROUPED, B, WQ, WP>(a, px, sx, W_FIRST ? nw : 0, nx, run, turn, order, smem, slab);
-    if (!W_FIRST) run_pieces<T, DW, GROUPED, B, WQ, WP>(a, pw, sw, nx, nw, run, turn, order, smem, slab);
+    if (W_FIRST) run_pieces<T, DW, false, B, WQ, WP>(a, pw, sw, 0, nw, 1, turn, nullptr, smem, slab);
+    run_pieces<T, DX, false, B, WQ, WP>(a, px, sx, W_FIRST ? nw : 0, nx, 1, turn, nullptr, smem, slab);
+    if (!W_FIRST) run_pieces<T, DW, false, B, WQ, WP>(a, pw, sw, nx, nw, 1, turn, nullptr, smem, slab);
+}
+
+// dx or dW of a matrix per expert. dW's tiles have as many steps as their expert has rows: each XCD has an
+// eighth of each expert's, those with the most rows first (experts of 8 to 2000 rows, 506 on average: no workgroup has
+// more than a quarter above the mean, where an eighth of the experts for each XCD left one with twice the mean).
+template <typename T, Kind KIND, int B, int WQ, int WP>
+__global__ __launch_bounds__(64 * WQ * WP) void linear_experts_backward_kernel(LinArgs a, Plan plan) {
+    extern __shared__ __align__(16) uint8_t smem[];
+    typedef LinTile<T, KIND, B, B, WQ, WP> Product;
+    constexpr int SLAB = Slab<Product::TP>::BYTES;
+    const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), xcd = blockIdx.x & 7;
+    float* const slab = reinterpret_cast<float*>(smem + Product::LDS + wv * SLAB);
+    uint16_t* const order = reinterpret_cast<uint16_t*>(smem + Product::LDS + WQ * WP * SLAB);
+    int turn = 0;
+    if (KIND == DW) {
+        sort_experts(a, Product::TH, reinterpret_cast<int*>(smem), order);
+        const int run = max((plan.nq * plan.np + 7) >> 3, 1);
+        run_pieces<T, KIND, true, B, WQ, WP>(a, plan, Share{}, 0, (plan.whole + 8 * run - 1) / (8 * run) * run, run, turn, order, smem, slab);
+    } else {
+        const Share mine = share_of(plan, tiles_total(a, B) * plan.np, xcd);
+        run_pieces<T, KIND, true, B, WQ, WP>(a, plan, mine, 0, mine.whole, 1, turn, nullptr, smem, slab);
+    }
 }
 
 // The split tiles' sums, added in order of k, and what is done with them: a workgroup per
@@ -850,7 +865,7 @@ Plan plan_forward(int m, int N, int K, int experts, bool grouped, int* shape) {
 }
 
 // How dx and dW (where wanted) are: one kind of tiles for both, and in how many pieces along k those of either. With
-// both, what they take together, and two fifths of the shorter piece for its end; with one, whole rounds.
+// both (of one matrix), what they take together, and two fifths of the shorter piece for its end; with one, whole rounds.
 struct BackPlan {
     Plan x, w;
     int shape;
@@ -939,26 +954,37 @@ hipError_t launch_backward_tiles(const LinArgs& a, const BackPlan& b, hipStream_
     constexpr Shape S = SHAPES[I];
     typedef LinTile<T, DX, S.bq, S.bp, WQ, WP> X;
     typedef LinTile<T, DW, S.bq, S.bp, WQ, WP> W;
-    const size_t lds = std::max(X::LDS, W::LDS) + WQ * WP * Slab<X::TP>::BYTES + (a.offsets != nullptr ? (size_t)a.experts * 2 : 0);
-    auto* const k = a.offsets != nullptr ? linear_backward_kernel<T, true, true, S.bq, WQ, WP>
-                    : b.w_first ? linear_backward_kernel<T, false, true, S.bq, WQ, WP> : linear_backward_kernel<T, false, false, S.bq, WQ, WP>;
+    const size_t lds = std::max(X::LDS, W::LDS) + WQ * WP * Slab<X::TP>::BYTES;
+    auto* const k = b.w_first ? linear_backward_kernel<T, true, S.bq, WQ, WP> : linear_backward_kernel<T, false, S.bq, WQ, WP>;
     hipError_t e = launch_kernel(k, dim3(grid_of(pieces_of(b.x) + pieces_of(b.w), S.slots)), dim3(X::TH), lds, st, a, b.x, b.w);
     if (e == hipSuccess) e = launch_join<T, DX, MOE_ACT_NONE, I, WQ, WP>(a, b.x, st);
     return e != hipSuccess ? e : launch_join<T, DW, MOE_ACT_NONE, I, WQ, WP>(a, b.w, st);
 }
+template <typename T, Kind KIND, int I, int WQ, int WP>
+hipError_t launch_experts_tiles(const LinArgs& a, const Plan& plan, hipStream_t st) {
+    constexpr Shape S = SHAPES[I];
+    typedef LinTile<T, KIND, S.bq, S.bp, WQ, WP> P;
+    const size_t lds = P::LDS + WQ * WP * Slab<P::TP>::BYTES + (KIND == DW ? (size_t)a.experts * 2 : 0);
+    return launch_kernel(linear_experts_backward_kernel<T, KIND, S.bq, WQ, WP>, dim3(grid_of(pieces_of(plan), S.slots)), dim3(P::TH), lds, st, a, plan);
+}
+template <typename T, Kind KIND>
+hipError_t launch_experts(const LinArgs& a, hipStream_t st) {
+    const BackPlan b = plan_backward(a.m, a.N, a.K, a.experts, true, KIND == DX, KIND == DW);
+    const Plan& plan = KIND == DX ? b.x : b.w;
+    return b.shape == 0 ? launch_experts_tiles<T, KIND, 0, 2, 4>(a, plan, st) : launch_experts_tiles<T, KIND, 1, 2, 2>(a, plan, st);
+}
 template <typename T>
 hipError_t launch_backward(const LinArgs& a, float* partial_x, float* partial_w, hipStream_t st) {
-    const bool grouped = a.offsets != nullptr, want_x = a.dx != nullptr && a.m > 0, want_w = a.dw != nullptr;
-    auto launch = [&](bool x, bool w) {
-        BackPlan b = plan_backward(a.m, a.N, a.K, a.experts, grouped, x, w);
-        b.x.partial = partial_x, b.w.partial = partial_w;
-        return b.shape == 0 ? launch_backward_tiles<T, 0, 2, 4>(a, b, st) : launch_backward_tiles<T, 1, 2, 2>(a, b, st);
-    };
-    if (!grouped || !want_x || !want_w) return launch(want_x, want_w);
-    // with offsets each by itself: tiles of dx that run side by side share an expert's weights in their XCD's L2, and
-    // pieces of dW between them part them (16184 rows of 32 experts, 2048 x 1408: 142 and 155 us, together 309)
-    const hipError_t e = launch(true, false);
-    return e != hipSuccess ? e : launch(false, true);
+    const bool want_x = a.dx != nullptr && a.m > 0, want_w = a.dw != nullptr;
+    if (a.offsets != nullptr) {
+        // each by itself: tiles of dx that run side by side share an expert's weights in their XCD's L2, and pieces of dW
+        // between them part them (16184 rows of 32 experts, 2048 x 1408: 142 and 155 us, together 309)
+        const hipError_t e = want_x ? launch_experts<T, DX>(a, st) : hipSuccess;
+        return e == hipSuccess && want_w ? launch_experts<T, DW>(a, st) : e;
+    }
+    BackPlan b = plan_backward(a.m, a.N, a.K, 1, false, want_x, want_w);
+    b.x.partial = partial_x, b.w.partial = partial_w;
+    return b.shape == 0 ? launch_backward_tiles<T, 0, 2, 4>(a, b, st) : launch_backward_tiles<T, 1, 2, 2>(a, b, st);
 }
 
 constexpr int MAX_M = 1 << 24, MAX_N = 1 << 17, MAX_K = 1 << 16, MAX_EXPERTS = 1024;

@@ -1,0 +1,63 @@
+"""GPU: products with a matrix per expert, by the kernels and tiles that the library's own rules choose for them, against
+float64 on the device."""
+import pytest
+import torch
+
+import block_reference as base
+import expert_reference as ref
+import mixture_experts_ffn_gemv_amd as moe
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+BF16, F16 = torch.bfloat16, torch.float16
+NAN = float("nan")
+
+
+def tensors(m, k, n, dtype, seed, n_experts=0):
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    rnd = lambda *s, scale=1.0: (torch.randn(*s, generator=g, device=DEV) * scale).to(dtype)   # noqa: E731
+    shape = (n_experts, n, k) if n_experts else (n, k)
+    return dict(x=rnd(m, k), dy=rnd(m, n), w=rnd(*shape, scale=1.2 / k ** 0.5), bias=rnd(*shape[:-1], scale=0.5), residual=rnd(m, n))
+
+
+def ends(counts):
+    offsets = [0]
+    for v in counts:
+        offsets.append(offsets[-1] + v)
+    return offsets
+
+
+def backward(c, act, offsets, saved, want):
+    f = moe.make_linear(c["w"], c["bias"], act=act)
+    work = torch.full((moe.moe_linear_workspace(f, c["x"].shape[0])[2],), 0xFF, dtype=torch.uint8, device=DEV)
+    out = {"dx": torch.full_like(c["x"], NAN), "dw": torch.full_like(c["w"], NAN), "dbias": torch.full_like(c["bias"], NAN)}
+    out = {name: out[name] for name in want}
+    moe.moe_linear_backward(f, c["x"], c["dy"], saved, work, offsets=offsets, **out)
+    torch.cuda.synchronize()
+    return out
+
+
+def forward(c, act, offsets):
+    f = moe.make_linear(c["w"], c["bias"], act=act)
+    work, saved = (torch.full((v,), 0xFF, dtype=torch.uint8, device=DEV) for v in moe.moe_linear_workspace(f, c["x"].shape[0])[:2])
+    y = torch.full_like(c["dy"], NAN)
+    moe.moe_linear_forward(f, c["x"], y, work, offsets=offsets, residual=c["residual"], saved=saved)
+    torch.cuda.synchronize()
+    return y, saved
+
+
+def check(got, want, what):
+    base.check(got, want[0].cpu(), want[1].cpu(), what)
+
+
+@pytest.mark.parametrize("counts,k,n,dtype,act", [([3, 0, 70, 130, 1], 264, 392, BF16, "silu"), ([1900, 0, 2500, 300, 257], 1040, 1032, F16, "gelu"),
+                                                  ([20] * 90 + [0] * 40, 136, 264, BF16, "none")])
+def test_gradients_of_experts_each_by_itself(counts, k, n, dtype, act):
+    offsets = ends(counts)
+    c = tensors(offsets[-1], k, n, dtype, seed=k, n_experts=len(counts))
+    off = torch.tensor(offsets, dtype=torch.int32, device=DEV)
+    _, saved = forward(c, act, off)
+    together = backward(c, act, off, saved, ("dx", "dw", "dbias"))
+    for name, t in together.items():
+        assert torch.isfinite(t).all()
+        assert torch.equal(backward(c, act, off, saved, (name,))[name], t), name
