@@ -569,10 +569,12 @@ int moe_linear_forward(const moe_linear* f, const void* x, int64_t ldx, const in
 /* Gradients from dy [m, N] (any row stride >= N): dz = dy act'(z); dx = dz W; dW = dz^T x; dbias = the sum of
  * dz over an expert's rows. (The residual's is dy itself.) x, offsets, m, the weights and saved are those of the
  * forward call. dx [m, K] (row stride lddx as ldx), dw [experts, N, K] (16-byte aligned) and dbias [experts, N] are
- * written, not added to; each may be NULL and is then not computed. An expert without rows gets zeros. dz is
- * rounded to the value type, as an operand of the products (in f16, past 65504 it is infinite), but not where m is
- * 8 or less and offsets NULL; dbias is summed in f32 before that. m = 0 writes zeros to dw and dbias. No output may overlap an input. Errors as
- * moe_linear_forward. */
+ * written, not added to; each may be NULL and is then not computed. An expert without rows gets zeros. dbias is summed
+ * in f32. As an operand of the products dz is rounded to the value type (in f16, past 65504 it is infinite). Of an expert
+ * with 64 rows or fewer, and of all where they have 64 or fewer on average (m <= 64 experts), what that leaves is an operand
+ * of its own, so that 2^-16 (f16: 2^-22) of dz is lost; an infinite x or weight makes NaN of the dw or dx that it meets
+ * there. Where m is 8 or less and offsets NULL, dz stays in f32. m = 0 writes zeros to dw and dbias. No output may overlap an
+ * input. Errors as moe_linear_forward. */
 int moe_linear_backward(const moe_linear* f, const void* x, int64_t ldx, const int32_t* offsets, int32_t m,
                         const void* dy, int64_t lddy, const void* saved, size_t saved_bytes, void* dx, int64_t lddx,
                         void* dw, void* dbias, void* work, size_t work_bytes, void* stream);

@@ -10,9 +10,12 @@
 // host knows only how many tiles there may be, and each workgroup finds its own from the offsets, which a
 // wavefront adds up 64 at a time. A workgroup without a tile ends at once.
 //
-// dz is rounded to 16 bits, as an operand of the matrix cores, and nothing else before the results: the
-// gradients have sqrt(2) of the error that their own rounding gives them. (Of eight rows or fewer of one matrix it is not:
-// their backward pass is a kernel of its own.) z is kept in f32.
+// dz is rounded to 16 bits, as an operand of the matrix cores, and nothing else before the results: with many rows the
+// gradients have sqrt(2) of the error that their own rounding gives them. With few rows a handful of large dz may make up
+// most of a gradient, and their errors do not average out: of 1 to 16 rows of 64 to 256 outputs dx and dW were up to twice as
+// far off as their own rounding. There dz is in two parts, its rounding and that of what the first leaves: 2^-16 of dz is
+// lost in bf16, 2^-22 in f16. (Of eight rows or fewer of one matrix dz stays in f32: their backward pass is a kernel of its
+// own.) z is kept in f32.
 //
 // What bounds it: with few rows the weights' bytes (one row of 2304 x 5120 bf16: 8.0 us a call, 23.6 MB; six experts of
 // 5120 x 2304, one row each: 29 us, 4.9 TB/s; 64 experts of 2048 x 1408 f16, 47 rows each: 86 to 92 us, 390 MB); with many
@@ -36,11 +39,26 @@ struct LinArgs {
     const uint16_t *x, *w, *bias, *residual, *dy, *dz;
     float* z;              // [m, padded(N)]
     uint16_t *y, *dx, *dw, *dbias, *dz_out;
+    uint16_t* dz_rest;     // the second part of dz, of matrices with few rows; NULL: dz is exact, or no matrix has few rows
     const int32_t* offsets;   // [experts + 1]; NULL: one matrix for all rows
     int64_t ldx, ldr, ldy, lddy, lddz, lddx;
     int m, N, K, experts, act;
+    int only;              // dx and dW with offsets: of which experts (ALL, MANY, FEW)
     float* partial;        // column sums, [chunk + expert][N]
 };
+// A matrix of so many rows or fewer has dz in two parts, and where the matrices have no more on average, all of them. In dx
+// the parts are the halves of a tile of 128 rows, so that the weights are read once; in dW the halves of a K step. Backward
+// with two parts and with one: 64 rows of 5120 x 2304 32.8 and 32.2 us; of 32 experts of 2048 x 1408, 64 rows 105.9 and 105.5,
+// 1024 rows 121 and 115, 2048 rows 149 and 124. Where they have more on average the others are launched apart (16184 rows,
+// none of them few: 332 and 327), since a test of either in one kernel's K steps, or a loop around them, cost its registers
+// (580 and 642).
+constexpr int TWO_PARTS = 64;
+MOE_DEV __host__ bool all_two(int m, int experts) { return m <= (int64_t)TWO_PARTS * experts; }
+enum Only { ALL, MANY, FEW };   // experts: any, of more rows, of so many or fewer
+// Where the second part of `row` lies, which is one of a matrix's rows from row0 on. (One matrix has room for few rows.)
+MOE_DEV uint16_t* rest_of(const LinArgs& a, int row, int row0) {
+    return a.dz_rest + (a.experts > 1 || a.m <= TWO_PARTS ? row : row - row0) * a.lddz;
+}
 // rows of z and dz are padded to whole chunks of eight values
 MOE_DEV __host__ int padded(int N) { return (N + 7) / 8 * 8; }
 
@@ -75,6 +93,12 @@ MOE_DEV int offset_at(const LinArgs& a, int i) { return min(max(a.offsets[min(i,
 // the same of one i for the whole wavefront
 MOE_DEV int offset_of(const LinArgs& a, int i) { return __builtin_amdgcn_readfirstlane(offset_at(a, i)); }
 
+// an expert's rows, 0 if it is not meant
+MOE_DEV int rows_of(const LinArgs& a, int begin, int end) {
+    const int n = max(end - begin, 0);
+    return a.only == ALL || (n > TWO_PARTS) == (a.only == MANY) ? n : 0;
+}
+
 // A tile among those of `rows`-row tiles of the experts' rows: which expert, where it begins, its
 // rows; np tiles side by side. Every lane of the wavefront calls it.
 struct Slice {
@@ -85,7 +109,7 @@ MOE_DEV int tiles_total(const LinArgs& a, int rows) {
     const int lane = threadIdx.x & 63;
     int n = 0;
 #pragma unroll 4
-    for (int e = lane; e < a.experts; e += 64) n += (max(offset_at(a, e + 1) - offset_at(a, e), 0) + rows - 1) / rows;
+    for (int e = lane; e < a.experts; e += 64) n += (rows_of(a, offset_at(a, e), offset_at(a, e + 1)) + rows - 1) / rows;
     n = wave_inclusive_scan(n);
     return __builtin_amdgcn_readlane(n, 63);
 }
@@ -101,7 +125,7 @@ MOE_DEV bool find_slice(const LinArgs& a, int rows, int np, int tile, Slice& s) 
         for (int u = 0; u < U; ++u) {
             const int e = e0 + 64 * u + lane;
             lo[u] = offset_at(a, e);
-            cnt[u] = e < a.experts ? max(offset_at(a, e + 1) - lo[u], 0) : 0;
+            cnt[u] = e < a.experts ? rows_of(a, lo[u], offset_at(a, e + 1)) : 0;
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
@@ -163,12 +187,12 @@ MOE_DEV uint4 pack8(const float (&v)[8]) {
 
 // Where a tile lies and what it multiplies
 struct Tile {
-    Operand P, Q;
+    Operand P, Q;       // Q's second matrix: the second part of dz, with TWO
     int q0, p0;
     int expert, row0;   // q (DW: k) counts from this row
 };
-// order: of DW with offsets, the experts with the most rows first
-template <Kind KIND, bool GROUPED, int BQ, int BP>
+// order: of DW with offsets, the experts with the most rows first. TWO: dz is in two parts; BQ: rows of q, of either
+template <Kind KIND, bool GROUPED, int BQ, int BP, bool TWO>
 MOE_DEV Tile locate(const LinArgs& a, int tile, int nq, int np, const uint16_t* order) {
     Tile t;
     t.expert = 0, t.row0 = 0;
@@ -191,10 +215,11 @@ MOE_DEV Tile locate(const LinArgs& a, int tile, int nq, int np, const uint16_t* 
     const uint16_t* const w = a.w + (size_t)t.expert * a.N * a.K;
     const uint16_t* const x = a.x + t.row0 * a.ldx;
     const uint16_t* const dz = a.dz + t.row0 * a.lddz;
+    const uint16_t* const rest = TWO ? rest_of(a, t.row0, t.row0) : dz;
     // (dz's rows are padded to whole chunks with zeros)
     if (KIND == FWD) t.P = {w, w, a.K, a.N, a.K}, t.Q = {x, x, a.ldx, rows, a.K};
-    if (KIND == DX) t.P = {w, w, a.K, a.K, a.N}, t.Q = {dz, dz, a.lddz, rows, padded(a.N)};
-    if (KIND == DW) t.P = {x, x, a.ldx, a.K, rows}, t.Q = {dz, dz, a.lddz, padded(a.N), rows};
+    if (KIND == DX) t.P = {w, w, a.K, a.K, a.N}, t.Q = {dz, rest, a.lddz, rows, padded(a.N)};
+    if (KIND == DW) t.P = {x, x, a.ldx, a.K, rows}, t.Q = {dz, rest, a.lddz, padded(a.N), rows};
     // eight q tiles deep, so that the tiles an XCD works on at a time share their operands in its L2
     const int deep = 8 * np, gr = tile / deep, gq = min(8, nq - gr * 8), in = tile - gr * deep;
     t.q0 = (gr * 8 + in % gq) * BQ;
@@ -272,8 +297,9 @@ MOE_DEV void finish(const LinArgs& a, const Tile& t, int qw, int pw, const f32x4
         }
 }
 
-// order[i]: the expert with the i-th most rows (equal ones in their order). counts: room for E of them
-MOE_DEV void sort_experts(const LinArgs& a, int threads, int* counts, uint16_t* order) {
+// order[i]: the expert with the i-th most rows (equal ones in their order). counts: room for E of them. -> how many have
+// more than TWO_PARTS
+MOE_DEV int sort_experts(const LinArgs& a, int threads, int* counts, uint16_t* order) {
     for (int e = threadIdx.x; e < a.experts; e += threads) counts[e] = max(offset_at(a, e + 1) - offset_at(a, e), 0);
     __syncthreads();
     for (int e = threadIdx.x; e < a.experts; e += threads) {
@@ -282,7 +308,13 @@ MOE_DEV void sort_experts(const LinArgs& a, int threads, int* counts, uint16_t* 
         for (int i = 0; i < a.experts; ++i) before += counts[i] > mine || (counts[i] == mine && i < e) ? 1 : 0;
         order[before] = (uint16_t)e;
     }
+    int many = 0;
+    for (int e0 = 0; e0 < a.experts; e0 += 64) {
+        const int e = e0 + (threadIdx.x & 63);
+        many += __popcll(__ballot(e < a.experts && counts[min(e, a.experts - 1)] > TWO_PARTS));
+    }
     __syncthreads();
+    return many;
 }
 
 // The work of one product: the first `whole` tiles, each in one piece, and the `rest` in `splits` pieces along k.
@@ -293,8 +325,26 @@ struct Plan {
     float* partial;      // [split][rest][j][i][thread] of the split tiles' sums, four f32 each
 };
 
-template <typename T, Kind KIND, int BQ, int BP, int WQ, int WP>
-using LinTile = TileProduct<T, p_by_rows(KIND), q_by_rows(KIND), false, BQ, BP, WQ, WP>;
+// TWO: of matrices with dz in two parts
+template <typename T, Kind KIND, int BQ, int BP, int WQ, int WP, bool TWO = false>
+struct LinTile : TileProduct<T, p_by_rows(KIND), q_by_rows(KIND), false, BQ, BP, WQ, WP, TWO && KIND == DX, TWO && KIND == DW> {
+    typedef TileProduct<T, p_by_rows(KIND), q_by_rows(KIND), false, BQ, BP, WQ, WP, TWO && KIND == DX, TWO && KIND == DW> Base;
+    static constexpr bool FOLDED = TWO && KIND == DX;
+    // rows of q in results: a wavefront's 64 rows of dx in two parts are 32
+    static constexpr int BQ_OUT = FOLDED ? BQ / 2 : BQ, TQ_OUT = FOLDED ? Base::TQ / 2 : Base::TQ, NJ_OUT = FOLDED ? Base::NJ / 2 : Base::NJ;
+    static_assert(!FOLDED || Base::TQ == 64, "");
+    static MOE_DEV auto& results(f32x4 (&acc)[Base::NI][Base::NJ], f32x4 (&out)[Base::NI][NJ_OUT]) {
+        if constexpr (FOLDED) {
+#pragma unroll
+            for (int i = 0; i < Base::NI; ++i)
+#pragma unroll
+                for (int j = 0; j < NJ_OUT; ++j) out[i][j] = acc[i][j] + acc[i][j + NJ_OUT];
+            return out;
+        } else {
+            return acc;
+        }
+    }
+};
 
 struct Piece {
     Tile t;
@@ -321,10 +371,10 @@ MOE_DEV void piece_at(const Plan& plan, const Share& s, int place, Piece& x) {
         x.tile = plan.whole + item - x.split * plan.rest;
     }
 }
-template <Kind KIND, bool GROUPED, int BQ, int BP>
+template <Kind KIND, bool GROUPED, int BQ, int BP, bool TWO, int SPAN>
 MOE_DEV void open_piece(const LinArgs& a, const Plan& plan, const uint16_t* order, Piece& x) {
-    x.t = locate<KIND, GROUPED, BQ, BP>(a, x.tile, plan.nq, plan.np, order);
-    const int steps = (x.t.P.k + BK - 1) / BK;
+    x.t = locate<KIND, GROUPED, BQ, BP, TWO>(a, x.tile, plan.nq, plan.np, order);
+    const int steps = (x.t.P.k + SPAN - 1) / SPAN;
     x.kt0 = GROUPED || x.split < 0 ? 0 : (int)((int64_t)x.split * steps / plan.splits);
     x.nk = (GROUPED || x.split < 0 ? steps : (int)((int64_t)(x.split + 1) * steps / plan.splits)) - x.kt0;
 }
@@ -352,7 +402,7 @@ __global__ __launch_bounds__(64 * WQ * WP) void linear_forward_kernel(LinArgs a,
     if (place >= mine.whole + mine.pieces) return;
     Piece now;
     piece_at(plan, mine, place, now);
-    open_piece<FWD, GROUPED, BQ, BP>(a, plan, nullptr, now);
+    open_piece<FWD, GROUPED, BQ, BP, false, Product::KSPAN>(a, plan, nullptr, now);
     Product::begin({now.t.P, now.t.Q, 1, now.t.q0, now.t.p0, now.kt0, now.nk}, smem);
     for (;;) {
         f32x4 acc[NI][NJ];
@@ -362,7 +412,7 @@ __global__ __launch_bounds__(64 * WQ * WP) void linear_forward_kernel(LinArgs a,
         const bool more = place < mine.whole + mine.pieces;
         if (more) {
             piece_at(plan, mine, place, next);
-            open_piece<FWD, GROUPED, BQ, BP>(a, plan, nullptr, next);
+            open_piece<FWD, GROUPED, BQ, BP, false, Product::KSPAN>(a, plan, nullptr, next);
         }
         barrier_lds();   // every wavefront has read the last step
         [&](uint8_t* __restrict buffers, float* __restrict own) {
@@ -377,11 +427,11 @@ __global__ __launch_bounds__(64 * WQ * WP) void linear_forward_kernel(LinArgs a,
 
 // What a workgroup has of one product's pieces in the backward pass. The XCD's pieces, `count` of this product
 // after `base` of another, go to its workgroups forth and back; run: with offsets, dW's tiles side by side on an XCD.
-template <typename T, Kind KIND, bool GROUPED, int B, int WQ, int WP>
+template <typename T, Kind KIND, bool GROUPED, int B, int WQ, int WP, bool TWO>
 MOE_DEV void run_pieces(const LinArgs& a, const Plan& plan, const Share& mine, int base, int count, int run, int& turn,
                         const uint16_t* order, uint8_t* smem, float* slab) {
-    typedef LinTile<T, KIND, B, B, WQ, WP> Product;
-    constexpr int NI = Product::NI, NJ = Product::NJ;
+    typedef LinTile<T, KIND, B, B, WQ, WP, TWO> Product;
+    constexpr int NI = Product::NI, NJ = Product::NJ, NJ_OUT = Product::NJ_OUT;
     const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wq = wv / WP, wp = wv % WP;
     auto take = [&](Piece& x) -> bool {
         const int step = gridDim.x >> 3, at = blockIdx.x >> 3, xcd = blockIdx.x & 7;
@@ -395,7 +445,7 @@ MOE_DEV void run_pieces(const LinArgs& a, const Plan& plan, const Share& mine, i
             } else {
                 piece_at(plan, mine, place, x);
             }
-            open_piece<KIND, GROUPED, B, B>(a, plan, order, x);
+            open_piece<KIND, GROUPED, Product::BQ_OUT, B, TWO, Product::KSPAN>(a, plan, order, x);
             return true;
         }
     };
@@ -406,13 +456,15 @@ MOE_DEV void run_pieces(const LinArgs& a, const Plan& plan, const Share& mine, i
     for (;;) {
         f32x4 acc[NI][NJ];
         Product::template sums<true>({now.t.P, now.t.Q, 1, now.t.q0, now.t.p0, now.kt0, now.nk}, smem, acc);
+        f32x4 out[NI][NJ_OUT];
+        auto& v = Product::results(acc, out);
         Piece next;
         const bool more = take(next);
         barrier_lds();   // every wavefront has read the last step
         [&](uint8_t* __restrict buffers, float* __restrict own) {
             if (more) Product::begin({next.t.P, next.t.Q, 1, next.t.q0, next.t.p0, next.kt0, next.nk}, buffers);
-            if (!GROUPED && now.split >= 0) store_sums<Product::TH>(plan, now, acc);
-            else finish<T, KIND, MOE_ACT_NONE, Product::TP, NI, NJ>(a, now.t, now.t.q0 + wq * Product::TQ, wp * Product::TP, acc, own);
+            if (!GROUPED && now.split >= 0) store_sums<Product::TH>(plan, now, v);
+            else finish<T, KIND, MOE_ACT_NONE, Product::TP, NI, NJ_OUT>(a, now.t, now.t.q0 + wq * Product::TQ_OUT, wp * Product::TP, v, own);
         }(smem, slab);
         if (!more) return;
         now = next;
@@ -421,50 +473,52 @@ MOE_DEV void run_pieces(const LinArgs& a, const Plan& plan, const Share& mine, i
 
 // dx and dW of one matrix in one launch, so that the longer pieces of the one (W_FIRST: dW's) are filled up with the other's:
 // neither fills the CUs evenly by itself.
-template <typename T, bool W_FIRST, int B, int WQ, int WP>
+template <typename T, bool W_FIRST, int B, int WQ, int WP, bool TWO>
 __global__ __launch_bounds__(64 * WQ * WP) void linear_backward_kernel(LinArgs a, Plan px, Plan pw) {
     extern __shared__ __align__(16) uint8_t smem[];
-    typedef LinTile<T, DX, B, B, WQ, WP> ProductX;
-    typedef LinTile<T, DW, B, B, WQ, WP> ProductW;
+    typedef LinTile<T, DX, B, B, WQ, WP, TWO> ProductX;
+    typedef LinTile<T, DW, B, B, WQ, WP, TWO> ProductW;
     constexpr size_t LDS = ProductX::LDS > ProductW::LDS ? ProductX::LDS : ProductW::LDS;
     const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), xcd = blockIdx.x & 7;
     float* const slab = reinterpret_cast<float*>(smem + LDS + wv * Slab<ProductX::TP>::BYTES);
     const Share sx = share_of(px, px.whole, xcd), sw = share_of(pw, pw.whole, xcd);
     const int nx = sx.whole + sx.pieces, nw = sw.whole + sw.pieces;
     int turn = 0;
-    if (W_FIRST) run_pieces<T, DW, false, B, WQ, WP>(a, pw, sw, 0, nw, 1, turn, nullptr, smem, slab);
-    run_pieces<T, DX, false, B, WQ, WP>(a, px, sx, W_FIRST ? nw : 0, nx, 1, turn, nullptr, smem, slab);
-    if (!W_FIRST) run_pieces<T, DW, false, B, WQ, WP>(a, pw, sw, nx, nw, 1, turn, nullptr, smem, slab);
+    if (W_FIRST) run_pieces<T, DW, false, B, WQ, WP, TWO>(a, pw, sw, 0, nw, 1, turn, nullptr, smem, slab);
+    run_pieces<T, DX, false, B, WQ, WP, TWO>(a, px, sx, W_FIRST ? nw : 0, nx, 1, turn, nullptr, smem, slab);
+    if (!W_FIRST) run_pieces<T, DW, false, B, WQ, WP, TWO>(a, pw, sw, nx, nw, 1, turn, nullptr, smem, slab);
 }
 
-// dx or dW of a matrix per expert. dW's tiles have as many steps as their expert has rows: each XCD has an
+// dx or dW of a matrix per expert, of those that have dz in two parts or of the others. dW's tiles have as many steps as their expert has rows: each XCD has an
 // eighth of each expert's, those with the most rows first (experts of 8 to 2000 rows, 506 on average: no workgroup has
 // more than a quarter above the mean, where an eighth of the experts for each XCD left one with twice the mean).
-template <typename T, Kind KIND, int B, int WQ, int WP>
+template <typename T, Kind KIND, int B, int WQ, int WP, bool TWO>
 __global__ __launch_bounds__(64 * WQ * WP) void linear_experts_backward_kernel(LinArgs a, Plan plan) {
     extern __shared__ __align__(16) uint8_t smem[];
-    typedef LinTile<T, KIND, B, B, WQ, WP> Product;
+    typedef LinTile<T, KIND, B, B, WQ, WP, TWO> Product;
     constexpr int SLAB = Slab<Product::TP>::BYTES;
     const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), xcd = blockIdx.x & 7;
     float* const slab = reinterpret_cast<float*>(smem + Product::LDS + wv * SLAB);
-    uint16_t* const order = reinterpret_cast<uint16_t*>(smem + Product::LDS + WQ * WP * SLAB);
+    uint16_t* order = reinterpret_cast<uint16_t*>(smem + Product::LDS + WQ * WP * SLAB);
     int turn = 0;
     if (KIND == DW) {
-        sort_experts(a, Product::TH, reinterpret_cast<int*>(smem), order);
+        const int many = sort_experts(a, Product::TH, reinterpret_cast<int*>(smem), order);
+        if (a.only == FEW) order += many;
+        plan.whole = (a.only == ALL ? a.experts : a.only == MANY ? many : a.experts - many) * plan.nq * plan.np;
         const int run = max((plan.nq * plan.np + 7) >> 3, 1);
-        run_pieces<T, KIND, true, B, WQ, WP>(a, plan, Share{}, 0, (plan.whole + 8 * run - 1) / (8 * run) * run, run, turn, order, smem, slab);
+        run_pieces<T, KIND, true, B, WQ, WP, TWO>(a, plan, Share{}, 0, (plan.whole + 8 * run - 1) / (8 * run) * run, run, turn, order, smem, slab);
     } else {
-        const Share mine = share_of(plan, tiles_total(a, B) * plan.np, xcd);
-        run_pieces<T, KIND, true, B, WQ, WP>(a, plan, mine, 0, mine.whole, 1, turn, nullptr, smem, slab);
+        const Share mine = share_of(plan, tiles_total(a, Product::BQ_OUT) * plan.np, xcd);
+        run_pieces<T, KIND, true, B, WQ, WP, TWO>(a, plan, mine, 0, mine.whole, 1, turn, nullptr, smem, slab);
     }
 }
 
 // The split tiles' sums, added in order of k, and what is done with them: a workgroup per
 // tile and j (16 q of each wavefront)
-template <typename T, Kind KIND, int ACT, int BQ, int BP, int WQ, int WP>
+template <typename T, Kind KIND, int ACT, int BQ, int BP, int WQ, int WP, bool TWO>
 __global__ __launch_bounds__(64 * WQ * WP) void linear_join_kernel(LinArgs a, Plan plan) {
-    typedef LinTile<T, KIND, BQ, BP, WQ, WP> Product;
-    constexpr int TH = Product::TH, NI = Product::NI, NJ = Product::NJ;
+    typedef LinTile<T, KIND, BQ, BP, WQ, WP, TWO> Product;
+    constexpr int TH = Product::TH, NI = Product::NI, NJ = Product::NJ_OUT;
     __shared__ __align__(16) float slab[WQ * WP][Slab<Product::TP>::BYTES / 4];
     const int tid = threadIdx.x, wv = __builtin_amdgcn_readfirstlane(tid >> 6), wq = wv / WP, wp = wv % WP;
     const int r = blockIdx.x / NJ, j = blockIdx.x % NJ;
@@ -478,8 +532,8 @@ __global__ __launch_bounds__(64 * WQ * WP) void linear_join_kernel(LinArgs a, Pl
 #pragma unroll
         for (int i = 0; i < NI; ++i) v[i][0] += f[i * TH];
     }
-    const Tile t = locate<KIND, false, BQ, BP>(a, plan.whole + r, plan.nq, plan.np, nullptr);
-    finish<T, KIND, ACT, Product::TP, NI, 1>(a, t, t.q0 + wq * Product::TQ + 16 * j, wp * Product::TP, v, slab[wv]);
+    const Tile t = locate<KIND, false, Product::BQ_OUT, BP, TWO>(a, plan.whole + r, plan.nq, plan.np, nullptr);
+    finish<T, KIND, ACT, Product::TP, NI, 1>(a, t, t.q0 + wq * Product::TQ_OUT + 16 * j, wp * Product::TP, v, slab[wv]);
 }
 
 // ------------------------------------------------------------------ dz and its column sums
@@ -494,24 +548,26 @@ MOE_DEV __host__ int dz_rows(int m) { return m >= 512 * 64 ? 64 : m >= 512 * 32 
 // at most as many chunks have m rows or fewer
 int dz_chunks(int m) { return std::max({(m + 63) / 64, std::min((m + 15) / 16, 1024), std::min((m + 31) / 32, 1024)}); }
 
-// The experts of rising rows: the ends of 64 experts at a time wait in the lanes
+// The experts of rising rows: 64 experts' rows at a time wait in the lanes
 struct ExpertWalk {
-    int base, end;   // the lane's: where expert base + lane ends
+    int base, begin, end;   // the lane's: where expert base + lane begins and ends
 };
 MOE_DEV ExpertWalk walk_experts(const LinArgs& a, int row) {
     const int lane = threadIdx.x & 63;
     int n = 0;   // experts that end at `row` or before
     for (int e0 = 0; e0 < a.experts; e0 += 64) n += __popcll(__ballot(e0 + lane < a.experts && offset_at(a, e0 + lane + 1) <= row));
-    return {n, offset_at(a, n + lane + 1)};
+    return {n, offset_at(a, n + lane), offset_at(a, n + lane + 1)};
 }
-// the expert of `row` and where it ends (experts that are not there end with the last)
-MOE_DEV int expert_of(const LinArgs& a, ExpertWalk& w, int row, int& end) {
+// the expert of `row` and where it begins and ends (experts that are not there end with the last)
+MOE_DEV int expert_of(const LinArgs& a, ExpertWalk& w, int row, int& begin, int& end) {
     uint64_t past;
     while ((past = __ballot(w.end > row)) == 0 && w.base + 64 < a.experts) {
         w.base += 64;
+        w.begin = offset_at(a, w.base + (threadIdx.x & 63));
         w.end = offset_at(a, w.base + (threadIdx.x & 63) + 1);
     }
     const int l = past != 0 ? __builtin_ctzll(past) : 0;
+    begin = __builtin_amdgcn_readlane(w.begin, l);
     end = __builtin_amdgcn_readlane(w.end, l);
     return min(w.base + l, a.experts - 1);
 }
@@ -525,13 +581,30 @@ __global__ __launch_bounds__(256) void linear_dz_kernel(LinArgs a) {
     const int chunk = dz_rows(a.m), first = blockIdx.x * chunk, n0 = blockIdx.y * DZ_COLS + lane * 8, left = a.N - n0;
     const int last = min(first + chunk, a.offsets != nullptr ? offset_of(a, a.experts) : a.m);
     const bool parts = a.offsets != nullptr && a.partial != nullptr;   // each expert's sums are wanted
-    ExpertWalk walk{0, 0};
-    if (parts && first < last) walk = walk_experts(a, first);
+    const bool two = STORE && a.dz_rest != nullptr;
+    ExpertWalk walk{0, 0, 0};
+    uint64_t few = ~0ull;   // the chunk's rows that have a second part
+    const bool some = two && !all_two(a.m, a.experts);
+    if ((parts || some) && first < last) walk = walk_experts(a, first);
+    if (some) {
+        few = 0;
+        ExpertWalk w = walk;
+        for (int row = first; row < last;) {
+            int begin, end;
+            expert_of(a, w, row, begin, end);
+            const bool all = end - begin <= TWO_PARTS;
+            end = max(min(last, end), row + 1);
+            // (whatever the offsets hold, what is written lies among 64 rows)
+            if (all && row >= begin && end - begin <= TWO_PARTS) few |= (~0ull >> (64 - (end - row))) << (row - first);
+            row = end;
+        }
+    }
+    const int row0 = some ? offset_of(a, 0) : 0;
     int row = first;
     while (row < last) {
-        int e = 0, end = last;
+        int e = 0, begin = 0, end = last;
         if (parts) {
-            e = expert_of(a, walk, row, end);
+            e = expert_of(a, walk, row, begin, end);
             end = max(min(last, end), row + 1);   // (offsets that go back must not hold the loop up)
         }
         float sum[8];
@@ -561,7 +634,17 @@ __global__ __launch_bounds__(256) void linear_dz_kernel(LinArgs a) {
                 if (r < end) {
 #pragma unroll
                     for (int i = 0; i < 8; ++i) sum[i] += d[i];
-                    if (STORE) *reinterpret_cast<uint4*>(a.dz_out + r * a.lddz + n0) = pack8<T>(d);
+                    if (STORE) {
+                        const uint4 q = pack8<T>(d);
+                        *reinterpret_cast<uint4*>(a.dz_out + r * a.lddz + n0) = q;
+                        if (two && (few >> (r - first) & 1)) {
+                            float hi[8];
+                            unpack8<T>(q, hi);   // (what is infinite or NaN leaves nothing)
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) hi[i] = fabsf(hi[i]) <= 3.4e38f ? d[i] - hi[i] : 0.f;
+                            *reinterpret_cast<uint4*>(rest_of(a, r, row0) + n0) = pack8<T>(hi);
+                        }
+                    }
                 }
             }
         }
@@ -866,20 +949,24 @@ Plan plan_forward(int m, int N, int K, int experts, bool grouped, int* shape) {
 
 // How dx and dW (where wanted) are: one kind of tiles for both, and in how many pieces along k those of either. With
 // both (of one matrix), what they take together, and two fifths of the shorter piece for its end; with one, whole rounds.
+// two: of matrices with dz in two parts, whose dx has tiles of one kind.
+constexpr int TWO_SHAPE = 1;
 struct BackPlan {
     Plan x, w;
     int shape;
     bool w_first;
 };
-BackPlan plan_backward(int m, int N, int K, int experts, bool grouped, bool want_x, bool want_w) {
+BackPlan plan_backward(int m, int N, int K, int experts, bool grouped, bool two, bool want_x, bool want_w) {
     BackPlan best{};
     double best_cost = 1e300;
     for (int i = 0; i < BACK_SHAPES; ++i) {
+        if (two && (want_x || !grouped) && i != TWO_SHAPE) continue;
         const Shape& s = SHAPES[i];
+        const Shape half{s.bq / 2, s.bp, s.slots, s.step, s.back, s.ends};
         Extent e[2];
         Plan p[2]{};
         for (int k = 0; k < 2; ++k) {
-            e[k] = extent(k == 0 ? DX : DW, m, N, K, experts, grouped, s);
+            e[k] = extent(k == 0 ? DX : DW, m, N, K, experts, grouped, two && k == 0 ? half : s);
             if (k == 0 ? want_x : want_w) p[k] = {e[k].nq, e[k].np, e[k].tiles, 0, 1, nullptr};
             else e[k].tiles = 0, e[k].likely = 0;
         }
@@ -918,12 +1005,12 @@ BackPlan plan_backward(int m, int N, int K, int experts, bool grouped, bool want
     return best;
 }
 
-template <typename T, Kind KIND, int ACT, int I, int WQ, int WP>
+template <typename T, Kind KIND, int ACT, int I, int WQ, int WP, bool TWO = false>
 hipError_t launch_join(const LinArgs& a, const Plan& plan, hipStream_t st) {
     constexpr Shape S = SHAPES[I];
-    typedef LinTile<T, KIND, S.bq, S.bp, WQ, WP> P;
+    typedef LinTile<T, KIND, S.bq, S.bp, WQ, WP, TWO> P;
     if (plan.rest == 0) return hipSuccess;
-    return launch_kernel(linear_join_kernel<T, KIND, ACT, S.bq, S.bp, WQ, WP>, dim3(plan.rest * P::NJ), dim3(P::TH), 0, st, a, plan);
+    return launch_kernel(linear_join_kernel<T, KIND, ACT, S.bq, S.bp, WQ, WP, TWO>, dim3(plan.rest * P::NJ_OUT), dim3(P::TH), 0, st, a, plan);
 }
 int grid_of(int64_t pieces, int slots) { return (int)std::min<int64_t>(slots, (pieces + 7) / 8 * 8); }
 int64_t pieces_of(const Plan& p) { return p.whole + (int64_t)p.rest * p.splits; }
@@ -949,42 +1036,54 @@ hipError_t launch_forward(const LinArgs& a, float* partial, hipStream_t st) {
     }
 }
 
-template <typename T, int I, int WQ, int WP>
+template <typename T, int I, int WQ, int WP, bool TWO>
 hipError_t launch_backward_tiles(const LinArgs& a, const BackPlan& b, hipStream_t st) {
     constexpr Shape S = SHAPES[I];
-    typedef LinTile<T, DX, S.bq, S.bp, WQ, WP> X;
-    typedef LinTile<T, DW, S.bq, S.bp, WQ, WP> W;
+    typedef LinTile<T, DX, S.bq, S.bp, WQ, WP, TWO> X;
+    typedef LinTile<T, DW, S.bq, S.bp, WQ, WP, TWO> W;
     const size_t lds = std::max(X::LDS, W::LDS) + WQ * WP * Slab<X::TP>::BYTES;
-    auto* const k = b.w_first ? linear_backward_kernel<T, true, S.bq, WQ, WP> : linear_backward_kernel<T, false, S.bq, WQ, WP>;
+    auto* const k = b.w_first ? linear_backward_kernel<T, true, S.bq, WQ, WP, TWO> : linear_backward_kernel<T, false, S.bq, WQ, WP, TWO>;
     hipError_t e = launch_kernel(k, dim3(grid_of(pieces_of(b.x) + pieces_of(b.w), S.slots)), dim3(X::TH), lds, st, a, b.x, b.w);
-    if (e == hipSuccess) e = launch_join<T, DX, MOE_ACT_NONE, I, WQ, WP>(a, b.x, st);
-    return e != hipSuccess ? e : launch_join<T, DW, MOE_ACT_NONE, I, WQ, WP>(a, b.w, st);
+    if (e == hipSuccess) e = launch_join<T, DX, MOE_ACT_NONE, I, WQ, WP, TWO>(a, b.x, st);
+    return e != hipSuccess || TWO ? e : launch_join<T, DW, MOE_ACT_NONE, I, WQ, WP>(a, b.w, st);   // (TWO: a step or two along k)
 }
-template <typename T, Kind KIND, int I, int WQ, int WP>
+template <typename T, Kind KIND, int I, int WQ, int WP, bool TWO>
 hipError_t launch_experts_tiles(const LinArgs& a, const Plan& plan, hipStream_t st) {
     constexpr Shape S = SHAPES[I];
-    typedef LinTile<T, KIND, S.bq, S.bp, WQ, WP> P;
+    typedef LinTile<T, KIND, S.bq, S.bp, WQ, WP, TWO> P;
     const size_t lds = P::LDS + WQ * WP * Slab<P::TP>::BYTES + (KIND == DW ? (size_t)a.experts * 2 : 0);
-    return launch_kernel(linear_experts_backward_kernel<T, KIND, S.bq, WQ, WP>, dim3(grid_of(pieces_of(plan), S.slots)), dim3(P::TH), lds, st, a, plan);
+    return launch_kernel(linear_experts_backward_kernel<T, KIND, S.bq, WQ, WP, TWO>, dim3(grid_of(pieces_of(plan), S.slots)), dim3(P::TH), lds, st, a, plan);
 }
+template <typename T, Kind KIND, bool TWO>
+hipError_t launch_experts_of(LinArgs a, Only only, hipStream_t st) {
+    a.only = only;
+    const BackPlan b = plan_backward(a.m, a.N, a.K, a.experts, true, TWO, KIND == DX, KIND == DW);
+    const Plan& plan = KIND == DX ? b.x : b.w;
+    if constexpr (!(TWO && KIND == DX))
+        if (b.shape == 0) return launch_experts_tiles<T, KIND, 0, 2, 4, TWO>(a, plan, st);
+    return launch_experts_tiles<T, KIND, 1, 2, 2, TWO>(a, plan, st);
+}
+// the experts with dz in two parts, and the others
 template <typename T, Kind KIND>
 hipError_t launch_experts(const LinArgs& a, hipStream_t st) {
-    const BackPlan b = plan_backward(a.m, a.N, a.K, a.experts, true, KIND == DX, KIND == DW);
-    const Plan& plan = KIND == DX ? b.x : b.w;
-    return b.shape == 0 ? launch_experts_tiles<T, KIND, 0, 2, 4>(a, plan, st) : launch_experts_tiles<T, KIND, 1, 2, 2>(a, plan, st);
+    if (a.dz_rest == nullptr) return launch_experts_of<T, KIND, false>(a, ALL, st);
+    if (all_two(a.m, a.experts)) return launch_experts_of<T, KIND, true>(a, ALL, st);
+    const hipError_t e = launch_experts_of<T, KIND, true>(a, FEW, st);
+    return e == hipSuccess ? launch_experts_of<T, KIND, false>(a, MANY, st) : e;
 }
 template <typename T>
 hipError_t launch_backward(const LinArgs& a, float* partial_x, float* partial_w, hipStream_t st) {
-    const bool want_x = a.dx != nullptr && a.m > 0, want_w = a.dw != nullptr;
+    const bool want_x = a.dx != nullptr && a.m > 0, want_w = a.dw != nullptr, two = a.dz_rest != nullptr;
     if (a.offsets != nullptr) {
         // each by itself: tiles of dx that run side by side share an expert's weights in their XCD's L2, and pieces of dW
         // between them part them (16184 rows of 32 experts, 2048 x 1408: 142 and 155 us, together 309)
         const hipError_t e = want_x ? launch_experts<T, DX>(a, st) : hipSuccess;
         return e == hipSuccess && want_w ? launch_experts<T, DW>(a, st) : e;
     }
-    BackPlan b = plan_backward(a.m, a.N, a.K, 1, false, want_x, want_w);
+    BackPlan b = plan_backward(a.m, a.N, a.K, 1, false, two, want_x, want_w);
     b.x.partial = partial_x, b.w.partial = partial_w;
-    return b.shape == 0 ? launch_backward_tiles<T, 0, 2, 4>(a, b, st) : launch_backward_tiles<T, 1, 2, 2>(a, b, st);
+    if (two) return launch_backward_tiles<T, TWO_SHAPE, 2, 2, true>(a, b, st);
+    return b.shape == 0 ? launch_backward_tiles<T, 0, 2, 4, false>(a, b, st) : launch_backward_tiles<T, 1, 2, 2, false>(a, b, st);
 }
 
 constexpr int MAX_M = 1 << 24, MAX_N = 1 << 17, MAX_K = 1 << 16, MAX_EXPERTS = 1024;
@@ -1006,7 +1105,11 @@ size_t forward_bytes(const moe_linear* f, int m) { return partial_bytes(FWD, m, 
 size_t saved_bytes_of(const moe_linear* f, int m) {
     return f->act == MOE_ACT_NONE ? 0 : round_up((size_t)m * padded(f->rows) * 4, 256);
 }
+// of either part of dz; the second is that of 64 rows or fewer, which with a matrix per expert may be any
 size_t dz_bytes(const moe_linear* f, int m) { return round_up((size_t)m * padded(f->rows) * 2, 256); }
+size_t rest_bytes(const moe_linear* f, int m) {
+    return f->act == MOE_ACT_NONE ? 0 : dz_bytes(f, f->experts > 1 ? m : std::min(m, TWO_PARTS));
+}
 size_t sums_bytes(const moe_linear* f, int m) {
     return f->bias == nullptr ? 0 : round_up((size_t)(dz_chunks(m) + f->experts) * f->rows * 4, 256);
 }
@@ -1023,7 +1126,7 @@ size_t few_back_bytes(const moe_linear* f, int m) {
     return f->experts > 1 ? 0 : round_up((size_t)cdiv(f->rows, few_back_rows(f->rows, f->cols)) * std::min(m, FEW_BACK) * f->cols * 4, 256);
 }
 size_t backward_bytes(const moe_linear* f, int m) {
-    return std::max(dz_bytes(f, m) + std::max(sums_bytes(f, m), dx_bytes(f, m) + dw_bytes(f, m)), few_back_bytes(f, m));
+    return std::max(dz_bytes(f, m) + rest_bytes(f, m) + std::max(sums_bytes(f, m), dx_bytes(f, m) + dw_bytes(f, m)), few_back_bytes(f, m));
 }
 
 LinArgs describe(const moe_linear* f, int m, const int32_t* offsets) {
@@ -1171,12 +1274,14 @@ int moe_linear_backward(const moe_linear* f, const void* x, int64_t ldx, const i
         direct = f->act == MOE_ACT_NONE && f->rows % 8 == 0 && rows_ok(dy, lddy, f->rows);
         a.dz_out = reinterpret_cast<uint16_t*>(work);
         a.dz = direct ? a.dy : a.dz_out, a.lddz = direct ? lddy : padded(f->rows);
+        if (f->act != MOE_ACT_NONE && (offsets != nullptr || m <= TWO_PARTS))
+            a.dz_rest = reinterpret_cast<uint16_t*>(reinterpret_cast<uint8_t*>(work) + dz_bytes(f, m));
     }
     a.dw = reinterpret_cast<uint16_t*>(dw);
     a.dbias = reinterpret_cast<uint16_t*>(dbias);
     uint8_t* const w = reinterpret_cast<uint8_t*>(work);
     const hipStream_t st = (hipStream_t)stream;
-    const size_t work_dz = m > 0 ? dz_bytes(f, m) : 0, work_dx = m > 0 ? dx_bytes(f, m) : 0;
+    const size_t work_dz = m > 0 ? dz_bytes(f, m) + rest_bytes(f, m) : 0, work_dx = m > 0 ? dx_bytes(f, m) : 0;
     return status_of(f->dtype == MOE_BF16 ? backward<Bf16>(a, w, work_dz, work_dx, direct, st) : backward<F16>(a, w, work_dz, work_dx, direct, st));
 }
 

@@ -77,15 +77,19 @@ MOE_DEV int lane_here() {
 
 // A BQ x BP tile of the output by WQ x WP wavefronts: acc[i][j] of a lane holds p = 16 i + 4 (lane / 16) +
 // 0..3 and q = 16 j + lane % 16 of its wavefront's part. PR, QR: p or q (not k) is the operand's
-// consecutive index. PAIRED: of every 64 p, the first 32 are P's first matrix, the others the second.
-template <typename T, bool PR, bool QR, bool PAIRED, int BQ, int BP, int WQ, int WP>
+// consecutive index. PAIRED: of every 64 p, the first 32 are P's first matrix, the others the second;
+// Q_PAIRED: the same of q. K_PAIRED (both operands by rows): a K step is 32 k of the operands' first matrices and the same 32
+// of their second.
+template <typename T, bool PR, bool QR, bool PAIRED, int BQ, int BP, int WQ, int WP, bool Q_PAIRED = false, bool K_PAIRED = false>
 struct TileProduct {
     static constexpr int TH = 64 * WQ * WP, TQ = BQ / WQ, TP = BP / WP, NI = TP / 16, NJ = TQ / 16;
     static constexpr int UP = BP * 8 / TH, UQ = BQ * 8 / TH, NW = TH / 64;   // 16-byte units per thread
     static constexpr int P_BYTES = tile_bytes(BP, PR), STEP = P_BYTES + tile_bytes(BQ, QR);
-    static constexpr int PSPAN = PAIRED ? BP / 2 : BP;
+    static constexpr int PSPAN = PAIRED ? BP / 2 : BP, QSPAN = Q_PAIRED ? BQ / 2 : BQ, KSPAN = K_PAIRED ? BK / 2 : BK;
     static constexpr size_t LDS = 2 * STEP;
     static_assert(NW == 8 || NW == 4, "");
+    static_assert(!(PAIRED && PR) && !(Q_PAIRED && QR), "");
+    static_assert(!K_PAIRED || (PR && QR && BP == BQ && BQ == 32 * NW), "");   // (a unit's k are below 32 or none is)
     static_assert((!PR || BP == 128 || BP == 256) && (!QR || BQ == 128 || BQ == 256), "");
 
     // A product's tile and its K steps kt0 .. kt0 + nk - 1; segs matrices one after another along k
@@ -110,29 +114,38 @@ struct TileProduct {
         s.off_p = PR ? (uint32_t)(run_row_wave(BP, NW, wv, slot_p) * w.P.ld + lane % (BP / 8) * 8) * 2
                      : (uint32_t)(first * w.P.ld + chunk * 8) * 2;
         s.off_q = QR ? (uint32_t)(run_row_wave(BQ, NW, wv, slot_q) * w.Q.ld + lane % (BQ / 8) * 8) * 2
-                     : (uint32_t)(row_k * w.Q.ld + chunk * 8) * 2;
+                     : (uint32_t)((Q_PAIRED ? row_k & 31 : row_k) * w.Q.ld + chunk * 8) * 2;
         return s;
     }
 
     // requests step kt's tiles (past the last: zeros)
     static MOE_DEV void stage(const Work& w, const Units& s, int kt, uint8_t* buf) {
         const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-        const int seg_steps = (w.P.k + BK - 1) / BK;
+        const int seg_steps = (w.P.k + KSPAN - 1) / KSPAN;
         const bool past = kt >= w.nk;
         kt += w.kt0;
         const int seg = w.segs == 2 && kt >= seg_steps ? 1 : 0;
-        const int k0 = (kt - seg * seg_steps) * BK;
+        const int k0 = (kt - seg * seg_steps) * KSPAN;
         auto side = [&](uint32_t off, const Operand& o, bool by_rows, int R, int at, int span, bool paired, int U, uint8_t* dst) {
             const uint16_t* base = seg ? o.b : o.a;
-            const int left = min(o.rows - at, span), kleft = min(BK, o.k - k0);
+            const int left = min(o.rows - at, span), kleft = min(KSPAN, o.k - k0);
             const uint32_t beyond = s.chunk * 8 >= kleft ? PAST : 0u;   // a K tail's missing chunks
             if (by_rows) {
                 const auto buffer = buffer_rsrc(base + (size_t)k0 * o.ld + at, past ? 0u : (uint32_t)((kleft - 1) * o.ld + left) * 2);
                 // (with both operands by rows the units' offsets would not fit into the registers beside the sums)
                 if (PR && QR) asm volatile("" : "+v"(off));
+                if constexpr (K_PAIRED) {
+                    const auto other = buffer_rsrc(o.b + (size_t)k0 * o.ld + at, past ? 0u : (uint32_t)((kleft - 1) * o.ld + left) * 2);
 #pragma unroll
-                for (int u = 0; u < U; ++u)
-                    buffer_load_lds16(buffer, dst + (u * NW + wv) * PIECE, off + (uint32_t)(run_row_unit(R, NW, u) * o.ld * 2));
+                    for (int u = 0; u < U; ++u) {
+                        const int row = run_row_unit(R, NW, u);
+                        buffer_load_lds16(row < KSPAN ? buffer : other, dst + (u * NW + wv) * PIECE, off + (uint32_t)(row % KSPAN * o.ld * 2));
+                    }
+                } else {
+#pragma unroll
+                    for (int u = 0; u < U; ++u)
+                        buffer_load_lds16(buffer, dst + (u * NW + wv) * PIECE, off + (uint32_t)(run_row_unit(R, NW, u) * o.ld * 2));
+                }
             } else {
                 const uint32_t bytes = past ? 0u : (uint32_t)((left - 1) * o.ld + kleft) * 2;
                 const size_t corner = (size_t)at * o.ld + k0;
@@ -152,7 +165,7 @@ struct TileProduct {
             }
         };
         side(s.off_p, w.P, PR, BP, w.p0, PSPAN, PAIRED, UP, buf);
-        side(s.off_q, w.Q, QR, BQ, w.q0, BQ, false, UQ, buf + P_BYTES);
+        side(s.off_q, w.Q, QR, BQ, w.q0, QSPAN, Q_PAIRED, UQ, buf + P_BYTES);
     }
 
     // requests the first two steps, into buffers that nobody reads any more
