@@ -297,21 +297,37 @@ MOE_DEV void finish(const LinArgs& a, const Tile& t, int qw, int pw, const f32x4
         }
 }
 
-// order[i]: the expert with the i-th most rows (equal ones in their order). counts: room for E of them. -> how many have
-// more than TWO_PARTS
+// order[i]: the experts with more than TWO_PARTS rows and then the others, so that either are one run; up to 64 of them (a lane
+// each) with the most rows first, equal ones in their order, and more as they come. counts: room for E of them. -> how many
+// have more than TWO_PARTS. Every workgroup does this before its first load. dW with the most rows first (of more than 64, each
+// compared with each) and as they come: 32 experts of 2048 x 1408, 16184 rows 140 and 172 us; 64 of 1024 x 1024, 8000 rows
+// 49 and 53; 128 of 512 x 512, 4000 rows 24.6 and 21.2; 384 of 256 x 256, 2500 rows 29.7 and 20.5; 1024 of 72 x 40, 2500 rows
+// 123 and 13.
 MOE_DEV int sort_experts(const LinArgs& a, int threads, int* counts, uint16_t* order) {
     for (int e = threadIdx.x; e < a.experts; e += threads) counts[e] = max(offset_at(a, e + 1) - offset_at(a, e), 0);
     __syncthreads();
-    for (int e = threadIdx.x; e < a.experts; e += threads) {
-        const int mine = counts[e];
-        int before = 0;
-        for (int i = 0; i < a.experts; ++i) before += counts[i] > mine || (counts[i] == mine && i < e) ? 1 : 0;
-        order[before] = (uint16_t)e;
-    }
+    const int lane = threadIdx.x & 63;
     int many = 0;
-    for (int e0 = 0; e0 < a.experts; e0 += 64) {
-        const int e = e0 + (threadIdx.x & 63);
-        many += __popcll(__ballot(e < a.experts && counts[min(e, a.experts - 1)] > TWO_PARTS));
+    if (a.experts <= 64) {
+        const int mine = lane < a.experts ? counts[lane] : -1;
+        int before = 0;
+        for (int i = 0; i < a.experts; ++i) {
+            const int n = __builtin_amdgcn_readlane(mine, i);
+            before += n > mine || (n == mine && i < lane) ? 1 : 0;
+        }
+        if (threadIdx.x < a.experts) order[before] = (uint16_t)lane;
+        many = __popcll(__ballot(mine > TWO_PARTS));
+    } else {
+        for (int e0 = 0; e0 < a.experts; e0 += 64) many += __popcll(__ballot(e0 + lane < a.experts && counts[min(e0 + lane, a.experts - 1)] > TWO_PARTS));
+        int more = 0;   // experts before these with more than TWO_PARTS
+        for (int e0 = 0; e0 < a.experts; e0 += 64) {
+            const int e = e0 + lane;
+            const bool on = e < a.experts && counts[min(e, a.experts - 1)] > TWO_PARTS;
+            const uint64_t all = __ballot(on);
+            const int of = __popcll(all & ((1ull << lane) - 1));
+            if (e < a.experts && threadIdx.x < 64) order[on ? more + of : many + (e0 - more) + (lane - of)] = (uint16_t)e;
+            more += __popcll(all);
+        }
     }
     __syncthreads();
     return many;

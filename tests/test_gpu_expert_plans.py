@@ -61,3 +61,26 @@ def test_gradients_of_experts_each_by_itself(counts, k, n, dtype, act):
     for name, t in together.items():
         assert torch.isfinite(t).all()
         assert torch.equal(backward(c, act, off, saved, (name,))[name], t), name
+
+
+@pytest.mark.parametrize("n_experts", [64, 65, 200])
+def test_gradients_of_many_experts_with_few_rows_and_many(n_experts):
+    # (those with few rows are launched apart: more rows on average than that, in an order that their number decides)
+    counts = [(200, 3, 0, 65, 64, 128, 1)[e * 5 % 7] for e in range(n_experts)]
+    offsets = ends(counts)
+    used, m = offsets[-1], offsets[-1] + 9
+    assert used > 64 * n_experts
+    c = tensors(m, 72, 136, F16, seed=n_experts, n_experts=n_experts)
+    for name in ("x", "dy", "residual"):
+        c[name][used:] = NAN
+    off = torch.tensor(offsets, dtype=torch.int32, device=DEV)
+    y, saved = forward(c, "silu", off)
+    got = {"y": y, **backward(c, "silu", off, saved, ("dx", "dw", "dbias"))}
+    assert torch.isnan(got["y"][used:]).all() and torch.isnan(got["dx"][used:]).all()
+    for e, (a, b) in enumerate(zip(offsets, offsets[1:])):
+        if a == b:
+            assert not got["dw"][e].any() and not got["dbias"][e].any(), e
+            continue
+        want = ref.linear(c["x"][a:b], c["w"][e], c["bias"][e], c["residual"][a:b], "silu", dy=c["dy"][a:b])
+        for name, t in got.items():
+            check(t[a:b] if name in ("y", "dx") else t[e], want[name], f"{name} of expert {e}")
