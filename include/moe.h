@@ -506,7 +506,8 @@ int moe_sort_workspace(int32_t m, int32_t topk, int32_t n_experts, size_t* bytes
  *   pick_of [m * topk]     the pick (token * topk + j) of each sorted row, -1 behind the last; may be NULL
  *   offsets [n_experts + 1]  the first row of each expert, and the number of rows
  * All device memory, row-major, 4-byte aligned; work 256-byte aligned. An expert may be picked twice by a
- * token. m = 0 writes zeros to offsets. MOE_EINVAL, MOE_ESCRATCH, MOE_EHIP. */
+ * token. No output overlaps idx (MOE_EINVAL), the workspace or another output. m = 0 writes zeros to offsets.
+ * MOE_EINVAL, MOE_ESCRATCH, MOE_EHIP. */
 int moe_sort(const int32_t* idx, int32_t m, int32_t topk, int32_t n_experts, int32_t* row_of, int32_t* pick_of,
              int32_t* offsets, void* work, size_t work_bytes, void* stream);
 

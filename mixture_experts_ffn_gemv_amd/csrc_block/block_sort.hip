@@ -304,6 +304,11 @@ int check_move(int32_t dtype, int32_t dim, int32_t m, int32_t topk, int32_t rows
     return row_of != nullptr && aligned_to(row_of, 4) ? MOE_OK : MOE_EINVAL;
 }
 
+bool overlap(const void* p, size_t bytes, const void* q, size_t other) {
+    const uintptr_t a = (uintptr_t)p, b = (uintptr_t)q;
+    return p != nullptr && q != nullptr && a < b + other && b < a + bytes;
+}
+
 // Whether results are written past the L2s, which hold 32 MB: six rows each of 8192 x 5120 bf16 there and back 202 us so
 // and 233 through them, of 1999 44.3 and 45.0, and no difference for fewer.
 bool past_l2(int64_t rows, int dim, size_t size) { return (size_t)rows * dim * size > (32u << 20); }
@@ -416,6 +421,10 @@ int moe_sort(const int32_t* idx, int32_t m, int32_t topk, int32_t n_experts, int
     if (m > 0 && (idx == nullptr || row_of == nullptr)) return MOE_EINVAL;
     if (need > 0 && (work == nullptr || !aligned_to(work, 256))) return MOE_EINVAL;
     if (work_bytes < need) return MOE_ESCRATCH;
+    // (a workgroup reads picks of which others write the rows)
+    const size_t picks = (size_t)m * topk * 4;
+    if (overlap(idx, picks, row_of, picks) || overlap(idx, picks, pick_of, picks) || overlap(idx, picks, offsets, ((size_t)n_experts + 1) * 4))
+        return MOE_EINVAL;
     SortArgs a{};
     a.idx = idx, a.row_of = row_of, a.pick_of = pick_of, a.offsets = offsets, a.counts = reinterpret_cast<int32_t*>(work);
     a.n = m * topk, a.experts = n_experts;
