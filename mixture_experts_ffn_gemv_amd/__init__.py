@@ -421,6 +421,14 @@ _DTYPES = {torch.bfloat16: MOE_BF16, torch.float16: MOE_F16, torch.float32: MOE_
 _ACTS = {"silu": MOE_ACT_SILU, "gelu": MOE_ACT_GELU}
 
 
+_MOST = 2 ** 31 - 1   # sizes are 32 bits in C, and ctypes would cut off what is above them
+
+
+def _small(where, *sizes):
+    if max(sizes) > _MOST:
+        raise MoeError(MOE_EINVAL, where)
+
+
 def _dtype(t, where):
     if t not in _DTYPES:
         raise MoeError(MOE_EINVAL, where)
@@ -438,7 +446,7 @@ def _rows(t, m, dim, dtype, where):
     """A device matrix [m, dim] with consecutive values in each row -> (pointer, row stride); None -> (None, 0)."""
     if t is None:
         return None, 0
-    if t.shape != (m, dim) or t.dtype is not dtype or not t.is_cuda:
+    if t.shape != (m, dim) or t.dtype is not dtype or not t.is_cuda or m > _MOST:
         raise MoeError(MOE_EINVAL, where)
     ld, one = t.stride()
     if one != 1 and dim != 1:
@@ -470,6 +478,7 @@ def make_ffn(w_gate, w_up, w_down, act="silu", limit=0.0):
     if w_gate.dim() != 2:
         raise MoeError(MOE_EINVAL, "make_ffn")
     inter, dim = w_gate.shape
+    _small("make_ffn", inter, dim)
     dt = w_gate.dtype
     f = moe_ffn(dim, inter, _dtype(dt, "make_ffn"), _act(act, "make_ffn"), limit,
                 _whole(w_gate, (inter, dim), dt, "make_ffn"), _whole(w_up, (inter, dim), dt, "make_ffn"),
@@ -480,6 +489,7 @@ def make_ffn(w_gate, w_up, w_down, act="silu", limit=0.0):
 
 def moe_ffn_workspace(f, m):
     """-> (forward, saved, backward) bytes for m rows."""
+    _small("moe_ffn_workspace", m)
     out = [ctypes.c_size_t() for _ in range(3)]
     _check(lib().moe_ffn_workspace(ctypes.byref(f), m, *[ctypes.byref(o) for o in out]), "moe_ffn_workspace")
     return tuple(o.value for o in out)
@@ -504,6 +514,7 @@ def moe_ffn_backward(f, x, dy, saved, work, dx=None, dw_gate=None, dw_up=None, d
 
 def make_norm(dim, dtype, w_post=None, w_pre=None, eps=1e-6, res_scale=1.0):
     """Describe the norms around a block: w_post and w_pre [dim] or None (kept alive by the result)."""
+    _small("make_norm", dim)
     f = moe_norm(dim, _dtype(dtype, "make_norm"), eps, res_scale, _whole(w_post, (dim,), dtype, "make_norm"),
                  _whole(w_pre, (dim,), dtype, "make_norm"))
     f.torch_dtype, f.tensors = dtype, (w_post, w_pre)
@@ -512,6 +523,7 @@ def make_norm(dim, dtype, w_post=None, w_pre=None, eps=1e-6, res_scale=1.0):
 
 def moe_norm_workspace(f, m):
     """-> workspace bytes of moe_norm_backward for m rows."""
+    _small("moe_norm_workspace", m)
     out = ctypes.c_size_t()
     _check(lib().moe_norm_workspace(ctypes.byref(f), m, ctypes.byref(out)), "moe_norm_workspace")
     return out.value
@@ -558,6 +570,7 @@ def make_w4(codes, scales, zeros=None, group=None):
     if codes.dim() != 2 or scales.dim() != 2 or not scales.shape[1]:
         raise MoeError(MOE_EINVAL, me)
     rows, cols = codes.shape[0], 2 * codes.shape[1]
+    _small(me, rows, cols)
     group = cols // scales.shape[1] if group is None else group
     if group <= 0 or cols % group:
         raise MoeError(MOE_EINVAL, me)
@@ -605,7 +618,7 @@ def _any_rows(t, dtype, where):
         raise MoeError(MOE_EINVAL, where)
     m, dim = shape
     ld, one = t.stride()
-    if one != 1 and dim != 1:
+    if (one != 1 and dim != 1) or m > _MOST or dim > _MOST:
         raise MoeError(MOE_EINVAL, where)
     return t.data_ptr(), ld if m > 1 else dim, m, dim   # (one row: its stride leads nowhere)
 
@@ -615,11 +628,13 @@ def _picks(t, where):
     shape = t.shape
     if t.dtype is not torch.int32 or len(shape) != 2 or not t.is_cuda or not t.is_contiguous():
         raise MoeError(MOE_EINVAL, where)
+    _small(where, *shape)
     return t.data_ptr(), shape[0], shape[1]
 
 
 def moe_sort_workspace(m, topk, n_experts):
     """-> the bytes that moe_sort works in."""
+    _small("moe_sort_workspace", m, topk, n_experts)
     size = ctypes.c_size_t()
     _check(lib().moe_sort_workspace(m, topk, n_experts, ctypes.byref(size)), "moe_sort_workspace")
     return size.value
@@ -630,6 +645,7 @@ def moe_sort(idx, n_experts, row_of, pick_of, offsets, work, stream=None):
     offsets [n_experts + 1], all int32."""
     me = "moe_sort"
     picks, m, topk = _picks(idx, me)
+    _small(me, n_experts)
     return _check(lib().moe_sort(
         picks, m, topk, n_experts, _whole(row_of, (m, topk), torch.int32, me), _whole(pick_of, (m * topk,), torch.int32, me),
         _whole(offsets, (n_experts + 1,), torch.int32, me), *_bytes(work, me),
@@ -693,6 +709,7 @@ def make_linear(w, bias=None, act="none"):
         raise MoeError(MOE_EINVAL, me)
     rows, cols = w.shape[-2:]
     experts, dt = w.shape[0] if w.dim() == 3 else 1, w.dtype
+    _small(me, rows, cols, experts)
     act = _LINEAR_ACTS.get(act, act)
     if act not in (MOE_ACT_SILU, MOE_ACT_GELU, MOE_ACT_NONE):
         raise MoeError(MOE_EINVAL, me)
@@ -703,6 +720,7 @@ def make_linear(w, bias=None, act="none"):
 
 def moe_linear_workspace(f, m):
     """-> (forward, saved, backward) bytes for m rows."""
+    _small("moe_linear_workspace", m)
     out = [ctypes.c_size_t() for _ in range(3)]
     _check(lib().moe_linear_workspace(ctypes.byref(f), m, *[ctypes.byref(o) for o in out]), "moe_linear_workspace")
     return tuple(o.value for o in out)
@@ -731,6 +749,7 @@ def moe_linear_backward(f, x, dy, saved, work, offsets=None, dx=None, dw=None, d
 
 def make_dropout(dim, dtype, p):
     """Describe dropout of rows of dim values of that type with probability p."""
+    _small("make_dropout", dim)
     f = moe_dropout(dim, _dtype(dtype, "make_dropout"), p)
     f.torch_dtype = dtype
     return f
