@@ -65,6 +65,7 @@ def test_gradients_of_some_rows_are_rounded_once(m, k, n, dtype, act):
     ([0, 1, 0, 8, 2], 3, 520, 100, F16, "gelu"),
     ([64, 65, 3, 0, 200, 1], 5, 136, 264, BF16, "gelu"),      # experts with few rows beside others with many
     ([2, 0, 1] * 60, 0, 72, 130, F16, "silu"),                # several experts in every chunk of rows, more than a wavefront's lanes
+    ([60, 0, 33, 64, 1, 90, 32, 7] * 3, 2, 1032, 2056, F16, "silu"),   # dW by the largest tiles
     ([300, 0, 17, 31, 64, 900], 11, 392, 520, BF16, "silu")])
 def test_gradients_of_experts_with_few_rows_are_rounded_once(counts, behind, k, n, dtype, act):
     offsets = [0]

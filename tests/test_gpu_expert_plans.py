@@ -84,3 +84,64 @@ def test_gradients_of_many_experts_with_few_rows_and_many(n_experts):
         want = ref.linear(c["x"][a:b], c["w"][e], c["bias"][e], c["residual"][a:b], "silu", dy=c["dy"][a:b])
         for name, t in got.items():
             check(t[a:b] if name in ("y", "dx") else t[e], want[name], f"{name} of expert {e}")
+
+
+def experts_against_float64(counts, behind, k, n, dtype, act, seed):
+    offsets = ends(counts)
+    used, m = offsets[-1], offsets[-1] + behind
+    c = tensors(m, k, n, dtype, seed=seed, n_experts=len(counts))
+    for name in ("x", "dy", "residual"):
+        c[name][used:] = NAN   # rows behind the last are not read
+    off = torch.tensor(offsets, dtype=torch.int32, device=DEV)
+    y, saved = forward(c, act, off)
+    got = {"y": y, **backward(c, act, off, saved, ("dx", "dw", "dbias"))}
+    assert torch.isnan(got["y"][used:]).all() and torch.isnan(got["dx"][used:]).all()
+    idle = [e for e, v in enumerate(counts) if v == 0]
+    assert not got["dw"][idle].any() and not got["dbias"][idle].any()
+    for e, (a, b) in enumerate(zip(offsets, offsets[1:])):
+        if a == b:
+            continue
+        want = ref.linear(c["x"][a:b], c["w"][e], c["bias"][e], c["residual"][a:b], act, dy=c["dy"][a:b])
+        for name, t in got.items():
+            check(t[a:b] if name in ("y", "dx") else t[e], want[name], f"{name} of expert {e}")
+
+
+def picked(n_experts, at):
+    counts = [0] * n_experts
+    for e in at:
+        counts[e] += 1
+    return counts
+
+
+@pytest.mark.parametrize("counts,behind,k,n,dtype,act", [
+    # so few rows that each goes by the weights of its expert: experts past those whose offsets are read at a time (64 and 256),
+    # rows of x of many steps, outputs that sixteen do not divide
+    (picked(300, (3, 70, 130, 256, 299, 299)), 0, 5128, 1030, BF16, "silu"),
+    (picked(384, (0, 63, 64, 255, 320, 383)), 0, 5120, 2304, BF16, "none"),
+    (picked(280, (279, 257, 257, 5)), 1, 2568, 1000, F16, "gelu"),
+    # an expert with more rows than a workgroup has room for
+    (picked(300, (290,) * 5 + (17, 100, 299)), 0, 2056, 2309, F16, "silu"),
+    ([9, 0, 1, 0, 2, 0, 0, 0], 0, 2056, 1033, BF16, "gelu"),
+    ([0, 1, 11, 0, 0, 0, 0, 1, 0, 0], 1, 5120, 1030, F16, "none")])
+def test_few_rows_of_many_experts(counts, behind, k, n, dtype, act):
+    experts_against_float64(counts, behind, k, n, dtype, act, seed=k + n)
+
+
+@pytest.mark.parametrize("counts,k,n,dtype,act", [
+    # the largest tiles in y, dx and dW, none of them whole
+    ([700, 0, 33, 1500, 64, 65, 900, 257] * 4, 2056, 1544, BF16, "silu"),
+    ([1801, 300, 3000, 0, 1, 2000, 800, 400, 600, 700, 398, 0], 2568, 2309, F16, "gelu")])
+def test_experts_by_the_largest_tiles(counts, k, n, dtype, act):
+    experts_against_float64(counts, 5, k, n, dtype, act, seed=k)
+
+
+def test_one_matrix_by_the_largest_tiles():
+    m, k, n = 5000, 2600, 2309   # 200 of them in y, 220 in dx, 110 in dW, none of the last ones whole
+    c = tensors(m, k, n, BF16, seed=5)
+    want = ref.linear(c["x"], c["w"], c["bias"], c["residual"], "silu", dy=c["dy"])
+    y, saved = forward(c, "silu", None)
+    got = {"y": y, **backward(c, "silu", None, saved, ("dx", "dw", "dbias"))}
+    for name, t in got.items():
+        check(t, want[name], name)
+    for name in ("dx", "dw", "dbias"):   # each by itself: against the same reference, since it may be cut up otherwise
+        check(backward(c, "silu", None, saved, (name,))[name], want[name], f"{name} by itself")
