@@ -43,18 +43,17 @@ struct LinArgs {
     const int32_t* offsets;   // [experts + 1]; NULL: one matrix for all rows
     int64_t ldx, ldr, ldy, lddy, lddz, lddx;
     int m, N, K, experts, act;
-    int only;              // dx and dW with offsets: of which experts (ALL, MANY, FEW)
     float* partial;        // column sums, [chunk + expert][N]
 };
 // A matrix of so many rows or fewer has dz in two parts, and where the matrices have no more on average, all of them. In dx
 // the parts are the halves of a tile of 128 rows, so that the weights are read once; in dW the halves of a K step. Backward
 // with two parts and with one: 64 rows of 5120 x 2304 32.8 and 32.2 us; of 32 experts of 2048 x 1408, 64 rows 105.9 and 105.5,
-// 1024 rows 121 and 115, 2048 rows 149 and 124. Where they have more on average the others are launched apart (16184 rows,
-// none of them few: 332 and 327), since a test of either in one kernel's K steps, or a loop around them, cost its registers
-// (580 and 642).
+// 1024 rows 121 and 115, 2048 rows 149 and 124. Where they have more on average the experts with few rows are the last tiles
+// of the same launch, by code of their own (16184 rows, none of them few: 327 and 326), since a test in each K step, or a
+// loop around a tile's, cost registers (486 and 642).
 constexpr int TWO_PARTS = 64;
 MOE_DEV __host__ bool all_two(int m, int experts) { return m <= (int64_t)TWO_PARTS * experts; }
-enum Only { ALL, MANY, FEW };   // experts: any, of more rows, of so many or fewer
+enum Only { ALL, MANY, FEW };   // of which experts: any, with more rows, with so many or fewer
 // Where the second part of `row` lies, which is one of a matrix's rows from row0 on. (One matrix has room for few rows.)
 MOE_DEV uint16_t* rest_of(const LinArgs& a, int row, int row0) {
     return a.dz_rest + (a.experts > 1 || a.m <= TWO_PARTS ? row : row - row0) * a.lddz;
@@ -94,9 +93,10 @@ MOE_DEV int offset_at(const LinArgs& a, int i) { return min(max(a.offsets[min(i,
 MOE_DEV int offset_of(const LinArgs& a, int i) { return __builtin_amdgcn_readfirstlane(offset_at(a, i)); }
 
 // an expert's rows, 0 if it is not meant
-MOE_DEV int rows_of(const LinArgs& a, int begin, int end) {
+template <Only ONLY>
+MOE_DEV int rows_of(int begin, int end) {
     const int n = max(end - begin, 0);
-    return a.only == ALL || (n > TWO_PARTS) == (a.only == MANY) ? n : 0;
+    return ONLY == ALL || (n > TWO_PARTS) == (ONLY == MANY) ? n : 0;
 }
 
 // A tile among those of `rows`-row tiles of the experts' rows: which expert, where it begins, its
@@ -105,15 +105,17 @@ struct Slice {
     int expert, row0, rows;    // the expert's rows
     int tile;                  // which of the expert's tiles (q and p)
 };
+template <Only ONLY>
 MOE_DEV int tiles_total(const LinArgs& a, int rows) {
     const int lane = threadIdx.x & 63;
     int n = 0;
 #pragma unroll 4
-    for (int e = lane; e < a.experts; e += 64) n += (rows_of(a, offset_at(a, e), offset_at(a, e + 1)) + rows - 1) / rows;
+    for (int e = lane; e < a.experts; e += 64) n += (rows_of<ONLY>(offset_at(a, e), offset_at(a, e + 1)) + rows - 1) / rows;
     n = wave_inclusive_scan(n);
     return __builtin_amdgcn_readlane(n, 63);
 }
 // false: there are not so many
+template <Only ONLY>
 MOE_DEV bool find_slice(const LinArgs& a, int rows, int np, int tile, Slice& s) {
     const int lane = threadIdx.x & 63;
     constexpr int U = 4;   // 256 experts' offsets are requested at a time
@@ -125,7 +127,7 @@ MOE_DEV bool find_slice(const LinArgs& a, int rows, int np, int tile, Slice& s) 
         for (int u = 0; u < U; ++u) {
             const int e = e0 + 64 * u + lane;
             lo[u] = offset_at(a, e);
-            cnt[u] = e < a.experts ? rows_of(a, lo[u], offset_at(a, e + 1)) : 0;
+            cnt[u] = e < a.experts ? rows_of<ONLY>(lo[u], offset_at(a, e + 1)) : 0;
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
@@ -192,7 +194,7 @@ struct Tile {
     int expert, row0;   // q (DW: k) counts from this row
 };
 // order: of DW with offsets, the experts with the most rows first. TWO: dz is in two parts; BQ: rows of q, of either
-template <Kind KIND, bool GROUPED, int BQ, int BP, bool TWO>
+template <Kind KIND, bool GROUPED, int BQ, int BP, bool TWO, Only ONLY>
 MOE_DEV Tile locate(const LinArgs& a, int tile, int nq, int np, const uint16_t* order) {
     Tile t;
     t.expert = 0, t.row0 = 0;
@@ -207,7 +209,7 @@ MOE_DEV Tile locate(const LinArgs& a, int tile, int nq, int np, const uint16_t* 
             rows = max(offset_of(a, t.expert + 1) - t.row0, 0);
         } else {
             Slice s;
-            find_slice(a, BQ, np, tile, s);
+            find_slice<ONLY>(a, BQ, np, tile, s);
             t.expert = s.expert, t.row0 = s.row0, rows = s.rows, tile = s.tile;
             nq = (rows + BQ - 1) / BQ;
         }
@@ -346,15 +348,15 @@ template <typename T, Kind KIND, int BQ, int BP, int WQ, int WP, bool TWO = fals
 struct LinTile : TileProduct<T, p_by_rows(KIND), q_by_rows(KIND), false, BQ, BP, WQ, WP, TWO && KIND == DX, TWO && KIND == DW> {
     typedef TileProduct<T, p_by_rows(KIND), q_by_rows(KIND), false, BQ, BP, WQ, WP, TWO && KIND == DX, TWO && KIND == DW> Base;
     static constexpr bool FOLDED = TWO && KIND == DX;
-    // rows of q in results: a wavefront's 64 rows of dx in two parts are 32
+    // rows of q in results: of a wavefront's 64 rows of dx the first 32 are of the first part, the others of the second
     static constexpr int BQ_OUT = FOLDED ? BQ / 2 : BQ, TQ_OUT = FOLDED ? Base::TQ / 2 : Base::TQ, NJ_OUT = FOLDED ? Base::NJ / 2 : Base::NJ;
-    static_assert(!FOLDED || Base::TQ == 64, "");
+    static_assert(!FOLDED || Base::TQ % 64 == 0, "");
     static MOE_DEV auto& results(f32x4 (&acc)[Base::NI][Base::NJ], f32x4 (&out)[Base::NI][NJ_OUT]) {
         if constexpr (FOLDED) {
 #pragma unroll
             for (int i = 0; i < Base::NI; ++i)
 #pragma unroll
-                for (int j = 0; j < NJ_OUT; ++j) out[i][j] = acc[i][j] + acc[i][j + NJ_OUT];
+                for (int j = 0; j < NJ_OUT; ++j) out[i][j] = acc[i][j / 2 * 4 + j % 2] + acc[i][j / 2 * 4 + j % 2 + 2];
             return out;
         } else {
             return acc;
@@ -387,9 +389,9 @@ MOE_DEV void piece_at(const Plan& plan, const Share& s, int place, Piece& x) {
         x.tile = plan.whole + item - x.split * plan.rest;
     }
 }
-template <Kind KIND, bool GROUPED, int BQ, int BP, bool TWO, int SPAN>
+template <Kind KIND, bool GROUPED, int BQ, int BP, bool TWO, int SPAN, Only ONLY>
 MOE_DEV void open_piece(const LinArgs& a, const Plan& plan, const uint16_t* order, Piece& x) {
-    x.t = locate<KIND, GROUPED, BQ, BP, TWO>(a, x.tile, plan.nq, plan.np, order);
+    x.t = locate<KIND, GROUPED, BQ, BP, TWO, ONLY>(a, x.tile, plan.nq, plan.np, order);
     const int steps = (x.t.P.k + SPAN - 1) / SPAN;
     x.kt0 = GROUPED || x.split < 0 ? 0 : (int)((int64_t)x.split * steps / plan.splits);
     x.nk = (GROUPED || x.split < 0 ? steps : (int)((int64_t)(x.split + 1) * steps / plan.splits)) - x.kt0;
@@ -413,12 +415,12 @@ __global__ __launch_bounds__(64 * WQ * WP) void linear_forward_kernel(LinArgs a,
     constexpr int NI = Product::NI, NJ = Product::NJ;
     const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wq = wv / WP, wp = wv % WP;
     float* const slab = reinterpret_cast<float*>(smem + Product::LDS + wv * Slab<Product::TP>::BYTES);
-    const Share mine = share_of(plan, GROUPED ? tiles_total(a, BQ) * plan.np : plan.whole, blockIdx.x & 7);
+    const Share mine = share_of(plan, GROUPED ? tiles_total<ALL>(a, BQ) * plan.np : plan.whole, blockIdx.x & 7);
     int place = blockIdx.x >> 3;
     if (place >= mine.whole + mine.pieces) return;
     Piece now;
     piece_at(plan, mine, place, now);
-    open_piece<FWD, GROUPED, BQ, BP, false, Product::KSPAN>(a, plan, nullptr, now);
+    open_piece<FWD, GROUPED, BQ, BP, false, Product::KSPAN, ALL>(a, plan, nullptr, now);
     Product::begin({now.t.P, now.t.Q, 1, now.t.q0, now.t.p0, now.kt0, now.nk}, smem);
     for (;;) {
         f32x4 acc[NI][NJ];
@@ -428,7 +430,7 @@ __global__ __launch_bounds__(64 * WQ * WP) void linear_forward_kernel(LinArgs a,
         const bool more = place < mine.whole + mine.pieces;
         if (more) {
             piece_at(plan, mine, place, next);
-            open_piece<FWD, GROUPED, BQ, BP, false, Product::KSPAN>(a, plan, nullptr, next);
+            open_piece<FWD, GROUPED, BQ, BP, false, Product::KSPAN, ALL>(a, plan, nullptr, next);
         }
         barrier_lds();   // every wavefront has read the last step
         [&](uint8_t* __restrict buffers, float* __restrict own) {
@@ -443,7 +445,7 @@ __global__ __launch_bounds__(64 * WQ * WP) void linear_forward_kernel(LinArgs a,
 
 // What a workgroup has of one product's pieces in the backward pass. The XCD's pieces, `count` of this product
 // after `base` of another, go to its workgroups forth and back; run: with offsets, dW's tiles side by side on an XCD.
-template <typename T, Kind KIND, bool GROUPED, int B, int WQ, int WP, bool TWO>
+template <typename T, Kind KIND, bool GROUPED, int B, int WQ, int WP, bool TWO, Only ONLY>
 MOE_DEV void run_pieces(const LinArgs& a, const Plan& plan, const Share& mine, int base, int count, int run, int& turn,
                         const uint16_t* order, uint8_t* smem, float* slab) {
     typedef LinTile<T, KIND, B, B, WQ, WP, TWO> Product;
@@ -461,7 +463,7 @@ MOE_DEV void run_pieces(const LinArgs& a, const Plan& plan, const Share& mine, i
             } else {
                 piece_at(plan, mine, place, x);
             }
-            open_piece<KIND, GROUPED, Product::BQ_OUT, B, TWO, Product::KSPAN>(a, plan, order, x);
+            open_piece<KIND, GROUPED, Product::BQ_OUT, B, TWO, Product::KSPAN, ONLY>(a, plan, order, x);
             return true;
         }
     };
@@ -500,32 +502,45 @@ __global__ __launch_bounds__(64 * WQ * WP) void linear_backward_kernel(LinArgs a
     const Share sx = share_of(px, px.whole, xcd), sw = share_of(pw, pw.whole, xcd);
     const int nx = sx.whole + sx.pieces, nw = sw.whole + sw.pieces;
     int turn = 0;
-    if (W_FIRST) run_pieces<T, DW, false, B, WQ, WP, TWO>(a, pw, sw, 0, nw, 1, turn, nullptr, smem, slab);
-    run_pieces<T, DX, false, B, WQ, WP, TWO>(a, px, sx, W_FIRST ? nw : 0, nx, 1, turn, nullptr, smem, slab);
-    if (!W_FIRST) run_pieces<T, DW, false, B, WQ, WP, TWO>(a, pw, sw, nx, nw, 1, turn, nullptr, smem, slab);
+    if (W_FIRST) run_pieces<T, DW, false, B, WQ, WP, TWO, ALL>(a, pw, sw, 0, nw, 1, turn, nullptr, smem, slab);
+    run_pieces<T, DX, false, B, WQ, WP, TWO, ALL>(a, px, sx, W_FIRST ? nw : 0, nx, 1, turn, nullptr, smem, slab);
+    if (!W_FIRST) run_pieces<T, DW, false, B, WQ, WP, TWO, ALL>(a, pw, sw, nx, nw, 1, turn, nullptr, smem, slab);
 }
 
-// dx or dW of a matrix per expert, of those that have dz in two parts or of the others. dW's tiles have as many steps as their expert has rows: each XCD has an
-// eighth of each expert's, those with the most rows first (experts of 8 to 2000 rows, 506 on average: no workgroup has
-// more than a quarter above the mean, where an eighth of the experts for each XCD left one with twice the mean).
-template <typename T, Kind KIND, int B, int WQ, int WP, bool TWO>
+// dx or dW of a matrix per expert, with dz in one part (PARTS 1), in two (2), or in two of those with few rows (BOTH). dW's
+// tiles have as many steps as their expert has rows: each XCD has an eighth of each expert's, those with the most rows
+// first (experts of 8 to 2000 rows, 506 on average: no workgroup has more than a quarter above the mean, where an eighth of the
+// experts for each XCD left one with twice the mean).
+constexpr int BOTH = 3;
+template <typename T, Kind KIND, int B, int WQ, int WP, int PARTS>
 __global__ __launch_bounds__(64 * WQ * WP) void linear_experts_backward_kernel(LinArgs a, Plan plan) {
     extern __shared__ __align__(16) uint8_t smem[];
-    typedef LinTile<T, KIND, B, B, WQ, WP, TWO> Product;
+    typedef LinTile<T, KIND, B, B, WQ, WP, PARTS == 2> Product;
+    typedef LinTile<T, KIND, B, B, WQ, WP, true> Few;
     constexpr int SLAB = Slab<Product::TP>::BYTES;
+    constexpr Only FIRST = PARTS == BOTH ? MANY : ALL;
     const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), xcd = blockIdx.x & 7;
     float* const slab = reinterpret_cast<float*>(smem + Product::LDS + wv * SLAB);
-    uint16_t* order = reinterpret_cast<uint16_t*>(smem + Product::LDS + WQ * WP * SLAB);
+    uint16_t* const order = reinterpret_cast<uint16_t*>(smem + Product::LDS + WQ * WP * SLAB);
     int turn = 0;
     if (KIND == DW) {
-        const int many = sort_experts(a, Product::TH, reinterpret_cast<int*>(smem), order);
-        if (a.only == FEW) order += many;
-        plan.whole = (a.only == ALL ? a.experts : a.only == MANY ? many : a.experts - many) * plan.nq * plan.np;
-        const int run = max((plan.nq * plan.np + 7) >> 3, 1);
-        run_pieces<T, KIND, true, B, WQ, WP, TWO>(a, plan, Share{}, 0, (plan.whole + 8 * run - 1) / (8 * run) * run, run, turn, order, smem, slab);
+        const int many = sort_experts(a, Product::TH, reinterpret_cast<int*>(smem), order), each = plan.nq * plan.np;
+        const int run = max((each + 7) >> 3, 1);
+        auto count = [&](int tiles) { return (tiles + 8 * run - 1) / (8 * run) * run; };
+        if (PARTS == BOTH) plan.whole = many * each;
+        const int n = count(plan.whole);
+        run_pieces<T, KIND, true, B, WQ, WP, PARTS == 2, FIRST>(a, plan, Share{}, 0, n, run, turn, order, smem, slab);
+        if (PARTS == BOTH) {
+            plan.whole = (a.experts - many) * each;
+            run_pieces<T, KIND, true, B, WQ, WP, true, FEW>(a, plan, Share{}, n, count(plan.whole), run, turn, order + many, smem, slab);
+        }
     } else {
-        const Share mine = share_of(plan, tiles_total(a, Product::BQ_OUT) * plan.np, xcd);
-        run_pieces<T, KIND, true, B, WQ, WP, TWO>(a, plan, mine, 0, mine.whole, 1, turn, nullptr, smem, slab);
+        const Share mine = share_of(plan, tiles_total<FIRST>(a, Product::BQ_OUT) * plan.np, xcd);
+        run_pieces<T, KIND, true, B, WQ, WP, PARTS == 2, FIRST>(a, plan, mine, 0, mine.whole, 1, turn, nullptr, smem, slab);
+        if (PARTS == BOTH) {
+            const Share few = share_of(plan, tiles_total<FEW>(a, Few::BQ_OUT) * plan.np, xcd);
+            run_pieces<T, KIND, true, B, WQ, WP, true, FEW>(a, plan, few, mine.whole, few.whole, 1, turn, nullptr, smem, slab);
+        }
     }
 }
 
@@ -548,7 +563,7 @@ __global__ __launch_bounds__(64 * WQ * WP) void linear_join_kernel(LinArgs a, Pl
 #pragma unroll
         for (int i = 0; i < NI; ++i) v[i][0] += f[i * TH];
     }
-    const Tile t = locate<KIND, false, Product::BQ_OUT, BP, TWO>(a, plan.whole + r, plan.nq, plan.np, nullptr);
+    const Tile t = locate<KIND, false, Product::BQ_OUT, BP, TWO, ALL>(a, plan.whole + r, plan.nq, plan.np, nullptr);
     finish<T, KIND, ACT, Product::TP, NI, 1>(a, t, t.q0 + wq * Product::TQ_OUT + 16 * j, wp * Product::TP, v, slab[wv]);
 }
 
@@ -717,7 +732,7 @@ __global__ __launch_bounds__(64 * FEW_WAVES) void linear_few_kernel(LinArgs a, i
     const int n0 = blockIdx.x * 16, row_bytes = few_row(a.K) * 2, runs = row_bytes / 1024;
     Slice s{0, 0, a.m, 0};
     if (a.offsets != nullptr) {
-        if (!find_slice(a, room, 1, blockIdx.y, s)) return;
+        if (!find_slice<ALL>(a, room, 1, blockIdx.y, s)) return;
     } else {
         s.tile = blockIdx.y;
     }
@@ -1063,29 +1078,25 @@ hipError_t launch_backward_tiles(const LinArgs& a, const BackPlan& b, hipStream_
     if (e == hipSuccess) e = launch_join<T, DX, MOE_ACT_NONE, I, WQ, WP, TWO>(a, b.x, st);
     return e != hipSuccess || TWO ? e : launch_join<T, DW, MOE_ACT_NONE, I, WQ, WP>(a, b.w, st);   // (TWO: a step or two along k)
 }
-template <typename T, Kind KIND, int I, int WQ, int WP, bool TWO>
+template <typename T, Kind KIND, int I, int WQ, int WP, int PARTS>
 hipError_t launch_experts_tiles(const LinArgs& a, const Plan& plan, hipStream_t st) {
     constexpr Shape S = SHAPES[I];
-    typedef LinTile<T, KIND, S.bq, S.bp, WQ, WP, TWO> P;
+    typedef LinTile<T, KIND, S.bq, S.bp, WQ, WP> P;
     const size_t lds = P::LDS + WQ * WP * Slab<P::TP>::BYTES + (KIND == DW ? (size_t)a.experts * 2 : 0);
-    return launch_kernel(linear_experts_backward_kernel<T, KIND, S.bq, WQ, WP, TWO>, dim3(grid_of(pieces_of(plan), S.slots)), dim3(P::TH), lds, st, a, plan);
+    return launch_kernel(linear_experts_backward_kernel<T, KIND, S.bq, WQ, WP, PARTS>, dim3(grid_of(pieces_of(plan), S.slots)), dim3(P::TH), lds, st, a, plan);
 }
-template <typename T, Kind KIND, bool TWO>
-hipError_t launch_experts_of(LinArgs a, Only only, hipStream_t st) {
-    a.only = only;
-    const BackPlan b = plan_backward(a.m, a.N, a.K, a.experts, true, TWO, KIND == DX, KIND == DW);
+template <typename T, Kind KIND, int PARTS>
+hipError_t launch_experts_of(const LinArgs& a, hipStream_t st) {
+    const BackPlan b = plan_backward(a.m, a.N, a.K, a.experts, true, PARTS == 2, KIND == DX, KIND == DW);
     const Plan& plan = KIND == DX ? b.x : b.w;
-    if constexpr (!(TWO && KIND == DX))
-        if (b.shape == 0) return launch_experts_tiles<T, KIND, 0, 2, 4, TWO>(a, plan, st);
-    return launch_experts_tiles<T, KIND, 1, 2, 2, TWO>(a, plan, st);
+    if constexpr (!(KIND == DX && PARTS == 2))
+        if (b.shape == 0) return launch_experts_tiles<T, KIND, 0, 2, 4, PARTS>(a, plan, st);
+    return launch_experts_tiles<T, KIND, 1, 2, 2, PARTS>(a, plan, st);
 }
-// the experts with dz in two parts, and the others
 template <typename T, Kind KIND>
 hipError_t launch_experts(const LinArgs& a, hipStream_t st) {
-    if (a.dz_rest == nullptr) return launch_experts_of<T, KIND, false>(a, ALL, st);
-    if (all_two(a.m, a.experts)) return launch_experts_of<T, KIND, true>(a, ALL, st);
-    const hipError_t e = launch_experts_of<T, KIND, true>(a, FEW, st);
-    return e == hipSuccess ? launch_experts_of<T, KIND, false>(a, MANY, st) : e;
+    if (a.dz_rest == nullptr) return launch_experts_of<T, KIND, 1>(a, st);
+    return all_two(a.m, a.experts) ? launch_experts_of<T, KIND, 2>(a, st) : launch_experts_of<T, KIND, BOTH>(a, st);
 }
 template <typename T>
 hipError_t launch_backward(const LinArgs& a, float* partial_x, float* partial_w, hipStream_t st) {
