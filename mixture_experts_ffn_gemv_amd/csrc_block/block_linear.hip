@@ -754,6 +754,7 @@ __global__ __launch_bounds__(64 * FEW_WAVES) void linear_few_kernel(LinArgs a, i
         const int row = r / runs, k = (r - row * runs) * 512 + (lane ^ (row & 15)) * 8;
         buffer_load_lds16(X, smem + r * 1024, k < a.K ? (uint32_t)(row * a.ldx + k) * 2 : PAST);
     }
+    __atomic_signal_fence(__ATOMIC_SEQ_CST);   // (x is requested before any weight: the wait below counts back from the last)
     uint4 wq[AHEAD];
     auto request = [&](int i, int c) { wq[i] = *reinterpret_cast<const uint4*>(w + min(32 * min(c, chunks - 1) + 8 * g, a.K - 8)); };
 #pragma unroll
