@@ -628,8 +628,10 @@ def _picks(t, where):
     shape = t.shape
     if t.dtype is not torch.int32 or len(shape) != 2 or not t.is_cuda or not t.is_contiguous():
         raise MoeError(MOE_EINVAL, where)
-    _small(where, *shape)
-    return t.data_ptr(), shape[0], shape[1]
+    m, topk = shape
+    if m > _MOST or topk > _MOST:
+        raise MoeError(MOE_EINVAL, where)
+    return t.data_ptr(), m, topk
 
 
 def moe_sort_workspace(m, topk, n_experts):
@@ -645,7 +647,8 @@ def moe_sort(idx, n_experts, row_of, pick_of, offsets, work, stream=None):
     offsets [n_experts + 1], all int32."""
     me = "moe_sort"
     picks, m, topk = _picks(idx, me)
-    _small(me, n_experts)
+    if n_experts > _MOST:
+        raise MoeError(MOE_EINVAL, me)
     return _check(lib().moe_sort(
         picks, m, topk, n_experts, _whole(row_of, (m, topk), torch.int32, me), _whole(pick_of, (m * topk,), torch.int32, me),
         _whole(offsets, (n_experts + 1,), torch.int32, me), *_bytes(work, me),
