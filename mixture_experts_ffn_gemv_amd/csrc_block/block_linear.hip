@@ -20,8 +20,8 @@
 // What bounds it: with few rows the weights' bytes (one row of 2304 x 5120 bf16: 8.0 us a call, 23.6 MB; six experts of
 // 5120 x 2304, one row each: 29 us, 4.9 TB/s; 64 experts of 2048 x 1408 f16, 47 rows each: 86 to 92 us, 390 MB); with many
 // the matrix cores (8192 rows of 5120 x 2304 bf16: forward 190 us and the join of its last tiles 11, together 0.96 PFLOP/s;
-// dz 28 us; dx and dW 387 us, 1.0 PFLOP/s; 16184 rows of 32 experts of 2048 x 1408: forward 138 to 151 us, dx 146, dW 155,
-// 93 GFLOP each). A tile's K step of 256 x 256 takes 1.45 us forward, 1.65 in dx and 1.75 in dW; the rest are the ends of
+// dz 29 us; dx and dW 384 us, 1.0 PFLOP/s; 16184 rows of 32 experts of 2048 x 1408: forward 138 to 151 us, dx 145, dW 157,
+// 93 GFLOP each; kernels in a profiled run, whose sum is 4% above the calls'). A tile's K step of 256 x 256 takes 1.45 us forward, 1.65 in dx and 1.75 in dW; the rest are the ends of
 // tiles, where z, y and the residual pass through all CUs at once, and rounds that are not full.
 #include <cmath>
 
@@ -118,7 +118,9 @@ MOE_DEV int tiles_total(const LinArgs& a, int rows) {
 template <Only ONLY>
 MOE_DEV bool find_slice(const LinArgs& a, int rows, int np, int tile, Slice& s) {
     const int lane = threadIdx.x & 63;
-    constexpr int U = 4;   // 256 experts' offsets are requested at a time
+    // 256 experts at a time, but one load after another: the second of an expert's two is behind a branch, before which the
+    // compiler waits for the first (eight trips to the L2 for up to 256 experts, sixteen for 384)
+    constexpr int U = 4;
     s = {0, 0, 0, 0};
     int before = 0;   // tiles of the experts before these
     for (int e0 = 0; e0 < a.experts; e0 += 64 * U) {
@@ -407,7 +409,9 @@ MOE_DEV void store_sums(const Plan& plan, const Piece& x, const f32x4 (&acc)[NI]
 
 // Both kernels: a workgroup takes one piece after another. The loads of the next piece's first two steps are under
 // way while it finishes the one before. The pointers into LDS are a lambda's own restricted ones there, so that the
-// compiler does not wait for these loads before it reads the slab. GROUPED: with offsets.
+// compiler does not wait for these loads before it reads the slab. In dx and dW it waits nowhere in a tile's end; forward it
+// does, once or twice in each of the sixteen passes from the third on: the branches of load8 and store8 for a row's tail keep
+// it from counting what is under way, in whole tiles too. GROUPED: with offsets.
 template <typename T, bool GROUPED, int ACT, int BQ, int BP, int WQ, int WP>
 __global__ __launch_bounds__(64 * WQ * WP) void linear_forward_kernel(LinArgs a, Plan plan) {
     extern __shared__ __align__(16) uint8_t smem[];
@@ -1169,7 +1173,8 @@ LinArgs describe(const moe_linear* f, int m, const int32_t* offsets) {
 // Whether m rows take the kernel for few rows; `room`: rows of x that a workgroup of it has LDS for, all of them or with
 // offsets twice the average (more of one expert read its weights again, from the L2). x has to fit whole, and with offsets
 // it is for so few experts that tiles of 32 rows leave CUs idle; with short k, of which each wavefront has but a load or two,
-// for fewer. That kernel and those tiles, weights from memory, K x N:
+// for fewer (the bounds, a quarter of K's values up to 200 or 256 tiles, are fitted to these figures). That kernel and those
+// tiles, weights from memory, K x N:
 //   4096 x 4096          1 row 9.9 and 15.7 us, 8 rows 10.4 and 15.5, 16 rows (not whole) 15.2 and 15.5
 //   8192 x 1024          1 row 11.2 and 14.5 us, 16 rows (not whole) 19.1 and 14.4
 //   2048 x 65536         1 row 55.6 and 64.4 us, 16 rows 63.9 and 64.9

@@ -12,7 +12,7 @@
 //
 // Memory bounds the moves: 8192 tokens of 5120 bf16 with six picks each are brought to their rows in 103 us (587 MB, 5.7
 // TB/s), summed in 102 to 118 (587 MB), and the sums' gradients made in 220 to 242 (1.09 GB, 4.5 to 5.0 TB/s); their 49152
-// picks are sorted in 10.5. For one token each of the three is a launch of 3 us.
+// picks are sorted in 8.2 (10.4 between a step's other kernels). For one token each of the three is a launch of 3 us.
 #include "block_rows.h"
 
 namespace moe {
@@ -24,8 +24,10 @@ constexpr int MAX_PICKS = 1 << 26;
 // ------------------------------------------------------------------ sort
 
 constexpr int STEP = 1024;      // picks per step of a workgroup, a lane each
-// As many steps or fewer are sorted by one launch, in which every workgroup counts all the picks: 8192 picks 5.9 us and in
-// two launches 8.8, 24576 6.1 to 7.8 and 9.2 to 10.9, 49152 8.3 to 9.4 and 10.8 to 11.1, 65536 9.6 and 9.0
+// As many steps or fewer are sorted by one launch, in which every workgroup counts all the picks. One launch and two, calls one
+// after another: picks of 384 experts, 8190 5.6 and 8.3 us, 24576 6.1 and 8.5, 40962 7.5 and 8.6, 49152 8.2 and 8.6, 57342 8.9
+// and 9.1, 65538 9.5 and 8.8; of 1024, 49152 8.4 and 11.1; of eight, whose counts more lanes add to at a time, 32768 9.1 and
+// 8.4, 49152 13.1 and 8.5. So the bound is where many experts gain little more, and with a few experts it comes late.
 constexpr int WHOLE_STEPS = 48;
 constexpr int MAX_BLOCKS = 256;
 
@@ -198,7 +200,8 @@ __global__ __launch_bounds__(256) void dispatch_kernel(MoveArgs a) {
     }
 }
 
-// out[t] = sum over j of w[t, j] e[row_of[t, j]] (WEIGHTED; else w = 1), `J` rows requested at a time
+// out[t] = sum over j of w[t, j] e[row_of[t, j]] (WEIGHTED; else w = 1), `J` rows at a time: none is added before the last is
+// requested. (Each row's number is waited for, and with it the row before: within a wavefront they come one after another.)
 template <typename T, Tail TAIL, bool WEIGHTED, bool ONCE, int J>
 __global__ __launch_bounds__(256) void combine_kernel(MoveArgs a) {
     constexpr int V = Raw<T>::V;
@@ -336,7 +339,7 @@ hipError_t launch_combine_j(const MoveArgs& a, hipStream_t st) {
     return launch_walk(tail == SHORT ? combine_kernel<T, SHORT, WEIGHTED, false, J>
                        : tail == WHOLE ? combine_kernel<T, WHOLE, WEIGHTED, ONCE, J> : combine_kernel<T, SHIFTED, WEIGHTED, ONCE, J>, a, V, ONCE, st);
 }
-// As many of a token's rows are requested at a time as it has, up to eight, and a request for a row that it does not have costs
+// As many of a token's rows are taken at a time as it has, up to eight, and a request for a row that it does not have costs
 // as much as one for another: sums of two rows of 8192 x 5120 bf16 42 us so and 63 with eight at a time, of six 101 and
 // 106; the gradients of six rows of 1999 44.6 and 45.9.
 template <typename T, bool WEIGHTED, bool ONCE>
