@@ -530,7 +530,8 @@ int moe_combine_forward(int32_t dtype, int32_t dim, const void* e, int64_t lde, 
                         const int32_t* row_of, int32_t m, int32_t topk, void* y, int64_t ldy, void* stream);
 
 /* Its gradients: de[row_of[t, j]] = weights[t, j] dy[t] (rows that no pick has are left as they are) and
- * dweights[t, j] = dy[t] . e[row_of[t, j]] (f32 [m, topk]; 0 for a pick without a row). Either may be NULL. */
+ * dweights[t, j] = dy[t] . e[row_of[t, j]] (f32 [m, topk]; 0 for a pick without a row). Either may be NULL; e is needed
+ * for both. */
 int moe_combine_backward(int32_t dtype, int32_t dim, const void* dy, int64_t lddy, const void* e, int64_t lde,
                          int32_t rows, const float* weights, const int32_t* row_of, int32_t m, int32_t topk, void* de,
                          int64_t ldde, float* dweights, void* stream);
