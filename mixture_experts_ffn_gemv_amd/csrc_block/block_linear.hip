@@ -21,8 +21,9 @@
 // 5120 x 2304, one row each: 29 us, 4.9 TB/s; 64 experts of 2048 x 1408 f16, 47 rows each: 86 to 92 us, 390 MB); with many
 // the matrix cores (8192 rows of 5120 x 2304 bf16: forward 190 us and the join of its last tiles 11, together 0.96 PFLOP/s;
 // dz 29 us; dx and dW 384 us, 1.0 PFLOP/s; 16184 rows of 32 experts of 2048 x 1408: forward 138 to 151 us, dx 145, dW 157,
-// 93 GFLOP each; kernels in a profiled run, whose sum is 4% above the calls'). A tile's K step of 256 x 256 takes 1.45 us forward, 1.65 in dx and 1.75 in dW; the rest are the ends of
-// tiles, where z, y and the residual pass through all CUs at once, and rounds that are not full.
+// 93 GFLOP each; kernels in a profiled run, whose sum is 4% above the calls'). A tile's K step of 256 x 256 takes 1.45 us
+// forward, 1.65 in dx and 1.75 in dW; the rest are the ends of tiles, where z, y and the residual pass through all CUs at
+// once, and rounds that are not full.
 #include <cmath>
 
 #include "block_rows.h"
@@ -322,11 +323,12 @@ MOE_DEV int sort_experts(const LinArgs& a, int threads, int* counts, uint16_t* o
         if (threadIdx.x < a.experts) order[before] = (uint16_t)lane;
         many = __popcll(__ballot(mine > TWO_PARTS));
     } else {
-        for (int e0 = 0; e0 < a.experts; e0 += 64) many += __popcll(__ballot(e0 + lane < a.experts && counts[min(e0 + lane, a.experts - 1)] > TWO_PARTS));
+        auto has_many = [&](int e) { return e < a.experts && counts[min(e, a.experts - 1)] > TWO_PARTS; };
+        for (int e0 = 0; e0 < a.experts; e0 += 64) many += __popcll(__ballot(has_many(e0 + lane)));
         int more = 0;   // experts before these with more than TWO_PARTS
         for (int e0 = 0; e0 < a.experts; e0 += 64) {
             const int e = e0 + lane;
-            const bool on = e < a.experts && counts[min(e, a.experts - 1)] > TWO_PARTS;
+            const bool on = has_many(e);
             const uint64_t all = __ballot(on);
             const int of = __popcll(all & ((1ull << lane) - 1));
             if (e < a.experts && threadIdx.x < 64) order[on ? more + of : many + (e0 - more) + (lane - of)] = (uint16_t)e;
